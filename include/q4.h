@@ -278,6 +278,91 @@ q4_status q8_linear_w8a32(const float *x, const int8_t *wq, const float *sw, flo
 q4_status q8_linear_w8a16(const uint16_t *x_bf16, const int8_t *wq, const float *sw, uint16_t *y_bf16,
                           float *y_f32, int64_t M, int64_t N, int64_t K, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MX FP4; OCP Microscaling Formats,
+ * E2M1 elements under E8M0 scales).
+ *
+ * Layout: a row of K numbers is cut into B = ceil(K/32) blocks of 32 columns
+ * (the last one may be short).  A block is 16 bytes of codes, column 2b in
+ * bits 0-3 of byte b and 2b+1 in bits 4-7, and one scale byte.  Codes: bit 3
+ * is the sign, bits 0-2 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6.  A scale byte s
+ * stands for 2^(s - 127); 255 is NaN.  Codes past column K of a row's last
+ * block are 0.  Arrays: codes uint8 [rows, 16 B], 16-byte aligned (EINVAL
+ * otherwise); scales uint8 [rows, B].
+ * ---------------------------------------------------------------------- */
+
+/* Quantize rows.  x: [M, K] f32 or bf16 (xt).  Per block, with t = max|x|:
+ * the scale byte is max(floor(log2 t) - 2, -127) + 127 (0 for t = 0), and a
+ * code is x divided by the scale, rounded to the nearest code, ties to even,
+ * magnitudes beyond 6 to 6.  A block with a NaN or an infinity gets scale
+ * 255 and codes 0, so that it decodes to NaN.  EINVAL for codes or scales
+ * overlapping x or each other. */
+q4_status q4_mx_quantize_rows(const void *x, q4_dtype xt, int64_t M, int64_t K, uint8_t *codes,
+                              uint8_t *scales, void *stream);
+
+/* The numbers that rows stand for, as f32 or bf16 (yt): y [M, K].  Exact in
+ * both types (an f32 overflow, possible with scales above 252, gives
+ * infinity). */
+q4_status q4_mx_dequantize_rows(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K,
+                                void *y, q4_dtype yt, void *stream);
+
+/* y = x W^T with both operands in MX FP4, summed in f32 and rounded once to
+ * f32 or bf16 (yt).  xq, sx: M rows, wq, sw: N rows, of K columns each;
+ * y: [M, N].  A scale of 255 makes its whole row or column of y NaN.  K == 0
+ * sets y to 0. */
+q4_status q4_linear_w4a4_mx(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw,
+                            void *y, q4_dtype yt, int64_t M, int64_t N, int64_t K, void *stream);
+
+/* Bytes of device workspace q4_linear_w4a4_mx_dynamic needs for M rows of K:
+ * room for their codes and their scales, each 256-byte aligned. */
+size_t q4_w4a4_mx_dynamic_workspace(int64_t M, int64_t K);
+
+/* q4_mx_quantize_rows of x [M, K] (f32 or bf16, xt) into the caller's
+ * workspace ws (device memory, 256-byte aligned, at least
+ * q4_w4a4_mx_dynamic_workspace(M, K) bytes), then q4_linear_w4a4_mx.  Up to
+ * 16 rows the codes are formed inside the product instead (the same codes)
+ * and ws is left untouched; its contents after any call are unspecified.
+ * EINVAL for a small or misaligned workspace or one overlapping another
+ * buffer. */
+q4_status q4_linear_w4a4_mx_dynamic(const void *x, q4_dtype xt, const uint8_t *wq, const uint8_t *sw,
+                                    void *y, q4_dtype yt, int64_t M, int64_t N, int64_t K, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+/* y = x W^T with bf16 x [M, K] and MX FP4 weights, summed in f32 and rounded
+ * once to f32 or bf16 (yt).  The weights are exact in bf16, so the matrix
+ * products see them unrounded.  Any K >= 0. */
+q4_status q4_linear_w4a16_mx(const uint16_t *x_bf16, const uint8_t *wq, const uint8_t *sw, void *y,
+                             q4_dtype yt, int64_t M, int64_t N, int64_t K, void *stream);
+
+/* Pairs that q4_qk_norm_rope rotates. */
+typedef enum {
+  Q4_ROPE_HALVES = 0,     /* column i with column i + R/2 */
+  Q4_ROPE_NEIGHBOURS = 1  /* column 2i with column 2i + 1 */
+} q4_rope_pairs;
+
+/* Queries and keys of a decoder layer, in one pass: each head's row of D
+ * numbers becomes x / sqrt(mean(x^2) + eps) * gain, and its first R columns
+ * are rotated by its token's angles, (a, b) -> (a cos - b sin, b cos + a sin).
+ * Computed in f32, rounded once.
+ *   q, k: T tokens of Hq and Hk heads, f32 or bf16 (xt); a token's heads are
+ *     q_token (k_token) elements from the next token's and a head's row is
+ *     q_head (k_head) elements from the next head's, its D numbers side by
+ *     side: the outputs of the q and k linears, or slices of a fused one.
+ *   q_gain, k_gain: [D], f32 or bf16 (gt); NULL for a gain of 1.
+ *   positions: int64 [T]; cos_sin: f32 [P, R], row p holding R/2 cosines and
+ *     then R/2 sines of position p's angles.  A token whose position is not in
+ *     0 .. P - 1 gets NaN in its rotated columns.
+ *   q_out: [T, Hq, D], k_out: [T, Hk, D], contiguous, f32 or bf16 (yt).
+ * Hk == 0: no keys; k, k_gain and k_out may be NULL.
+ * EINVAL also for eps < 0 or NaN, a negative stride, or an output overlapping
+ * an input or the other output; ESHAPE for D odd or outside 2 .. 65536, R odd
+ * or outside 2 .. D, P < 1, or T * (Hq + Hk) beyond 2^31 - 1. */
+q4_status q4_qk_norm_rope(const void *q, int64_t q_token, int64_t q_head, const void *k, int64_t k_token,
+                          int64_t k_head, q4_dtype xt, const void *q_gain, const void *k_gain, q4_dtype gt,
+                          const int64_t *positions, const float *cos_sin, void *q_out, void *k_out,
+                          q4_dtype yt, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t P,
+                          float eps, q4_rope_pairs pairs, void *stream);
+
 /* Process-wide route override for A/B tests and benchmarks ([int8] "Tier
  * law": routes are chosen by measurement and can be forced).  A forced route
  * that cannot serve a shape falls back to the generic kernels.  EINVAL for

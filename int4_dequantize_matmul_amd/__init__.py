@@ -25,6 +25,7 @@ OK, EINVAL, ESHAPE, EDEVICE, EMISMATCH = 0, 1, 2, 3, 4
 ENC = {"twos": 0, "excess8": 1}
 DT = {"f32": 0, "bf16": 1}
 PATHS = {"auto": 0, "generic": 1, "gemv": 2, "tiled": 3, "gemv_mc": 4}
+ROPE_PAIRS = {"halves": 0, "neighbours": 1}
 PATH_NAMES = {v: k for k, v in PATHS.items()}
 OPS = {"w4a32": 0, "w4a16": 1, "w4a16_zp": 2, "w4a8": 3, "w4a8_zp": 4, "w8a8": 5}
 W4A8_MAX_K = 1048576
@@ -68,6 +69,15 @@ _SIG = {
     "q4_selftest_workspace": (ctypes.c_size_t, []),
     "q4_selftest": (ctypes.c_int, [_P, ctypes.c_size_t, _P]),
     "q4_selftest_report": (ctypes.c_char_p, []),
+    "q4_mx_quantize_rows": (ctypes.c_int, [_P, ctypes.c_int, _I, _I, _P, _P, _P]),
+    "q4_mx_dequantize_rows": (ctypes.c_int, [_P, _P, _I, _I, _P, ctypes.c_int, _P]),
+    "q4_linear_w4a4_mx": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int, _I, _I, _I, _P]),
+    "q4_w4a4_mx_dynamic_workspace": (ctypes.c_size_t, [_I, _I]),
+    "q4_linear_w4a4_mx_dynamic": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, ctypes.c_int, _I, _I, _I, _P,
+                                                 ctypes.c_size_t, _P]),
+    "q4_linear_w4a16_mx": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _I, _I, _I, _P]),
+    "q4_qk_norm_rope": (ctypes.c_int, [_P, _I, _I, _P, _I, _I, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P,
+                                       ctypes.c_int, _I, _I, _I, _I, _I, _I, ctypes.c_float, ctypes.c_int, _P]),
     "q4_set_path": (ctypes.c_int, [ctypes.c_int]),
     "q4_get_path": (ctypes.c_int, []),
     "q4_last_path": (ctypes.c_int, []),
@@ -417,6 +427,188 @@ def q8_linear_w8a8(xq, sx, wq, sw, y=None):
     _check("q8_linear_w8a8", _lib().q8_linear_w8a8(_ptr(xq), _ptr(sx), _ptr(wq), _ptr(sw), _ptr(y),
                                                     M, N, K, _stream(xq)))
     return y
+
+
+# ---------------------------------------------------------------------------
+# MX FP4: codes uint8 [rows, 16 ceil(K/32)] and scales uint8 [rows, ceil(K/32)]
+# ---------------------------------------------------------------------------
+
+_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _dt(t: torch.Tensor) -> int:
+    return 1 if t.dtype == torch.bfloat16 else 0
+
+
+def _mx(codes, scales, name: str) -> int:
+    """Checks a pair of MX FP4 arrays; returns their blocks per row."""
+    _dev(codes, name, (torch.uint8,), 2)
+    _dev(scales, f"{name}'s scales", (torch.uint8,), 2)
+    rows, blocks = scales.shape
+    if codes.shape[0] != rows or codes.shape[1] != 16 * blocks:
+        raise ValueError(f"{name} has shape {tuple(codes.shape)}, expected {(rows, 16 * blocks)} for scales of "
+                         f"shape {(rows, blocks)}")
+    if codes.device != scales.device:
+        raise ValueError(f"{name} and its scales are on different devices")
+    return blocks
+
+
+def _same_device(*tensors):
+    for t in tensors[1:]:
+        if t.device != tensors[0].device:
+            raise ValueError(f"tensors on different devices: {tensors[0].device} and {t.device}")
+
+
+def _out(y, M: int, N: int, dtype: str, like: torch.Tensor):
+    """The output tensor: y if given (checked), else a new one."""
+    if y is None:
+        return torch.empty((M, N), dtype=_DTYPES[dtype], device=like.device)
+    _dev(y, "y", (_DTYPES[dtype],), 2)
+    if y.shape != (M, N):
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected {(M, N)}")
+    _same_device(like, y)
+    return y
+
+
+def q4_mx_quantize_rows(x: torch.Tensor):
+    """f32 or bf16 rows [M, K] -> (codes uint8 [M, 16 ceil(K/32)], scales uint8 [M, ceil(K/32)])."""
+    _dev(x, "x", _FLOATS, 2)
+    M, K = x.shape
+    B = (K + 31) // 32
+    codes = torch.empty((M, 16 * B), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((M, B), dtype=torch.uint8, device=x.device)
+    if M and K:
+        _check("q4_mx_quantize_rows", _lib().q4_mx_quantize_rows(_ptr(x), _dt(x), M, K, _ptr(codes), _ptr(scales),
+                                                                 _stream(x)))
+    return codes, scales
+
+
+def q4_mx_dequantize_rows(codes, scales, K: int | None = None, dtype: str = "f32", y=None):
+    """Codes and scales -> the numbers they stand for, [M, K] (K: 32 a block if not given)."""
+    B = _mx(codes, scales, "codes")
+    M = codes.shape[0]
+    K = 32 * B if K is None else K
+    if (K + 31) // 32 != B:
+        raise ValueError(f"K = {K} has {(K + 31) // 32} blocks, the scales have {B}")
+    y = _out(y, M, K, dtype, codes)
+    if M and K:
+        _check("q4_mx_dequantize_rows", _lib().q4_mx_dequantize_rows(_ptr(codes), _ptr(scales), M, K, _ptr(y),
+                                                                     DT[dtype], _stream(codes)))
+    return y
+
+
+def q4_linear_w4a4_mx(xq, sx, wq, sw, dtype: str = "bf16", y=None):
+    """MX FP4 rows xq, sx [M, ...] times MX FP4 weights wq, sw [N, ...] -> y [M, N] in dtype."""
+    B = _mx(xq, sx, "xq")
+    if _mx(wq, sw, "wq") != B:
+        raise ValueError(f"xq has {B} blocks a row, wq {sw.shape[1]}")
+    _same_device(xq, wq)
+    M, N = xq.shape[0], wq.shape[0]
+    y = _out(y, M, N, dtype, xq)
+    if M and N:
+        _check("q4_linear_w4a4_mx", _lib().q4_linear_w4a4_mx(_ptr(xq), _ptr(sx), _ptr(wq), _ptr(sw), _ptr(y),
+                                                             DT[dtype], M, N, 32 * B, _stream(xq)))
+    return y
+
+
+def q4_w4a4_mx_dynamic_workspace(M: int, K: int) -> int:
+    return int(_lib().q4_w4a4_mx_dynamic_workspace(M, K))
+
+
+def _mx_weights(x, wq, sw):
+    K = x.shape[1]
+    if _mx(wq, sw, "wq") != (K + 31) // 32:
+        raise ValueError(f"x has {K} columns, wq {sw.shape[1]} blocks of 32 a row")
+    _same_device(x, wq)
+    return x.shape[0], wq.shape[0], K
+
+
+def q4_linear_w4a4_mx_dynamic(x, wq, sw, dtype: str = "bf16", ws=None, y=None):
+    """f32 or bf16 x [M, K], quantized in the call, times MX FP4 weights -> y [M, N] in dtype."""
+    _dev(x, "x", _FLOATS, 2)
+    M, N, K = _mx_weights(x, wq, sw)
+    y = _out(y, M, N, dtype, x)
+    if M and N:
+        if ws is None:
+            ws = torch.empty(q4_w4a4_mx_dynamic_workspace(M, K), dtype=torch.uint8, device=x.device)
+        _check("q4_linear_w4a4_mx_dynamic",
+               _lib().q4_linear_w4a4_mx_dynamic(_ptr(x), _dt(x), _ptr(wq), _ptr(sw), _ptr(y), DT[dtype], M, N, K,
+                                                _ptr(ws), ws.numel() * ws.element_size(), _stream(x)))
+    return y
+
+
+def q4_linear_w4a16_mx(x, wq, sw, dtype: str = "bf16", y=None):
+    """bf16 x [M, K] times MX FP4 weights -> y [M, N] in dtype."""
+    _dev(x, "x", (torch.bfloat16,), 2)
+    M, N, K = _mx_weights(x, wq, sw)
+    y = _out(y, M, N, dtype, x)
+    if M and N:
+        _check("q4_linear_w4a16_mx", _lib().q4_linear_w4a16_mx(_ptr(x), _ptr(wq), _ptr(sw), _ptr(y), DT[dtype],
+                                                               M, N, K, _stream(x)))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# queries and keys
+# ---------------------------------------------------------------------------
+
+def _heads(t, name: str, T, D):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in _FLOATS:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_FLOATS}")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [tokens, heads, D] with the D numbers of a head side by side")
+    if t.shape[0] != T or t.shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({T}, heads, {D})")
+
+
+def q4_qk_norm_rope(q, k, q_gain, k_gain, positions, cos_sin, eps: float = 1e-6, pairs: str = "halves",
+                    dtype: str | None = None):
+    """Norm of each query and key head (times its gain) with the rotation of
+    its first R columns.  q [T, Hq, D], k [T, Hk, D] or None: f32 or bf16,
+    slices of a fused projection as they are; gains [D] or None; positions
+    int64 [T]; cos_sin f32 [P, R] -> (q_out, k_out or None) in dtype (default:
+    q's)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [tokens, heads, D]")
+    T, Hq, D = q.shape
+    _heads(q, "q", T, D)
+    _dev(positions, "positions", (torch.int64,), 1)
+    _dev(cos_sin, "cos_sin", (torch.float32,), 2)
+    if positions.shape[0] != T:
+        raise ValueError(f"positions has {positions.shape[0]} entries for {T} tokens")
+    _same_device(q, positions, cos_sin)
+    Hk = 0
+    if k is not None:
+        _heads(k, "k", T, D)
+        if k.dtype != q.dtype:
+            raise TypeError(f"q and k differ in dtype: {q.dtype} and {k.dtype}")
+        _same_device(q, k)
+        Hk = k.shape[1]
+    gt = None
+    for g, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+        if g is not None:
+            _dev(g, name, _FLOATS, 1)
+            _same_device(q, g)
+            if g.shape[0] != D:
+                raise ValueError(f"{name} has {g.shape[0]} entries for heads of {D}")
+            if gt is not None and gt != g.dtype:
+                raise TypeError("q_gain and k_gain differ in dtype")
+            gt = g.dtype
+    out = q.dtype if dtype is None else _DTYPES[dtype]
+    qo = torch.empty((T, Hq, D), dtype=out, device=q.device)
+    ko = None if k is None else torch.empty((T, Hk, D), dtype=out, device=q.device)
+    if T == 0 or Hq + Hk == 0:
+        return qo, ko
+    k_token, k_head = (k.stride(0), k.stride(1)) if Hk else (0, 0)
+    _check("q4_qk_norm_rope",
+           _lib().q4_qk_norm_rope(_ptr(q), q.stride(0), q.stride(1), _ptr(k), k_token, k_head, _dt(q), _ptr(q_gain),
+                                  _ptr(k_gain), 1 if gt == torch.bfloat16 else 0, _ptr(positions), _ptr(cos_sin),
+                                  _ptr(qo), _ptr(ko), 1 if out == torch.bfloat16 else 0, T, Hq, Hk, D,
+                                  cos_sin.shape[1], cos_sin.shape[0], eps, ROPE_PAIRS[pairs], _stream(q)))
+    return qo, ko
 
 
 def q4_selftest(device="cuda:0") -> str:

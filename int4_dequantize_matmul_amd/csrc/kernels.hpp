@@ -116,4 +116,34 @@ hipError_t launch_tiled_w4a16(const uint16_t *x, const uint8_t *wq, const uint16
                               uint16_t *yb, int64_t M, int64_t N, int64_t K, int64_t G, int enc,
                               hipStream_t st, const uint8_t *zp = nullptr);
 
+// MX FP4 (blocks of 32 E2M1 codes under one E8M0 byte).  packed and wq, xq
+// are 16-byte aligned, rows of 16 ceil(K/32) bytes; scales rows of ceil(K/32).
+hipError_t launch_mx_quantize(const void *x, bool x_bf16, int64_t M, int64_t K, uint8_t *packed, uint8_t *scales,
+                              hipStream_t st);
+hipError_t launch_mx_dequantize(const uint8_t *packed, const uint8_t *scales, int64_t M, int64_t K, void *y,
+                                bool y_bf16, hipStream_t st);
+// Products by blocks of 16 weight rows; any M up to 16 * 65535, K > 0.  The
+// fused form quantizes f32 or bf16 rows itself.
+hipError_t launch_mx_gemv_w4a4(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, void *y,
+                               bool y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t st);
+hipError_t launch_mx_gemv_w4a4_fused(const void *x, bool x_bf16, const uint8_t *wq, const uint8_t *sw, void *y,
+                                     bool y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t st);
+hipError_t launch_mx_gemv_w4a16(const uint16_t *x, const uint8_t *wq, const uint8_t *sw, void *y, bool y_bf16,
+                                int64_t M, int64_t N, int64_t K, hipStream_t st);
+
+// Norm of each query and key head with the rotation of its first R columns.
+// Strides in elements; wq, wk (gains) and the keys may be null (then Hk == 0).
+struct QkArgs {
+  const void *q, *k;
+  int64_t q_t, q_h, k_t, k_h;   // strides of a token and of a head
+  const void *wq, *wk;
+  bool w_bf16;
+  const int64_t *pos;           // [T]
+  const float *table;           // [P, R]: R/2 cosines, then R/2 sines
+  void *qo, *ko;                // [T, Hq, D], [T, Hk, D]
+  int64_t T, Hq, Hk, D, R, P;
+  float eps;
+};
+hipError_t launch_qk_norm_rope(const QkArgs &a, bool in_bf16, bool out_bf16, bool neighbours, hipStream_t st);
+
 }  // namespace q4

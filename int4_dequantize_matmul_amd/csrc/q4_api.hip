@@ -650,3 +650,160 @@ extern "C" q4_status q8_linear_w8a8(const int8_t *xq, const float *sx, const int
   if (p == Q4_PATH_GEMV) return finish(q4::launch_gemv_w8a8(xq, sx, wq, sw, y, M, N, K, st), p);
   return finish(q4::launch_generic_int(xq, sx, wq, true, sw, y, M, N, K, 0, Q4_ENC_EXCESS8, st), p);
 }
+
+// ---- MX FP4 ---------------------------------------------------------------
+
+namespace {
+
+uint64_t mx_blocks(int64_t K) { return (u(K) + 31) / 32; }
+uint64_t mx_codes(int64_t rows, int64_t K) { return u(rows) * mx_blocks(K) * 16; }
+uint64_t mx_scales(int64_t rows, int64_t K) { return u(rows) * mx_blocks(K); }
+uint64_t size_of(int dt) { return dt == Q4_DT_BF16 ? 2 : 4; }
+bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+// Up to this many rows the dynamic call forms the activations' codes inside
+// the product.
+constexpr int64_t kMxFusedMaxM = 16;
+
+q4_status w4a4_mx_launch(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, void *y,
+                         int yt, int64_t M, int64_t N, int64_t K, hipStream_t st) {
+  return finish(q4::launch_mx_gemv_w4a4(xq, sx, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_GEMV);
+}
+
+}  // namespace
+
+extern "C" q4_status q4_mx_quantize_rows(const void *x, q4_dtype xt_arg, int64_t M, int64_t K, uint8_t *codes,
+                                         uint8_t *scales, void *stream) {
+  const int xt = enum_bits(xt_arg);
+  if (!x || !codes || !scales || M < 0 || K < 0 || bad_dt(xt) || misaligned(codes, 16)) return Q4_EINVAL;
+  if (M > kMaxNK || K > kMaxNK) return Q4_ESHAPE;
+  if (any_overlap({{codes, mx_codes(M, K)}, {scales, mx_scales(M, K)}}, {{x, u(M) * u(K) * size_of(xt)}}))
+    return Q4_EINVAL;
+  if (M == 0 || K == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  return finish(q4::launch_mx_quantize(x, xt == Q4_DT_BF16, M, K, codes, scales, S(stream)), Q4_PATH_GEMV);
+}
+
+extern "C" q4_status q4_mx_dequantize_rows(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K,
+                                           void *y, q4_dtype yt_arg, void *stream) {
+  const int yt = enum_bits(yt_arg);
+  if (!codes || !scales || !y || M < 0 || K < 0 || bad_dt(yt) || misaligned(codes, 16)) return Q4_EINVAL;
+  if (M > kMaxNK || K > kMaxNK) return Q4_ESHAPE;
+  if (any_overlap({{y, u(M) * u(K) * size_of(yt)}}, {{codes, mx_codes(M, K)}, {scales, mx_scales(M, K)}}))
+    return Q4_EINVAL;
+  if (M == 0 || K == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  return finish(q4::launch_mx_dequantize(codes, scales, M, K, y, yt == Q4_DT_BF16, S(stream)), Q4_PATH_GEMV);
+}
+
+extern "C" q4_status q4_linear_w4a4_mx(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw,
+                                       void *y, q4_dtype yt_arg, int64_t M, int64_t N, int64_t K, void *stream) {
+  const int yt = enum_bits(yt_arg);
+  if (!xq || !sx || !wq || !sw || !y || bad_dims(M, N, K) || bad_dt(yt)) return Q4_EINVAL;
+  if (misaligned(xq, 16) || misaligned(wq, 16)) return Q4_EINVAL;
+  if (big_dims(M, N, K)) return Q4_ESHAPE;
+  if (any_overlap({{y, u(M) * u(N) * size_of(yt)}}, {{xq, mx_codes(M, K)}, {sx, mx_scales(M, K)},
+                                                     {wq, mx_codes(N, K)}, {sw, mx_scales(N, K)}}))
+    return Q4_EINVAL;
+  if (M == 0 || N == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  if (K == 0) return finish(q4::launch_zero(y, u(M) * u(N) * size_of(yt), S(stream)), Q4_PATH_GENERIC);
+  return w4a4_mx_launch(xq, sx, wq, sw, y, yt, M, N, K, S(stream));
+}
+
+extern "C" size_t q4_w4a4_mx_dynamic_workspace(int64_t M, int64_t K) {
+  if (M < 0 || K < 0) return 0;
+  return static_cast<size_t>(round256(mx_codes(M, K)) + round256(mx_scales(M, K)));
+}
+
+extern "C" q4_status q4_linear_w4a4_mx_dynamic(const void *x, q4_dtype xt_arg, const uint8_t *wq,
+                                               const uint8_t *sw, void *y, q4_dtype yt_arg, int64_t M, int64_t N,
+                                               int64_t K, void *ws, size_t ws_bytes, void *stream) {
+  const int xt = enum_bits(xt_arg), yt = enum_bits(yt_arg);
+  if (!x || !wq || !sw || !y || !ws || bad_dims(M, N, K) || bad_dt(xt) || bad_dt(yt)) return Q4_EINVAL;
+  if (misaligned(wq, 16) || misaligned(ws, 256)) return Q4_EINVAL;
+  if (big_dims(M, N, K)) return Q4_ESHAPE;
+  const size_t need = q4_w4a4_mx_dynamic_workspace(M, K);
+  if (ws_bytes < need) return Q4_EINVAL;
+  if (any_overlap({{y, u(M) * u(N) * size_of(yt)}, {ws, need}},
+                  {{x, u(M) * u(K) * size_of(xt)}, {wq, mx_codes(N, K)}, {sw, mx_scales(N, K)}}))
+    return Q4_EINVAL;
+  if (M == 0 || N == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  hipStream_t st = S(stream);
+  if (K == 0) return finish(q4::launch_zero(y, u(M) * u(N) * size_of(yt), st), Q4_PATH_GENERIC);
+  const bool forced = g_path.load(std::memory_order_relaxed) == Q4_PATH_TILED;
+  if (M <= kMxFusedMaxM && !forced)
+    return finish(q4::launch_mx_gemv_w4a4_fused(x, xt == Q4_DT_BF16, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st),
+                  Q4_PATH_GEMV);
+  uint8_t *xq = static_cast<uint8_t *>(ws), *sx = xq + round256(mx_codes(M, K));
+  if (q4::launch_mx_quantize(x, xt == Q4_DT_BF16, M, K, xq, sx, st) != hipSuccess) return Q4_EDEVICE;
+  return w4a4_mx_launch(xq, sx, wq, sw, y, yt, M, N, K, st);
+}
+
+extern "C" q4_status q4_linear_w4a16_mx(const uint16_t *x_bf16, const uint8_t *wq, const uint8_t *sw, void *y,
+                                        q4_dtype yt_arg, int64_t M, int64_t N, int64_t K, void *stream) {
+  const int yt = enum_bits(yt_arg);
+  if (!x_bf16 || !wq || !sw || !y || bad_dims(M, N, K) || bad_dt(yt) || misaligned(wq, 16)) return Q4_EINVAL;
+  if (big_dims(M, N, K)) return Q4_ESHAPE;
+  if (any_overlap({{y, u(M) * u(N) * size_of(yt)}},
+                  {{x_bf16, u(M) * u(K) * 2}, {wq, mx_codes(N, K)}, {sw, mx_scales(N, K)}}))
+    return Q4_EINVAL;
+  if (M == 0 || N == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  hipStream_t st = S(stream);
+  if (K == 0) return finish(q4::launch_zero(y, u(M) * u(N) * size_of(yt), st), Q4_PATH_GENERIC);
+  return finish(q4::launch_mx_gemv_w4a16(x_bf16, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_GEMV);
+}
+
+// ---- queries and keys -------------------------------------------------------
+
+namespace {
+
+// Bytes from the first to past the last element of T tokens of H heads.
+// False if an element's offset could pass 2^60.
+bool span(int64_t T, int64_t H, int64_t D, int64_t token, int64_t head, uint64_t size, uint64_t *bytes) {
+  *bytes = 0;
+  if (T == 0 || H == 0) return true;
+  const double last = static_cast<double>(T - 1) * static_cast<double>(token) +
+                      static_cast<double>(H - 1) * static_cast<double>(head) + static_cast<double>(D);
+  if (last > 0x1p58) return false;
+  *bytes = (u(T - 1) * u(token) + u(H - 1) * u(head) + u(D)) * size;
+  return true;
+}
+
+}  // namespace
+
+extern "C" q4_status q4_qk_norm_rope(const void *q, int64_t q_token, int64_t q_head, const void *k,
+                                     int64_t k_token, int64_t k_head, q4_dtype xt_arg, const void *q_gain,
+                                     const void *k_gain, q4_dtype gt_arg, const int64_t *positions,
+                                     const float *cos_sin, void *q_out, void *k_out, q4_dtype yt_arg, int64_t T,
+                                     int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t P, float eps,
+                                     q4_rope_pairs pairs_arg, void *stream) {
+  const int xt = enum_bits(xt_arg), gt = enum_bits(gt_arg), yt = enum_bits(yt_arg), pairs = enum_bits(pairs_arg);
+  if (!q || !q_out || !positions || !cos_sin || T < 0 || Hq < 0 || Hk < 0 || D < 0 || R < 0 || P < 0)
+    return Q4_EINVAL;
+  if (Hk > 0 && (!k || !k_out)) return Q4_EINVAL;
+  if (bad_dt(xt) || bad_dt(gt) || bad_dt(yt) || !(eps >= 0.0f)) return Q4_EINVAL;
+  if (pairs != Q4_ROPE_HALVES && pairs != Q4_ROPE_NEIGHBOURS) return Q4_EINVAL;
+  if (q_token < 0 || q_head < 0 || (Hk > 0 && (k_token < 0 || k_head < 0))) return Q4_EINVAL;
+  if (D % 2 != 0 || D < 2 || D > 65536 || R % 2 != 0 || R < 2 || R > D || P < 1 || P > kMaxNK) return Q4_ESHAPE;
+  constexpr int64_t most = INT32_MAX;
+  if (T > most || Hq > most || Hk > most || Hq + Hk > most || (T > 0 && Hq + Hk > most / T)) return Q4_ESHAPE;
+  if (Hk == 0) k = k_gain = k_out = nullptr, k_token = k_head = 0;
+  uint64_t qb, kb;
+  if (!span(T, Hq, D, q_token, q_head, size_of(xt), &qb) || !span(T, Hk, D, k_token, k_head, size_of(xt), &kb))
+    return Q4_ESHAPE;
+  const uint64_t gb = u(D) * size_of(gt);
+  if (any_overlap({{q_out, u(T) * u(Hq) * u(D) * size_of(yt)}, {k_out, u(T) * u(Hk) * u(D) * size_of(yt)}},
+                  {{q, qb}, {k, kb}, {q_gain, gb}, {k_gain, gb}, {positions, u(T) * 8},
+                   {cos_sin, u(P) * u(R) * 4}}))
+    return Q4_EINVAL;
+  if (T == 0 || Hq + Hk == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  const q4::QkArgs a = {q, k, q_token, q_head, k_token, k_head, q_gain, k_gain, gt == Q4_DT_BF16, positions,
+                        cos_sin, q_out, k_out, T, Hq, Hk, D, R, P, eps};
+  return finish(q4::launch_qk_norm_rope(a, xt == Q4_DT_BF16, yt == Q4_DT_BF16, pairs == Q4_ROPE_NEIGHBOURS,
+                                        S(stream)),
+                Q4_PATH_GEMV);
+}

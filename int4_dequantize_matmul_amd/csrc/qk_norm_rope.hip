@@ -1,0 +1,240 @@
+// Queries and keys of a decoder layer in one pass: each head's row of D
+// numbers is divided by its root mean square, multiplied by a gain, and its
+// first R columns are rotated by the token's angles:
+//   y = x / sqrt(mean(x^2) + eps) * w
+//   (a, b) -> (a cos - b sin, b cos + a sin) for the R / 2 pairs (a, b)
+// with pair i made of columns i and i + R/2 (halves) or 2 i and 2 i + 1
+// (neighbours).  Sums and products in f32, one rounding at the store.
+//
+// Bound: memory; every number is read and written once.  A head's row stays
+// in the registers of a group of L lanes (L a power of two): a lane has the
+// columns of whole pairs, so the rotation crosses no lanes, and the square
+// sum takes log2 L moves.  In units of V columns (16 bytes where sizes,
+// strides and addresses allow it, one column or one pair otherwise): halves,
+// a unit is V columns of the first half with the V opposite ones; neighbours,
+// V columns that hold V / 2 pairs; past R a unit is V plain columns.  Rows of
+// more than 64 units take turns over them, and read their row a second time
+// for the result.
+#include "kernels.hpp"
+#include "mx_device.hpp"
+
+namespace q4 {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <bool BF16, int V>
+__device__ __forceinline__ void load_v(const void *p, int64_t i, float (&o)[V]) {
+  if constexpr (BF16) {
+    const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+    if constexpr (V == 8) {
+      const uint4 t = load16(q);
+      const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[2 * j] = __uint_as_float(w[j] << 16);
+        o[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    } else if constexpr (V == 4) {
+      const uint2 t = *reinterpret_cast<const uint2 *>(q);
+      o[0] = __uint_as_float(t.x << 16), o[1] = __uint_as_float(t.x & 0xFFFF0000u);
+      o[2] = __uint_as_float(t.y << 16), o[3] = __uint_as_float(t.y & 0xFFFF0000u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = bf16_to_f32(q[j]);
+    }
+  } else {
+    const float *q = static_cast<const float *>(p) + i;
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const float4 t = *reinterpret_cast<const float4 *>(q + j);
+        o[j] = t.x, o[j + 1] = t.y, o[j + 2] = t.z, o[j + 3] = t.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = q[j];
+    }
+  }
+}
+
+template <bool BF16, int V>
+__device__ __forceinline__ void store_v(void *p, int64_t i, const float (&o)[V]) {
+  if constexpr (BF16) {
+    uint16_t *q = static_cast<uint16_t *>(p) + i;
+    if constexpr (V % 2 == 0) {
+      uint32_t w[V / 2];
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16(o[2 * j], o[2 * j + 1]);
+      if constexpr (V == 8) {
+        *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else if constexpr (V == 4) {
+        *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          q[2 * j] = static_cast<uint16_t>(w[j]);
+          q[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) q[j] = static_cast<uint16_t>(pack_bf16(o[j], 0.0f));
+    }
+  } else {
+    float *q = static_cast<float *>(p) + i;
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(q + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) q[j] = o[j];
+    }
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_gain(const void *w, bool bf16, int i, float (&o)[V]) {
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = 1.0f;
+  } else if (bf16) {
+    load_v<true, V>(w, i, o);
+  } else {
+    load_v<false, V>(w, i, o);
+  }
+}
+
+// Units of a row: PU of rotated columns, then the plain ones.
+template <int V, bool NEIGHBOURS>
+struct Unit {
+  bool rotated;
+  int c0, c1;   // first columns of its V (and, in halves, its other V) columns
+  int p0;       // its first pair
+  __device__ __forceinline__ Unit(int u, int R) {
+    const int pu = NEIGHBOURS ? R / V : R / (2 * V);
+    rotated = u < pu;
+    if (NEIGHBOURS) {
+      c0 = u * V;
+      c1 = 0;
+      p0 = c0 / 2;
+    } else {
+      p0 = u * V;
+      c0 = rotated ? p0 : R + (u - pu) * V;
+      c1 = p0 + R / 2;
+    }
+  }
+};
+
+template <bool IB, bool OB, int V, bool NEIGHBOURS>
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkArgs a, int L, int units) {
+  const uint32_t id = blockIdx.x * static_cast<uint32_t>(kThreads / L) + threadIdx.x / L;
+  const int sub = threadIdx.x & (L - 1);
+  const uint32_t H = static_cast<uint32_t>(a.Hq + a.Hk);
+  const bool live = id < static_cast<uint32_t>(a.T) * H;
+  // dead groups go through the moves below with the others
+  const uint32_t t = live ? id / H : 0, h = live ? id - t * H : 0;
+  const bool key = h >= static_cast<uint32_t>(a.Hq);
+  const int64_t hh = key ? h - a.Hq : h;
+  const void *x = key ? a.k : a.q;
+  const int64_t xi = key ? t * a.k_t + hh * a.k_h : t * a.q_t + hh * a.q_h;
+  const void *w = key ? a.wk : a.wq;
+  void *y = key ? a.ko : a.qo;
+  const int64_t yi = (static_cast<int64_t>(t) * (key ? a.Hk : a.Hq) + hh) * a.D;
+  const int D = static_cast<int>(a.D), R = static_cast<int>(a.R);
+
+  float v0[V], v1[V];
+  float ss = 0.0f;
+  auto fetch = [&](const Unit<V, NEIGHBOURS> &u) {
+    load_v<IB, V>(x, xi + u.c0, v0);
+    if (!NEIGHBOURS && u.rotated) load_v<IB, V>(x, xi + u.c1, v1);
+  };
+  if (live)
+    for (int i = sub; i < units; i += L) {
+      const Unit<V, NEIGHBOURS> u(i, R);
+      fetch(u);
+#pragma unroll
+      for (int j = 0; j < V; ++j) ss = fmaf(v0[j], v0[j], ss);
+      if (!NEIGHBOURS && u.rotated) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) ss = fmaf(v1[j], v1[j], ss);
+      }
+    }
+  for (int d = 1; d < L; d <<= 1) ss += __shfl_xor(ss, d);
+  if (!live) return;
+  const float rms = 1.0f / sqrtf(ss / static_cast<float>(D) + a.eps);
+  const int64_t pos = a.pos[t];
+  const bool known = pos >= 0 && pos < a.P;   // an unknown position gives NaN, not a wild read
+  const float *cs = a.table + (known ? pos : 0) * R;
+
+  for (int i = sub; i < units; i += L) {
+    const Unit<V, NEIGHBOURS> u(i, R);
+    if (units > L) fetch(u);   // otherwise still in registers
+    float g0[V], g1[V];
+    load_gain<V>(w, a.w_bf16, u.c0, g0);
+#pragma unroll
+    for (int j = 0; j < V; ++j) v0[j] = v0[j] * rms * g0[j];
+    if (u.rotated) {
+      if constexpr (NEIGHBOURS) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+          const float c = known ? cs[u.p0 + j] : __builtin_nanf(""), s = cs[R / 2 + u.p0 + j];
+          const float p = v0[2 * j], q = v0[2 * j + 1];
+          v0[2 * j] = p * c - q * s;
+          v0[2 * j + 1] = q * c + p * s;
+        }
+      } else {
+        load_gain<V>(w, a.w_bf16, u.c1, g1);
+        float c[V], s[V];
+        load_v<false, V>(cs, u.p0, c);
+        load_v<false, V>(cs, R / 2 + u.p0, s);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float p = v0[j], q = v1[j] * rms * g1[j], cc = known ? c[j] : __builtin_nanf("");
+          v0[j] = p * cc - q * s[j];
+          v1[j] = q * cc + p * s[j];
+        }
+        store_v<OB, V>(y, yi + u.c1, v1);
+      }
+    }
+    store_v<OB, V>(y, yi + u.c0, v0);
+  }
+}
+
+template <bool IB, bool OB, int V, bool NB>
+void go(const QkArgs &a, hipStream_t st) {
+  const int64_t units = NB ? a.D / V : a.R / (2 * V) + (a.D - a.R) / V;
+  int L = 1;
+  while (L < units && L < 64) L *= 2;
+  const int64_t rows = a.T * (a.Hq + a.Hk), per = kThreads / L;
+  qk_norm_rope_kernel<IB, OB, V, NB><<<static_cast<unsigned>((rows + per - 1) / per), kThreads, 0, st>>>(
+      a, L, static_cast<int>(units));
+}
+
+bool mult(int64_t v, int64_t m) { return v % m == 0; }
+bool at16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <bool IB, bool OB, bool NB>
+void pick(const QkArgs &a, hipStream_t st) {
+  // 16 bytes of the wider type a unit: every row start, half and remainder
+  // has to be a multiple of it
+  constexpr int V = IB && OB ? 8 : 4, S = NB ? 2 : 1;
+  const int64_t half = NB ? a.R : a.R / 2;
+  const bool vec = mult(half, V) && mult(a.D - a.R, V) && mult(a.q_t, V) && mult(a.q_h, V) && mult(a.k_t, V) &&
+                   mult(a.k_h, V) && at16(a.q) && at16(a.k) && at16(a.qo) && at16(a.ko) && at16(a.wq) &&
+                   at16(a.wk) && at16(a.table) && mult(a.R / 2, 4);
+  if (vec) go<IB, OB, V, NB>(a, st);
+  else go<IB, OB, S, NB>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(const QkArgs &a, bool in_bf16, bool out_bf16, bool neighbours, hipStream_t st) {
+  if (in_bf16 && out_bf16) neighbours ? pick<true, true, true>(a, st) : pick<true, true, false>(a, st);
+  else if (in_bf16) neighbours ? pick<true, false, true>(a, st) : pick<true, false, false>(a, st);
+  else if (out_bf16) neighbours ? pick<false, true, true>(a, st) : pick<false, true, false>(a, st);
+  else neighbours ? pick<false, false, true>(a, st) : pick<false, false, false>(a, st);
+  return hipGetLastError();
+}
+
+}  // namespace q4

@@ -15,6 +15,7 @@ Modules:
             W8A8), the dynamic W4A8 composition, the asymmetric
             (per-group zero point) W4A16 and grouped W4A8, and the int8-weight
             float-activation linears W8A32 / W8A16
+  mx        MX FP4 rows and their products; head norms with rotation
   errors    the error measures used to judge the float paths
 
 Each public function is tied to facts outside the oracle by at least one
@@ -24,4 +25,4 @@ a plausible mistake in each and requires a check to fail.  Helpers used only
 inside the pins (dequantize_w4) are the "obvious recipe" those pins compare
 against and are checked with exact rationals there.
 """
-from . import errors, formats, linear, quantize  # noqa: F401
+from . import errors, formats, linear, mx, quantize  # noqa: F401
