@@ -664,9 +664,13 @@ bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>
 // Up to this many rows the dynamic call forms the activations' codes inside
 // the product.
 constexpr int64_t kMxFusedMaxM = 16;
+// Up to this many rows a product runs by blocks of 16 weight rows.
+constexpr int64_t kMxDecodeM = 64;
 
 q4_status w4a4_mx_launch(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, void *y,
                          int yt, int64_t M, int64_t N, int64_t K, hipStream_t st) {
+  if (route(q4::mx_tiled_w4a4_ok(M, N, K), true, M, kMxDecodeM) == Q4_PATH_TILED)
+    return finish(q4::launch_mx_tiled_w4a4(xq, sx, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_TILED);
   return finish(q4::launch_mx_gemv_w4a4(xq, sx, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_GEMV);
 }
 
