@@ -130,10 +130,13 @@ hipError_t launch_mx_gemv_w4a4_fused(const void *x, bool x_bf16, const uint8_t *
                                      bool y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t st);
 hipError_t launch_mx_gemv_w4a16(const uint16_t *x, const uint8_t *wq, const uint8_t *sw, void *y, bool y_bf16,
                                 int64_t M, int64_t N, int64_t K, hipStream_t st);
-// LDS-tiled product, any shape that mx_tiled_w4a4_ok takes.
+// LDS-tiled products, any shape that mx_tiled_*_ok takes.
 bool mx_tiled_w4a4_ok(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_tiled_w4a4(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, void *y,
                                 bool y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t st);
+bool mx_tiled_w4a16_ok(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_tiled_w4a16(const uint16_t *x, const uint8_t *wq, const uint8_t *sw, void *y, bool y_bf16,
+                                 int64_t M, int64_t N, int64_t K, hipStream_t st);
 
 // Norm of each query and key head with the rotation of its first R columns.
 // Strides in elements; wq, wk (gains) and the keys may be null (then Hk == 0).

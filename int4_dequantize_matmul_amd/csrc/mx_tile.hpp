@@ -1,0 +1,69 @@
+// Parts that the LDS-tiled MX FP4 products share: the order of tiles, the
+// order of weight rows in the matrix instructions, and the stores.  Four waves
+// (2 x 2), each 16 TN weight rows by 16 TM activation rows.
+#pragma once
+
+#include "mx_device.hpp"
+
+namespace q4 {
+
+constexpr int kFar = 0x7FFFFFF0;   // a buffer offset past every range: the load gives 0
+
+// bf16 results: a lane's four results of two neighbouring instructions are 8
+// neighbouring columns of y, which it stores in 16 bytes.  The instruction's
+// rows are weight rows in an order of its own for that: row i of instruction
+// t is weight row 32 (t / 2) + 8 (i / 4) + 4 (t % 2) + i % 4.  f32 results:
+// four columns are 16 bytes, rows in order.
+template <bool BOUT>
+__device__ __forceinline__ int w_row(int t, int i) {
+  return BOUT ? 32 * (t >> 1) + 8 * (i >> 2) + 4 * (t & 1) + (i & 3) : 16 * t + i;
+}
+
+// Tile of a workgroup.  Workgroups are dealt to the 8 XCDs in turn; each XCD
+// takes a run of tiles, in bands of 8 tiles of activation rows, so that the
+// tiles it works on at a time share few panels of both operands in its L2.
+struct TileAt {
+  int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(int tiles, int tiles_m) {
+  const int id = static_cast<int>(blockIdx.x), q = tiles >> 3, rem = tiles & 7, xcd = id & 7;
+  const int tile = xcd * q + min(xcd, rem) + (id >> 3);
+  const int tiles_n = tiles / tiles_m, band = tile / (8 * tiles_n), at = tile - band * 8 * tiles_n;
+  const int rows = min(tiles_m - 8 * band, 8);
+  return {8 * band + at % rows, at / rows};
+}
+
+// Stores of a wave: lane (c, q) has row c of each 16 activation rows, from
+// row m0 and column n0 on.
+template <int TN, int TM, bool BOUT>
+__device__ __forceinline__ void store_tile(void *y, int64_t M, int64_t N, int64_t m0, int64_t n0,
+                                           const f32x4 (&acc)[TM][TN]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm) {
+    const int64_t m = m0 + 16 * tm + r;
+    if (m >= M) continue;
+    if constexpr (BOUT) {
+#pragma unroll
+      for (int tn = 0; tn < TN; tn += 2) {
+        const int64_t n = n0 + 16 * tn + 8 * g;
+        const f32x4 u = acc[tm][tn], v = acc[tm][tn + 1];
+        if (n + 8 <= N) {
+          store_any(static_cast<uint16_t *>(y) + m * N + n,
+                    make_uint4(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])));
+        } else {
+          if (n < N) store_y4<true>(y, m, n, N, u);
+          if (n + 4 < N) store_y4<true>(y, m, n + 4, N, v);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) {
+        const int64_t n = n0 + 16 * tn + 4 * g;
+        if (n < N) store_y4<false>(y, m, n, N, acc[tm][tn]);
+      }
+    }
+  }
+}
+
+}  // namespace q4

@@ -9,6 +9,7 @@
 
 #include "kernels.hpp"
 #include "mx_device.hpp"
+#include "mx_tile.hpp"
 #include "q4_lds_dma.hpp"
 
 namespace q4 {
@@ -16,7 +17,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRow = 128;        // bytes of a row in a stage: 8 blocks, 256 columns
-constexpr int kFar = 0x7FFFFFF0; // a buffer offset past every range: the load gives 0
 
 struct TileArgs {
   const uint8_t *x, *sx, *w, *sw;
@@ -33,15 +33,6 @@ constexpr int stage_bytes() {
   return (BN + BM) * (kRow + (AL ? 8 : 32));
 }
 
-// bf16 results: a lane's four results of two neighbouring instructions are 8
-// neighbouring columns of y, which it stores in 16 bytes.  The instruction's
-// rows are weight rows in an order of its own for that: row i of instruction
-// t is weight row 32 (t / 2) + 8 (i / 4) + 4 (t % 2) + i % 4.  f32 results:
-// four columns are 16 bytes, rows in order.
-template <bool BOUT>
-__device__ __forceinline__ int w_row(int t, int i) {
-  return BOUT ? 32 * (t >> 1) + 8 * (i >> 2) + 4 * (t & 1) + (i & 3) : 16 * t + i;
-}
 // Chunk c of LDS row `row` sits at c ^ swz(row), which is c ^ (i % 8) for the
 // row of lane i in either order: 8 neighbouring lanes read 8 different chunks.
 template <bool BOUT>
@@ -57,15 +48,8 @@ __global__ __launch_bounds__(kThreads, TN * TM > 32 ? 1 : 2) void mx_tiled_w4a4(
   constexpr int kStage = stage_bytes<BN, BM, AL>();
   constexpr int kX = BN * kRow, kSW = (BN + BM) * kRow, kSX = kSW + BN * (AL ? 8 : 32);
 
-  // Workgroups are dealt to the 8 XCDs in turn: each XCD takes a run of
-  // tiles, rows of activations first, so that the tiles of one weight panel
-  // share an L2.
-  int tile = blockIdx.x;
-  {
-    const int q = a.tiles >> 3, rem = a.tiles & 7, xcd = tile & 7;
-    tile = xcd * q + min(xcd, rem) + (tile >> 3);
-  }
-  const int64_t m0 = static_cast<int64_t>(tile % a.tiles_m) * BM, n0 = static_cast<int64_t>(tile / a.tiles_m) * BN;
+  const TileAt at = tile_at(a.tiles, a.tiles_m);
+  const int64_t m0 = static_cast<int64_t>(at.m) * BM, n0 = static_cast<int64_t>(at.n) * BN;
   const int rows_m = static_cast<int>(min(a.M - m0, static_cast<int64_t>(BM)));
   const int rows_n = static_cast<int>(min(a.N - n0, static_cast<int64_t>(BN)));
   const int KB = a.KB, pitch = KB * 16, steps = (KB + 7) >> 3;
@@ -211,32 +195,7 @@ __global__ __launch_bounds__(kThreads, TN * TM > 32 ? 1 : 2) void mx_tiled_w4a4(
   }
   wait_vmcnt<0>();   // the loads past the end land before the LDS is handed on
 
-  // Stores: lane (c, q) has row c of each 16 activation rows.
-#pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const int64_t m = m0 + 16 * TM * wm + 16 * tm + r;
-    if (m >= a.M) continue;
-    if constexpr (BOUT) {
-#pragma unroll
-      for (int tn = 0; tn < TN; tn += 2) {
-        const int64_t n = n0 + 16 * TN * wn + 16 * tn + 8 * g;
-        const f32x4 u = acc[tm][tn], v = acc[tm][tn + 1];
-        if (n + 8 <= a.N) {
-          store_any(static_cast<uint16_t *>(a.y) + m * a.N + n,
-                    make_uint4(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])));
-        } else {
-          if (n < a.N) store_y4<true>(a.y, m, n, a.N, u);
-          if (n + 4 < a.N) store_y4<true>(a.y, m, n + 4, a.N, v);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn) {
-        const int64_t n = n0 + 16 * TN * wn + 16 * tn + 4 * g;
-        if (n < a.N) store_y4<false>(a.y, m, n, a.N, acc[tm][tn]);
-      }
-    }
-  }
+  store_tile<TN, TM, BOUT>(a.y, a.M, a.N, m0 + 16 * TM * wm, n0 + 16 * TN * wn, acc);
 }
 
 template <int TN, int TM, bool AL, bool BOUT>

@@ -757,6 +757,8 @@ extern "C" q4_status q4_linear_w4a16_mx(const uint16_t *x_bf16, const uint8_t *w
   if (!device_ok()) return Q4_EDEVICE;
   hipStream_t st = S(stream);
   if (K == 0) return finish(q4::launch_zero(y, u(M) * u(N) * size_of(yt), st), Q4_PATH_GENERIC);
+  if (route(q4::mx_tiled_w4a16_ok(M, N, K), true, M, kMxDecodeM) == Q4_PATH_TILED)
+    return finish(q4::launch_mx_tiled_w4a16(x_bf16, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_TILED);
   return finish(q4::launch_mx_gemv_w4a16(x_bf16, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_GEMV);
 }
 
