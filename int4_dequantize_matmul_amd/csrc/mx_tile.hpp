@@ -19,18 +19,23 @@ __device__ __forceinline__ int w_row(int t, int i) {
   return BOUT ? 32 * (t >> 1) + 8 * (i >> 2) + 4 * (t & 1) + (i & 3) : 16 * t + i;
 }
 
-// Tile of a workgroup.  Workgroups are dealt to the 8 XCDs in turn; each XCD
-// takes a run of tiles, in bands of 8 tiles of activation rows, so that the
-// tiles it works on at a time share few panels of both operands in its L2.
+// Workgroups are dealt to the 8 XCDs in turn.  The place of workgroup id of n
+// in an order that gives each XCD a run of neighbours.
+__device__ __forceinline__ int xcd_run(int id, int n) {
+  const int q = n >> 3, rem = n & 7, xcd = id & 7;
+  return xcd * q + min(xcd, rem) + (id >> 3);
+}
+
+// Tile i of tiles_m x tiles_n: bands of 8 tiles of activation rows, and the
+// tiles of a weight panel next to each other in a band, so that the tiles an
+// XCD works on at a time share few panels of both operands in its L2.
 struct TileAt {
   int m, n;
 };
-__device__ __forceinline__ TileAt tile_at(int tiles, int tiles_m) {
-  const int id = static_cast<int>(blockIdx.x), q = tiles >> 3, rem = tiles & 7, xcd = id & 7;
-  const int tile = xcd * q + min(xcd, rem) + (id >> 3);
-  const int tiles_n = tiles / tiles_m, band = tile / (8 * tiles_n), at = tile - band * 8 * tiles_n;
-  const int rows = min(tiles_m - 8 * band, 8);
-  return {8 * band + at % rows, at / rows};
+__device__ __forceinline__ TileAt tile_at(int i, int tiles_m, int tiles_n) {
+  const int band = i / (8 * tiles_n), at = i - band * 8 * tiles_n, rows = min(tiles_m - 8 * band, 8);
+  // (the divisions leave uniform values in vector registers)
+  return {__builtin_amdgcn_readfirstlane(8 * band + at % rows), __builtin_amdgcn_readfirstlane(at / rows)};
 }
 
 // Stores of a wave: lane (c, q) has row c of each 16 activation rows, from

@@ -5,12 +5,14 @@
 //
 // The weights stay packed up to the registers: a lane takes 8 codes (a dword)
 // and its block's scale to 8 bf16 values in four conversions, exactly.
-// K goes in stages of 64 columns through a ring of three in LDS, requested
-// two stages ahead by loads that write LDS; activation rows that do not start
-// on 16 bytes go through registers instead, one stage ahead.  In a stage lane
-// (r, g) holds columns 16 g .. 16 g + 15 of row r, 8 for each of two matrix
-// instructions (which sum over whatever columns their lanes hold), all in
-// block g / 2 of the stage's two.
+//
+// K goes in stages of 64 columns.  In a stage lane (r, g) holds columns
+// 16 g .. 16 g + 15 of row r, 8 for each of two matrix instructions (which sum
+// over whatever columns their lanes hold), all in block g / 2 of the stage's
+// two.  Loads that write LDS bring activations three stages ahead, weights by
+// pairs of stages and scales by up to eight: what these loads cost is the
+// rows they touch, not the bytes, so a row's bytes come many at a time.
+// Activation rows that do not start on 16 bytes go through registers.
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -21,45 +23,52 @@
 namespace q4 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kStages = 3;
-
 struct TileArgs {
   const uint16_t *x;
   const uint8_t *w, *sw;
   void *y;
   int64_t M, N;
   int K, KB;
-  int tiles_m, tiles;
+  int tiles_m, tiles_n;
+  int whole;   // workgroups with a whole tile; each later one has a quarter of one
 };
 
-// LDS of a stage: activation rows of 128 bytes; weights by 16 rows, the first
-// blocks of the 16 and then their second blocks; scales in slots of 4 bytes,
-// a row's two in one (SAL: rows of scales that start on 2 bytes) or one each.
-template <int TN, int TM, bool SAL>
-constexpr int stage_bytes() {
-  return 32 * TM * 128 + 32 * TN * 32 + 32 * TN * (SAL ? 4 : 8);
-}
+// LDS of a group of waves: three stages of activation rows of 128 bytes; two
+// pairs of stages of weight rows of 64 bytes; two buffers of scales.  SB: the
+// bytes of a row's scales that one lane loads: 16 (eight stages; rows of
+// scales that start on 16 bytes), 4 (a pair of stages), 1 (any rows; slots of
+// 4 bytes).
+template <int BN, int BM, int SB>
+struct Lds {
+  static constexpr int x = 0, x_stage = BM * 128;
+  static constexpr int w = x + 3 * x_stage, w_pair = BN * 64;
+  static constexpr int s = w + 2 * w_pair, s_row = SB == 4 ? 4 : 16, s_buf = BN * s_row;
+  static constexpr int bytes = s + 2 * s_buf;
+};
 
-template <int TN, int TM, bool XAL, bool SAL, bool BOUT>
-__global__ __launch_bounds__(kThreads, 2) void mx_tiled_w4a16(TileArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int BN = 32 * TN, BM = 32 * TM;
-  constexpr int kStage = stage_bytes<TN, TM, SAL>();
-  constexpr int kW = BM * 128, kS = kW + BN * 32;
-  constexpr int nW = TN >= 4 ? TN / 4 : 1;                       // weight loads of a wave in a stage
-  constexpr int scale_loads = SAL ? TN / 2 : TN;                 // of the workgroup
-  constexpr int nS = scale_loads >= 4 ? scale_loads / 4 : 1;     // of a wave
+// The tile of rows m0 .. and weight rows n0 .. by KG groups of NW waves, each
+// with a part of K; in a group WN waves lie side by side along the weight
+// rows; a wave has 16 TN weight rows by 16 TM rows.
+template <int KG, int NW, int WN, int TN, int TM, bool XAL, int SB, bool BOUT>
+__device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t n0) {
+  extern __shared__ __align__(16) uint8_t smem0[];
+  constexpr int WM = NW / WN, BN = 16 * WN * TN, BM = 16 * WM * TM;
+  using L = Lds<BN, BM, SB>;
+  // loads of a wave: activations in a stage, weights in a pair
+  constexpr int nX = BM / 8 / NW, nW = BN / 16 / NW;
+  static_assert(nX * 8 * NW == BM && nW * 16 * NW == BN, "whole loads");
 
-  const TileAt at = tile_at(a.tiles, a.tiles_m);
-  const int64_t m0 = static_cast<int64_t>(at.m) * BM, n0 = static_cast<int64_t>(at.n) * BN;
-  const int rows_m = static_cast<int>(min(a.M - m0, static_cast<int64_t>(BM)));
-  const int rows_n = static_cast<int>(min(a.N - n0, static_cast<int64_t>(BN)));
-  const int K = a.K, KB = a.KB, steps = (K + 63) >> 6;
+  const int rows_m = min(static_cast<int>(a.M - m0), BM);
+  const int rows_n = min(static_cast<int>(a.N - n0), BN);
+  const int K = a.K, KB = a.KB, all = (K + 63) >> 6;
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wv >> 1, wm = wv & 1;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = KG > 1 ? wave % NW : wave, kg = KG > 1 ? wave / NW : 0;
+  // this group's stages, a whole number of pairs
+  const int steps = KG > 1 ? ((all + KG - 1) / KG + 1) & ~1 : all, first = kg * steps;
+  uint8_t *smem = smem0 + kg * L::bytes;
+  const int wn = wv / WM, wm = wv % WM;
   const int r = lane & 15, g = lane >> 4;
 
   const uint16_t *xt = a.x + m0 * K;
@@ -68,90 +77,277 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tiled_w4a16(TileArgs a) {
   const __amdgpu_buffer_rsrc_t rs_s = rsrc(a.sw + n0 * KB, rows_n * KB);
   const uint32_t lds0 = lds_addr(smem);
 
-  // Staging.  Activations: a wave's load fills 8 LDS rows, lane i at row
-  // i / 8, position i % 8, which holds chunk (i % 8) ^ (row % 8): 8
-  // neighbouring rows then have a chunk in 8 different places.  Rows past the
-  // tile's end and columns past K lie past the buffer's range (or are sent
-  // there) and come as zeros, and so do whole stages past the last one.
+  // Staging.  Rows past the tile's end and columns past K lie past the
+  // buffer's range (or are sent there) and come as zeros, and so do whole
+  // stages past the last one.
+  // Activations: a load fills 8 LDS rows, lane i at row i / 8, position i % 8,
+  // which holds chunk (i % 8) ^ (row % 8): 8 neighbouring rows then have a
+  // chunk in 8 different places.
   const int lrow = lane >> 3, c_x = (lane & 7) ^ lrow;
-  const int x_row0 = 8 * TM * wv + lrow;
-  // Weights: lane i of load l has tile 2 l + i / 32, block i / 16 % 2, row
-  // i % 16 of the tile.
-  auto row_of = [&](int t, int i) { return 32 * (t >> 1) + w_row<BOUT>(t & 1, i); };
-  const int w_half = (lane >> 4) & 1, w_off = row_of(lane >> 5, r) * KB;
-  const int s_off = SAL ? row_of(lane >> 4, r) * KB : w_off + w_half;
-  const int s_half = SAL ? 0 : w_half;
-  auto issue = [&](int stage, int s) {
-    const uint32_t st = lds0 + stage * kStage;
-    if constexpr (XAL) {
-      const int k = 64 * s + 8 * c_x;
-      const int o = k < K ? (x_row0 * K + k) * 2 : kFar;
+  const int x_row0 = 8 * nX * wv + lrow;
+  auto issue_x = [&](int slot, int s) {
+    const int k = 64 * s + 8 * c_x, o = (x_row0 * K + k) * 2;
 #pragma unroll
-      for (int j = 0; j < TM; ++j) dma16(rs_x, st + (TM * wv + j) * 1024, k < K ? o + 16 * j * K : kFar, 0);
-    }
-    const bool in_w = 2 * s + w_half < KB, in_s = 2 * s + s_half < KB;
+    for (int j = 0; j < nX; ++j)
+      dma16(rs_x, lds0 + L::x + slot * L::x_stage + (nX * wv + j) * 1024, k < K ? o + 16 * j * K : kFar, 0);
+  };
+  // Weights: a load fills 16 rows of the order w_row; lane i at row i / 4,
+  // position i % 4, which holds block (i % 4) ^ (row / 4): 16 rows have a
+  // block in 16 different places.
+  auto row_of = [](int t, int i) { return 32 * (t >> 1) + w_row<BOUT>(t & 1, i); };
+  const int c_w = (lane & 3) ^ ((lane >> 4) & 3);
+  auto issue_w = [&](int d) {   // pair d of the group
+    const int b = 2 * first + 4 * d + c_w;
 #pragma unroll
     for (int j = 0; j < nW; ++j) {
-      const int l = TN >= 4 ? nW * wv + j : wv % TN;   // TN = 2: two waves bring the same rows
-      dma16(rs_w, st + kW + l * 1024, in_w ? (w_off + 32 * l * KB + 2 * s + w_half) * 16 : kFar, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < nS; ++j) {
-      const int l = scale_loads >= 4 ? nS * wv + j : wv % scale_loads;
-      const int o = in_s ? s_off + (SAL ? 64 : 32) * l * KB + 2 * s : kFar;
-      if constexpr (SAL) dma2(rs_s, st + kS + l * 256, o, 0);
-      else dma1(rs_s, st + kS + l * 256, o, 0);
+      const int t = nW * wv + j;
+      dma16(rs_w, lds0 + L::w + (d & 1) * L::w_pair + t * 1024, b < KB ? (row_of(t, lane >> 2) * KB + b) * 16 : kFar, 0);
     }
   };
-  // Activations through registers (XAL false).
-  Run8<true> xr[XAL ? 1 : TM];
+  // Scales, for the pair d and (SB = 16) the three after it.
+  auto issue_s = [&](int d) {
+    const int b = 2 * first + 4 * d;
+    const uint32_t to = lds0 + L::s + ((SB == 16 ? d >> 2 : d) & 1) * L::s_buf;
+    if constexpr (SB == 1) {
+      // lane i: byte i % 4 of row i / 4
+      const int i = b + (lane & 3);
+#pragma unroll
+      for (int j = 0; j < nW; ++j) {
+        const int t = nW * wv + j;
+        dma1(rs_s, to + t * 256, i < KB ? row_of(t, lane >> 2) * KB + i : kFar, 0);
+      }
+    } else if (wv < BN / 64) {   // a row a lane
+      static_assert(BN / 64 <= NW, "a load a wave");
+      const int o = b < KB ? row_of(4 * wv + g, r) * KB + b : kFar;
+      if constexpr (SB == 16) dma16(rs_s, to + wv * 1024, o, 0);
+      else dma4(rs_s, to + wv * 256, o, 0);
+    }
+  };
+  // Activations through registers (XAL false); rows past the end are the last
+  // one again.
+  Run8<true> xr[XAL ? 1 : nX];
   auto fetch = [&](int s) {
     const int k = 64 * s + 8 * c_x;
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int row = x_row0 + 8 * j;
-      xr[XAL ? 0 : j].zero();
-      if (row < rows_m) {
-        const int64_t i = static_cast<int64_t>(row) * K + k;
-        if (k + 8 <= K) xr[XAL ? 0 : j].load(xt, i);
-        else if (k < K) xr[XAL ? 0 : j].load_part(xt, i, K - k);
+    for (int j = 0; j < nX; ++j) {
+      const int64_t i = static_cast<int64_t>(min(x_row0 + 8 * j, rows_m - 1)) * K + k;
+      Run8<true> &v = xr[XAL ? 0 : j];
+      if (64 * s + 64 <= K) {
+        v.load(xt, i);
+      } else {
+        v.zero();
+        if (k + 8 <= K) v.load(xt, i);
+        else if (k < K) v.load_part(xt, i, K - k);
       }
     }
   };
-  auto put = [&](int stage) {
+  auto put = [&](int slot) {
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
+    for (int j = 0; j < nX; ++j) {
       const uint32_t *v = xr[XAL ? 0 : j].v;
-      *reinterpret_cast<uint4 *>(smem + stage * kStage + (TM * wv + j) * 1024 + lane * 16) =
+      *reinterpret_cast<uint4 *>(smem + L::x + slot * L::x_stage + (nX * wv + j) * 1024 + lane * 16) =
           make_uint4(v[0], v[1], v[2], v[3]);
     }
   };
 
-  f32x4 acc[TM][TN] = {};
-  const int x_base = (16 * TM * wm + r) * 128, w_base = kW + TN * wn * 512 + (g >> 1) * 256 + r * 16 + (g & 1) * 8;
-  const int s_base = kS + (SAL ? (TN * wn * 16 + r) * 4 + (g >> 1) : TN * wn * 128 + (g >> 1) * 64 + r * 4);
-  const int pos[2] = {((2 * g) ^ (r & 7)) << 4, ((2 * g + 1) ^ (r & 7)) << 4};
-  auto compute = [&](int stage) {
-    const uint8_t *st = smem + stage * kStage;
+  // Fragments: activations of half j of a stage, weights and scales of a stage.
+  struct Weights {
     uint2 c[TN];
-    uint32_t sc[TN];
-    uint4 xf[2][TM];
+    uint32_t s[TN];
+  };
+  const int x_base = L::x + (16 * TM * wm + r) * 128;
+  const int pos[2] = {((2 * g) ^ (r & 7)) << 4, ((2 * g + 1) ^ (r & 7)) << 4};
+  auto read_x = [&](uint4 (&f)[TM], int slot, int j) {
+#pragma unroll
+    for (int t = 0; t < TM; ++t) f[t] = load16(smem + x_base + slot * L::x_stage + pos[j] + t * 2048);
+  };
+  auto read_w = [&](Weights &f, int s) {   // s: stage of the group
+    const int blk = 2 * (s & 1) + (g >> 1);
+    const uint8_t *w = smem + L::w + ((s >> 1) & 1) * L::w_pair + TN * wn * 1024 + r * 64 + ((blk ^ (r >> 2)) << 4) + 8 * (g & 1);
+    const uint8_t *sc = smem + L::s + ((SB == 16 ? s >> 3 : s >> 1) & 1) * L::s_buf + (TN * wn * 16 + r) * L::s_row +
+                        (SB == 16 ? 2 * (s & 7) + (g >> 1) : SB == 4 ? blk : 4 * blk);
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      f.c[t] = *reinterpret_cast<const uint2 *>(w + t * 1024);
+      f.s[t] = sc[t * 16 * L::s_row];
+    }
+  };
+  f32x4 acc[TM][TN] = {};
+  auto multiply = [&](const uint4 (&x)[TM], const Weights &w, int j) {
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) {
+      const uint4 wf = mx_decode8_bf16(j ? w.c[tn].y : w.c[tn].x, mx_scale(w.s[tn]));
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) acc[tm][tn] = mfma_bf16_16x16x32(wf, x[tm], acc[tm][tn]);
+    }
+  };
+
+  // The barrier in the middle of stage s says that stage s + 1 has landed and
+  // that stage s has been read; the second half of s is multiplied while the
+  // first of s + 1 is read.  Stage s + 3 then takes the place of s and, after
+  // odd stages, pair (s + 3) / 2 + ... the place of the pair that s ends.
+  uint4 x0[TM], x1[TM];
+  Weights w0, w1;
+  issue_s(0);
+  if constexpr (SB != 16) issue_s(1);
+  issue_w(0);
+  if constexpr (XAL) {
+    issue_x(0, first);
+    issue_x(1, first + 1);
+    issue_x(2, first + 2);
+    issue_w(1);
+    wait_vmcnt<2 * nX + nW>();
+  } else {
+    issue_w(1);
+    fetch(first);
+    put(0);
+    fetch(first + 1);
+    put(1);
+    fetch(first + 2);
+    wait_vmcnt<0>();
+  }
+  lds_barrier();
+  read_w(w0, 0);
+  read_x(x0, 0, 0);
+  int c = 0;   // s % 3
+  auto step = [&](int s, auto odd_c, Weights &w, Weights &next) {
+    constexpr bool ODD = decltype(odd_c)::value;
+    const int c1 = c == 2 ? 0 : c + 1;
+    read_x(x1, c, 1);
+    multiply(x0, w, 0);
+    if constexpr (XAL) {
+      wait_vmcnt<ODD ? nX : nX + nW>();
+    } else {
+      wait_vmcnt<0>();
+      put(c == 0 ? 2 : c - 1);   // stage s + 2
+    }
+    lds_barrier();
+    if constexpr (ODD) {
+      if constexpr (SB != 16) issue_s((s >> 1) + 2);
+      else if ((s & 7) == 1) issue_s(4 * ((s >> 3) + 1));
+    }
+    if constexpr (XAL) issue_x(c, first + s + 3);
+    if constexpr (ODD) issue_w((s >> 1) + 2);
+    if constexpr (!XAL) fetch(first + s + 3);
+    read_w(next, s + 1);
+    read_x(x0, c1, 0);
+    multiply(x1, w, 1);
+    c = c1;
+  };
+  for (int s = 0; s < steps; s += 2) {
+    step(s, std::false_type{}, w0, w1);
+    if (s + 1 < steps) step(s + 1, std::true_type{}, w1, w0);
+  }
+  wait_vmcnt<0>();   // the loads past the end land before the LDS is used again
+
+  if constexpr (KG > 1) {
+    // the groups' sums, in their order; group i takes the 16 rows i, i + KG ..
+    f32x4 *part = reinterpret_cast<f32x4 *>(smem0) + (wv * 64 + lane);
+    constexpr int kPart = NW * 64;
+    static_assert(TM * TN * kPart * 16 <= L::bytes, "the sums fit");
+    lds_barrier();
+#pragma unroll
+    for (int t = 0; t < TM * TN; ++t) part[(kg * TM * TN + t) * kPart] = acc[t / TN][t % TN];
+    lds_barrier();
+    for (int tm = kg; tm < TM; tm += KG) {
+      f32x4 sum[1][TN];
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) {
+        sum[0][tn] = part[(tm * TN + tn) * kPart];
+#pragma unroll
+        for (int i = 1; i < KG; ++i) sum[0][tn] += part[((i * TM + tm) * TN + tn) * kPart];
+      }
+      store_tile<TN, 1, BOUT>(a.y, a.M, a.N, m0 + 16 * (TM * wm + tm), n0 + 16 * TN * wn, sum);
+    }
+  } else {
+    store_tile<TN, TM, BOUT>(a.y, a.M, a.N, m0 + 16 * TM * wm, n0 + 16 * TN * wn, acc);
+  }
+}
+
+template <int KG, int NW, int WN, int TN, int TM, bool XAL, int SB, bool BOUT>
+__global__ __launch_bounds__(64 * NW * KG, NW * KG == 4 ? 2 : NW * KG / 4) void mx_tiled_w4a16(TileArgs a) {
+  constexpr int BN = 16 * WN * TN, BM = 16 * (NW / WN) * TM;
+  const TileAt at = tile_at(xcd_run(static_cast<int>(blockIdx.x), a.whole), a.tiles_m, a.tiles_n);
+  tile_body<KG, NW, WN, TN, TM, XAL, SB, BOUT>(a, static_cast<int64_t>(at.m) * BM, static_cast<int64_t>(at.n) * BN);
+}
+
+// Large products, two workgroups a CU: three stages of both operands, one
+// barrier a stage.  Weights go to LDS in rows of 32 bytes, a stage's two
+// blocks; otherwise as above.
+template <int BN, int BM, int SB>
+struct LargeLds {
+  static constexpr int x = 0, w = BM * 128, stage = w + BN * 32;
+  static constexpr int s = 3 * stage, s_buf = BN * SB, bytes = s + 2 * s_buf;
+};
+
+template <int TN, int TM, int SB, bool BOUT>
+__device__ __forceinline__ void large_body(const TileArgs &a, int64_t m0, int64_t n0) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int BN = 64 * TN, BM = 16 * TM;
+  using L = LargeLds<BN, BM, SB>;
+  constexpr int nX = BM / 32, nW = BN / 128;   // loads of a wave in a stage
+  static_assert(nW * 128 == BN && nX * 32 == BM, "whole loads");
+
+  const int rows_m = min(static_cast<int>(a.M - m0), BM), rows_n = min(static_cast<int>(a.N - n0), BN);
+  const int K = a.K, KB = a.KB, steps = (K + 63) >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+
+  const __amdgpu_buffer_rsrc_t rs_x = rsrc(a.x + m0 * K, rows_m * 2 * K);
+  const __amdgpu_buffer_rsrc_t rs_w = rsrc(a.w + n0 * KB * 16, rows_n * KB * 16);
+  const __amdgpu_buffer_rsrc_t rs_s = rsrc(a.sw + n0 * KB, rows_n * KB);
+  const uint32_t lds0 = lds_addr(smem);
+
+  auto row_of = [](int t, int i) { return 32 * (t >> 1) + w_row<BOUT>(t & 1, i); };
+  const int c_x = (lane & 7) ^ (lane >> 3), x_row0 = 8 * nX * wv + (lane >> 3);
+  // lane i: row i / 2 of 32, position i % 2, which holds block
+  // (i % 2) ^ (row / 8 % 2): 16 rows have a block in 16 different places
+  const int c_w = (lane & 1) ^ ((lane >> 4) & 1), w_row0 = row_of(lane >> 5, (lane >> 1) & 15) * KB;
+  auto issue = [&](int slot, int s) {
+    const uint32_t st = lds0 + slot * L::stage;
+    if ((s & (SB / 2 - 1)) == 0 && wv < BN / 64) {
+      const int b = 2 * s, o = b < KB ? row_of(4 * wv + g, r) * KB + b : kFar;
+      const uint32_t to = lds0 + L::s + ((s / (SB / 2)) & 1) * L::s_buf;
+      if constexpr (SB == 16) dma16(rs_s, to + wv * 1024, o, 0);
+      else dma4(rs_s, to + wv * 256, o, 0);
+    }
+    const int k = 64 * s + 8 * c_x, o = (x_row0 * K + k) * 2, b = 2 * s + c_w;
+#pragma unroll
+    for (int j = 0; j < nX; ++j) dma16(rs_x, st + (nX * wv + j) * 1024, k < K ? o + 16 * j * K : kFar, 0);
+#pragma unroll
+    for (int j = 0; j < nW; ++j) {
+      const int l = nW * wv + j;
+      dma16(rs_w, st + L::w + l * 1024, b < KB ? (w_row0 + 32 * l * KB + b) * 16 : kFar, 0);
+    }
+  };
+
+  f32x4 acc[TM][TN] = {};
+  const int w_base = L::w + TN * wv * 512 + r * 32 + (((g >> 1) ^ (r >> 3)) << 4) + (g & 1) * 8;
+  const int s_base = L::s + (TN * wv * 16 + r) * SB + (g >> 1);
+  const int pos[2] = {((2 * g) ^ (r & 7)) << 4, ((2 * g + 1) ^ (r & 7)) << 4};
+  auto compute = [&](int slot, int s) {
+    const uint8_t *st = smem + slot * L::stage;
+    const uint8_t *sc = smem + s_base + ((s / (SB / 2)) & 1) * L::s_buf + 2 * (s & (SB / 2 - 1));
+    uint2 c[TN];
+    float scale[TN];
+    uint4 x[2][TM];
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
       c[t] = *reinterpret_cast<const uint2 *>(st + w_base + t * 512);
-      sc[t] = st[s_base + t * (SAL ? 64 : 128)];
+      scale[t] = mx_scale(sc[t * 16 * SB]);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int t = 0; t < TM; ++t) xf[j][t] = load16(st + x_base + pos[j] + t * 2048);
+      for (int t = 0; t < TM; ++t) x[j][t] = load16(st + r * 128 + pos[j] + t * 2048);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn) {
-        const uint4 wf = mx_decode8_bf16(j ? c[tn].y : c[tn].x, mx_scale(sc[tn]));
+        const uint4 wf = mx_decode8_bf16(j ? c[tn].y : c[tn].x, scale[tn]);
 #pragma unroll
-        for (int tm = 0; tm < TM; ++tm) acc[tm][tn] = mfma_bf16_16x16x32(wf, xf[j][tm], acc[tm][tn]);
+        for (int tm = 0; tm < TM; ++tm) acc[tm][tn] = mfma_bf16_16x16x32(wf, x[j][tm], acc[tm][tn]);
       }
   };
 
@@ -159,66 +355,102 @@ __global__ __launch_bounds__(kThreads, 2) void mx_tiled_w4a16(TileArgs a) {
   // landed and that the one read in step s - 1 is free.
   issue(0, 0);
   issue(1, 1);
-  if constexpr (!XAL) {
-    fetch(0);
-    put(0);
-    fetch(1);
-  }
   for (int s = 0, c = 0; s < steps; ++s) {
-    const int c1 = c == kStages - 1 ? 0 : c + 1, c2 = c1 == kStages - 1 ? 0 : c1 + 1;
-    if constexpr (XAL) {
-      wait_vmcnt<TM + nW + nS>();   // all but the loads of stage s + 1
-    } else {
-      wait_vmcnt<0>();
-      put(c1);
-    }
+    wait_vmcnt<nX + nW>();   // all but the loads of stage s + 1
     lds_barrier();
-    issue(c2, s + 2);
-    if constexpr (!XAL) fetch(s + 2);
-    compute(c);
-    c = c1;
+    issue(c == 0 ? 2 : c - 1, s + 2);
+    compute(c, s);
+    c = c == 2 ? 0 : c + 1;
   }
   wait_vmcnt<0>();   // the loads past the end land before the LDS is handed on
-
-  store_tile<TN, TM, BOUT>(a.y, a.M, a.N, m0 + 16 * TM * wm, n0 + 16 * TN * wn, acc);
+  store_tile<TN, TM, BOUT>(a.y, a.M, a.N, m0, n0 + 16 * TN * wv, acc);
 }
 
-template <int TN, int TM, bool XAL, bool SAL, bool BOUT>
-hipError_t go(TileArgs a, hipStream_t st) {
-  constexpr int lds = kStages * stage_bytes<TN, TM, SAL>();
-  a.tiles_m = static_cast<int>((a.M + 32 * TM - 1) / (32 * TM));
-  a.tiles = a.tiles_m * static_cast<int>((a.N + 32 * TN - 1) / (32 * TN));
-  static const hipError_t set = hipFuncSetAttribute(
-      reinterpret_cast<const void *>(mx_tiled_w4a16<TN, TM, XAL, SAL, BOUT>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+// Whole tiles of 128 x 256, and the last ones in quarters.
+template <int SB, bool BOUT>
+__global__ __launch_bounds__(256, 2) void mx_large_w4a16(TileArgs a) {
+  const int id = static_cast<int>(blockIdx.x);
+  if (id < a.whole) {
+    const TileAt at = tile_at(xcd_run(id, a.whole), a.tiles_m, a.tiles_n);
+    large_body<4, 8, SB, BOUT>(a, 128 * static_cast<int64_t>(at.m), 256 * static_cast<int64_t>(at.n));
+  } else {
+    const int q = xcd_run(id - a.whole, static_cast<int>(gridDim.x) - a.whole);
+    const TileAt at = tile_at(a.whole + (q >> 2), a.tiles_m, a.tiles_n);
+    const int64_t m0 = 128 * static_cast<int64_t>(at.m) + 64 * (q & 1);
+    const int64_t n0 = 256 * static_cast<int64_t>(at.n) + 128 * ((q >> 1) & 1);
+    if (m0 >= a.M || n0 >= a.N) return;   // the whole workgroup
+    large_body<2, 4, SB, BOUT>(a, m0, n0);
+  }
+}
+
+template <auto Kernel, int Lds>
+hipError_t launch(const TileArgs &a, int grid, int threads, hipStream_t st) {
+  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, Lds);
   if (set != hipSuccess) return set;
-  mx_tiled_w4a16<TN, TM, XAL, SAL, BOUT><<<static_cast<unsigned>(a.tiles), kThreads, lds, st>>>(a);
+  Kernel<<<static_cast<unsigned>(grid), threads, Lds, st>>>(a);
   return hipGetLastError();
 }
 
-template <bool XAL, bool SAL, bool BOUT>
+template <int KG, int NW, int WN, int TN, int TM, bool XAL, int SB, bool BOUT>
+hipError_t go(TileArgs a, hipStream_t st) {
+  constexpr int BN = 16 * WN * TN, BM = 16 * (NW / WN) * TM;
+  a.tiles_m = static_cast<int>((a.M + BM - 1) / BM);
+  a.tiles_n = static_cast<int>((a.N + BN - 1) / BN);
+  a.whole = a.tiles_m * a.tiles_n;
+  return launch<mx_tiled_w4a16<KG, NW, WN, TN, TM, XAL, SB, BOUT>, KG * Lds<BN, BM, SB>::bytes>(a, a.whole, 64 * NW * KG, st);
+}
+
+template <int SB, bool BOUT>
+hipError_t go_large(TileArgs a, int cus, hipStream_t st) {
+  a.tiles_m = static_cast<int>((a.M + 127) / 128);
+  a.tiles_n = static_cast<int>((a.N + 255) / 256);
+  const int tiles = a.tiles_m * a.tiles_n;
+  a.whole = tiles / cus * cus;
+  return launch<mx_large_w4a16<SB, BOUT>, LargeLds<256, 128, SB>::bytes>(a, a.whole + 4 * (tiles - a.whole), 256, st);
+}
+
+// The smallest tile whose grid the CUs take at once, its K shared out among
+// the waves (a workgroup's time is its stages' latencies then); past that the
+// large tiles.  Microseconds on 256 CUs, smaller tile | larger tile:
+//   N 2048 K 5632: 32 x 64 up to 256 rows (14.7 | 19.3), 64 x 64 at 512
+//     (21.2 | 26.8), 64 x 128 at 1024 (28.3 | 35.0)
+//   N 13312 K 2048: 32 x 64 at 32 rows (8.1 | 9.2), 64 x 64 at 64 (9.6 |
+//     12.0), 64 x 128 at 128 (12.6 | 15.5)
+// Between them and one round of 128 x 256: 128 x 128 where those are more than
+// the CUs (N 13312 K 2048, 512 rows: 30.6 against 35.2), else 64 x 128 without
+// a cut of K, three and more a CU (the same at 256 rows: 19.1 against 21.7).
+template <bool XAL, int SB, bool BOUT>
 hipError_t pick(const TileArgs &a, hipStream_t st) {
-  auto tiles = [&](int64_t bn, int64_t bm) { return ((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm); };
-  if (tiles(256, 128) >= 256) return go<8, 4, XAL, SAL, BOUT>(a, st);
-  if (tiles(128, 128) >= 256) return go<4, 4, XAL, SAL, BOUT>(a, st);
-  return go<2, 2, XAL, SAL, BOUT>(a, st);
+  constexpr int SK = SB == 16 ? 4 : SB;
+  const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (tiles(32, 64) <= cus) return go<4, 4, 2, 2, 1, XAL, SK, BOUT>(a, st);
+  if (tiles(64, 64) <= cus) return go<2, 4, 2, 2, 2, XAL, SK, BOUT>(a, st);
+  if (tiles(64, 128) <= cus) return go<2, 4, 4, 2, 4, XAL, SK, BOUT>(a, st);
+  if constexpr (XAL && SB > 1)
+    if (tiles(128, 256) >= cus || tiles(128, 128) <= cus) return go_large<SB, BOUT>(a, static_cast<int>(cus), st);
+  return go<1, 4, 4, 2, 8, XAL, SK, BOUT>(a, st);
 }
 
 }  // namespace
 
 // Ranges of the tiles' buffers in 30 bits, tile counts in 31.
 bool mx_tiled_w4a16_ok(int64_t M, int64_t N, int64_t K) {
-  return K <= (int64_t(1) << 21) && ((M + 63) / 64) * ((N + 63) / 64) < (int64_t(1) << 28);
+  return K <= (int64_t(1) << 20) && ((M + 63) / 64) * ((N + 63) / 64) < (int64_t(1) << 28);
 }
 
 hipError_t launch_mx_tiled_w4a16(const uint16_t *x, const uint8_t *wq, const uint8_t *sw, void *y, bool y_bf16,
                                  int64_t M, int64_t N, int64_t K, hipStream_t st) {
-  const TileArgs a = {x, wq, sw, y, M, N, static_cast<int>(K), static_cast<int>((K + 31) / 32), 0, 0};
+  const TileArgs a = {x, wq, sw, y, M, N, static_cast<int>(K), static_cast<int>((K + 31) / 32), 0, 0, 0};
   const auto at = [](const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
-  const bool xal = K % 8 == 0 && at(x, 16), sal = a.KB % 2 == 0 && at(sw, 2);
-  if (xal && sal) return y_bf16 ? pick<true, true, true>(a, st) : pick<true, true, false>(a, st);
-  if (xal) return y_bf16 ? pick<true, false, true>(a, st) : pick<true, false, false>(a, st);
+  const bool xal = K % 8 == 0 && at(x, 16);
+  const int sb = a.KB % 16 == 0 && at(sw, 16) ? 16 : a.KB % 4 == 0 && at(sw, 4) ? 4 : 1;
+  if (xal && sb == 16) return y_bf16 ? pick<true, 16, true>(a, st) : pick<true, 16, false>(a, st);
+  if (xal && sb == 4) return y_bf16 ? pick<true, 4, true>(a, st) : pick<true, 4, false>(a, st);
+  if (xal) return y_bf16 ? pick<true, 1, true>(a, st) : pick<true, 1, false>(a, st);
   // rows through registers: scales by the byte
-  return y_bf16 ? pick<false, false, true>(a, st) : pick<false, false, false>(a, st);
+  return y_bf16 ? pick<false, 1, true>(a, st) : pick<false, 1, false>(a, st);
 }
 
 }  // namespace q4

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads, TN * TM > 32 ? 1 : 2) void mx_tiled_w4a4(
   constexpr int kStage = stage_bytes<BN, BM, AL>();
   constexpr int kX = BN * kRow, kSW = (BN + BM) * kRow, kSX = kSW + BN * (AL ? 8 : 32);
 
-  const TileAt at = tile_at(a.tiles, a.tiles_m);
+  const TileAt at = tile_at(xcd_run(static_cast<int>(blockIdx.x), a.tiles), a.tiles_m, a.tiles / a.tiles_m);
   const int64_t m0 = static_cast<int64_t>(at.m) * BM, n0 = static_cast<int64_t>(at.n) * BN;
   const int rows_m = static_cast<int>(min(a.M - m0, static_cast<int64_t>(BM)));
   const int rows_n = static_cast<int>(min(a.N - n0, static_cast<int64_t>(BN)));

@@ -166,6 +166,47 @@ def test_w4a16(M, N, K, path, yt):
     check(q4.q4_linear_w4a16_mx(xd, dev(wq), dev(sw), yt), ref, mag, K, "w4a16")
 
 
+# More tiles than compute units: whole large tiles and the cut ones at the end,
+# with edges in both directions; rows of scales that start on 16 bytes, on 4,
+# and on any; rows of activations that start on 16 bytes and on 2.
+LARGE = [(1000, 8210, 512), (1290, 6401, 640), (1100, 8300, 96), (1030, 8193, 130), (700, 5000, 1024),
+         (513, 4100, 192), (260, 8197, 512), (900, 4600, 37), (130, 13317, 512)]
+
+
+@pytest.mark.parametrize("yt", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_products_of_many_tiles(M, N, K, yt):
+    xd, v = rows(M + N, M, K, "bf16")
+    wq, sw = weights(K + N, N, K)
+    ref, mag = X.linear_w4a16(v, wq, sw)
+    check(q4.q4_linear_w4a16_mx(xd, dev(wq), dev(sw), yt), ref, mag, K, "w4a16")
+    xq, sx = X.quantize_rows(v)
+    ref, mag = X.linear_w4a4(xq, sx, wq, sw)
+    check(q4.q4_linear_w4a4_mx(dev(xq), dev(sx), dev(wq), dev(sw), yt), ref, mag, K, "w4a4")
+
+
+@pytest.mark.parametrize("off", [1, 2, 4, 8])
+def test_scales_and_rows_of_any_alignment(off):
+    """Scale arrays and bf16 rows that start at odd addresses (codes start on 16 bytes)."""
+    for M, N, K in ((40, 300, 512), (20, 100, 256), (300, 8200, 512)):
+        _, v = rows(off, M, K, "bf16")
+        wq, sw = weights(off + 1, N, K)
+        xq, sx = X.quantize_rows(v)
+
+        def at(a, o):
+            buf = torch.zeros(a.size + o, dtype=torch.uint8, device=DEV)
+            buf[o:] = torch.from_numpy(np.ascontiguousarray(a).reshape(-1)).to(DEV)
+            return buf[o:].view(a.shape)
+
+        xb = bf16(v)[0]
+        xs = torch.zeros(xb.size + off, dtype=torch.bfloat16, device=DEV)
+        xs[off:] = dev(xb).reshape(-1)
+        ref, mag = X.linear_w4a16(v, wq, sw)
+        check(q4.q4_linear_w4a16_mx(xs[off:].view(M, K), dev(wq), at(sw, off), "f32"), ref, mag, K, "w4a16")
+        ref, mag = X.linear_w4a4(xq, sx, wq, sw)
+        check(q4.q4_linear_w4a4_mx(dev(xq), at(sx, off), dev(wq), at(sw, 16 - off), "f32"), ref, mag, K, "w4a4")
+
+
 @pytest.mark.parametrize("path", ["auto", "gemv", "tiled"])
 @pytest.mark.parametrize("M", [1, 5, 16, 40, 130])
 def test_products_index_probe(M, path):
