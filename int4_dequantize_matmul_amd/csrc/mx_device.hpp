@@ -148,6 +148,19 @@ __device__ __forceinline__ f32x4 mfma_mx_16x16x128(uint4 a, uint4 b, f32x4 c, ui
                                                           static_cast<int>(sb));
 }
 
+// The same with 32 rows and 64 columns: lane (r, h) has 32 columns of row r,
+// a block; result register 4 a + b of lane (c, h) is the element of A's row
+// 8 a + 4 h + b and B's row c.  On this chip it does the work of four of the
+// above in the time of two of them.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+template <int J>
+__device__ __forceinline__ f32x16 mfma_mx_32x32x64(uint4 a, uint4 b, f32x16 c, uint32_t sa, uint32_t sb) {
+  const i32x8 av = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w)};
+  const i32x8 bv = {static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, J, static_cast<int>(sa), J,
+                                                         static_cast<int>(sb));
+}
+
 // float32 -> bf16 pairs, round to nearest even, NaN kept.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};

@@ -71,4 +71,34 @@ __device__ __forceinline__ void store_tile(void *y, int64_t M, int64_t N, int64_
   }
 }
 
+// The same for results of 32 x 32 instructions: the row i of an instruction is
+// weight row w_row32(i) of its 32, so that lane (c, h) has 16 neighbouring
+// columns of y.
+__device__ __forceinline__ int w_row32(int i) { return 16 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3); }
+
+template <bool BOUT>
+__device__ __forceinline__ void store_16(void *y, int64_t m, int64_t n, int64_t N, const f32x16 &v) {
+  if constexpr (BOUT) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 8) {
+      uint16_t *p = static_cast<uint16_t *>(y) + m * N + n + j;
+      if (n + j + 8 <= N) {
+        store_any(p, make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
+                                      pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7])));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (n + j + i < N) p[i] = static_cast<uint16_t>(pack_bf16(v[j + i], 0.0f));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const f32x4 u = {v[j], v[j + 1], v[j + 2], v[j + 3]};
+      if (n + j + 4 <= N) store_any(static_cast<float *>(y) + m * N + n + j, u);
+      else if (n + j < N) store_y4<false>(y, m, n + j, N, u);
+    }
+  }
+}
+
 }  // namespace q4

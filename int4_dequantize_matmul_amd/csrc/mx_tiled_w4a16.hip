@@ -81,15 +81,17 @@ __device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t
   // buffer's range (or are sent there) and come as zeros, and so do whole
   // stages past the last one.
   // Activations: a load fills 8 LDS rows, lane i at row i / 8, position i % 8,
-  // which holds chunk (i % 8) ^ (row % 8): 8 neighbouring rows then have a
-  // chunk in 8 different places.
-  const int lrow = lane >> 3, c_x = (lane & 7) ^ lrow;
+  // which holds chunk (i % 8) ^ (row / 2 % 8): 16 neighbouring rows then have a
+  // chunk in the 16 different places that one clock reads.
+  const int lrow = lane >> 3;
+  auto chunk = [&](int j) { return (lane & 7) ^ (lrow >> 1) ^ (4 * ((nX * wv + j) & 1)); };   // of load j
   const int x_row0 = 8 * nX * wv + lrow;
   auto issue_x = [&](int slot, int s) {
-    const int k = 64 * s + 8 * c_x, o = (x_row0 * K + k) * 2;
 #pragma unroll
-    for (int j = 0; j < nX; ++j)
-      dma16(rs_x, lds0 + L::x + slot * L::x_stage + (nX * wv + j) * 1024, k < K ? o + 16 * j * K : kFar, 0);
+    for (int j = 0; j < nX; ++j) {
+      const int k = 64 * s + 8 * chunk(j);
+      dma16(rs_x, lds0 + L::x + slot * L::x_stage + (nX * wv + j) * 1024, k < K ? ((x_row0 + 8 * j) * K + k) * 2 : kFar, 0);
+    }
   };
   // Weights: a load fills 16 rows of the order w_row; lane i at row i / 4,
   // position i % 4, which holds block (i % 4) ^ (row / 4): 16 rows have a
@@ -127,9 +129,9 @@ __device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t
   // one again.
   Run8<true> xr[XAL ? 1 : nX];
   auto fetch = [&](int s) {
-    const int k = 64 * s + 8 * c_x;
 #pragma unroll
     for (int j = 0; j < nX; ++j) {
+      const int k = 64 * s + 8 * chunk(j);
       const int64_t i = static_cast<int64_t>(min(x_row0 + 8 * j, rows_m - 1)) * K + k;
       Run8<true> &v = xr[XAL ? 0 : j];
       if (64 * s + 64 <= K) {
@@ -156,7 +158,7 @@ __device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t
     uint32_t s[TN];
   };
   const int x_base = L::x + (16 * TM * wm + r) * 128;
-  const int pos[2] = {((2 * g) ^ (r & 7)) << 4, ((2 * g + 1) ^ (r & 7)) << 4};
+  const int pos[2] = {((2 * g) ^ (r >> 1)) << 4, ((2 * g + 1) ^ (r >> 1)) << 4};
   auto read_x = [&](uint4 (&f)[TM], int slot, int j) {
 #pragma unroll
     for (int t = 0; t < TM; ++t) f[t] = load16(smem + x_base + slot * L::x_stage + pos[j] + t * 2048);
@@ -300,7 +302,7 @@ __device__ __forceinline__ void large_body(const TileArgs &a, int64_t m0, int64_
   const uint32_t lds0 = lds_addr(smem);
 
   auto row_of = [](int t, int i) { return 32 * (t >> 1) + w_row<BOUT>(t & 1, i); };
-  const int c_x = (lane & 7) ^ (lane >> 3), x_row0 = 8 * nX * wv + (lane >> 3);
+  const int c_x = (lane & 7) ^ (lane >> 4), x_row0 = 8 * nX * wv + (lane >> 3);   // chunk c_x in even loads
   // lane i: row i / 2 of 32, position i % 2, which holds block
   // (i % 2) ^ (row / 8 % 2): 16 rows have a block in 16 different places
   const int c_w = (lane & 1) ^ ((lane >> 4) & 1), w_row0 = row_of(lane >> 5, (lane >> 1) & 15) * KB;
@@ -312,9 +314,13 @@ __device__ __forceinline__ void large_body(const TileArgs &a, int64_t m0, int64_
       if constexpr (SB == 16) dma16(rs_s, to + wv * 1024, o, 0);
       else dma4(rs_s, to + wv * 256, o, 0);
     }
-    const int k = 64 * s + 8 * c_x, o = (x_row0 * K + k) * 2, b = 2 * s + c_w;
+    const int b = 2 * s + c_w;
+    static_assert(nX % 2 == 0, "a wave's loads begin at 16 rows");
 #pragma unroll
-    for (int j = 0; j < nX; ++j) dma16(rs_x, st + (nX * wv + j) * 1024, k < K ? o + 16 * j * K : kFar, 0);
+    for (int j = 0; j < nX; ++j) {
+      const int k = 64 * s + 8 * (c_x ^ (4 * (j & 1)));
+      dma16(rs_x, st + (nX * wv + j) * 1024, k < K ? ((x_row0 + 8 * j) * K + k) * 2 : kFar, 0);
+    }
 #pragma unroll
     for (int j = 0; j < nW; ++j) {
       const int l = nW * wv + j;
@@ -325,7 +331,7 @@ __device__ __forceinline__ void large_body(const TileArgs &a, int64_t m0, int64_
   f32x4 acc[TM][TN] = {};
   const int w_base = L::w + TN * wv * 512 + r * 32 + (((g >> 1) ^ (r >> 3)) << 4) + (g & 1) * 8;
   const int s_base = L::s + (TN * wv * 16 + r) * SB + (g >> 1);
-  const int pos[2] = {((2 * g) ^ (r & 7)) << 4, ((2 * g + 1) ^ (r & 7)) << 4};
+  const int pos[2] = {((2 * g) ^ (r >> 1)) << 4, ((2 * g + 1) ^ (r >> 1)) << 4};
   auto compute = [&](int slot, int s) {
     const uint8_t *st = smem + slot * L::stage;
     const uint8_t *sc = smem + s_base + ((s / (SB / 2)) & 1) * L::s_buf + 2 * (s & (SB / 2 - 1));

@@ -2,9 +2,15 @@
 //
 //   y[m,n] = sum_b 2^(sx[m,b] + sw[n,b] - 254) sum_{k in b} cx[m,k] cw[n,k]
 //
-// The scaled 16 x 16 x 128 instruction takes the format as stored: a lane's
+// The scaled 32 x 32 x 64 instruction takes the format as stored: a lane's
 // operand is one block (16 bytes) and a byte of scale, so nothing is unpacked
 // and the sums stay in f32.
+//
+// K goes in stages of 256 columns, 128 bytes of a row, through two places in
+// LDS: a load that writes LDS costs what the rows it touches cost, in pieces
+// of 128 bytes (19 clocks a KB, 28 in pieces of 64 bytes).  A stage is four
+// instructions deep: in step q lane (r, h) takes block 4 h + q of row r, whose
+// scale is byte q of a dword.
 #include <type_traits>
 
 #include "kernels.hpp"
@@ -15,221 +21,294 @@
 namespace q4 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRow = 128;        // bytes of a row in a stage: 8 blocks, 256 columns
-
 struct TileArgs {
   const uint8_t *x, *sx, *w, *sw;
   void *y;
   int64_t M, N;
   int KB;
-  int tiles_m, tiles;
+  int tiles_m, tiles_n;
 };
 
-// LDS of a stage: weight rows, activation rows, and their scales: 8 bytes a
-// row, or (rows whose scales do not start on a dword) 8 dwords of one byte.
-template <int BN, int BM, bool AL>
-constexpr int stage_bytes() {
-  return (BN + BM) * (kRow + (AL ? 8 : 32));
-}
+// LDS of a group of waves: two stages of weight rows and then activation rows,
+// and two buffers of their scales in slots of 16 bytes.  S16 (rows of scales
+// that start on 16 bytes): a slot has the scales of two stages.  Otherwise the
+// three dwords that a stage's 8 scales lie in, wherever they begin.
+template <int BN, int BM>
+struct Lds {
+  static constexpr int rows = BN + BM, stage = rows * 128, s = 2 * stage, s_buf = rows * 16, bytes = s + 2 * s_buf;
+};
 
-// Chunk c of LDS row `row` sits at c ^ swz(row), which is c ^ (i % 8) for the
-// row of lane i in either order: 8 neighbouring lanes read 8 different chunks.
-template <bool BOUT>
-__device__ __forceinline__ int w_swz(int row) {
-  return BOUT ? (row & 3) | ((row >> 1) & 4) : row & 7;
-}
+// Tiles of 32 WM TM rows by 32 WN TN weight rows, by KG groups of NW waves,
+// each with a part of K; in a group WN waves lie side by side along the weight
+// rows; a wave has 32 TN weight rows by 32 TM rows.
+template <int KG, int NW, int WN, int TN, int TM, bool S16, bool BOUT>
+__global__ __launch_bounds__(64 * NW * KG, NW * KG <= 4 ? 2 : NW * KG / 4) void mx_tiled_w4a4(TileArgs a) {
+  extern __shared__ __align__(16) uint8_t smem0[];
+  constexpr int WM = NW / WN, BN = 32 * WN * TN, BM = 32 * WM * TM;
+  using L = Lds<BN, BM>;
 
-// Waves 2 x 2, each 16 TN weight rows by 16 TM activation rows.
-template <int TN, int TM, bool AL, bool BOUT>
-__global__ __launch_bounds__(kThreads, TN * TM > 32 ? 1 : 2) void mx_tiled_w4a4(TileArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int BN = 32 * TN, BM = 32 * TM;
-  constexpr int kStage = stage_bytes<BN, BM, AL>();
-  constexpr int kX = BN * kRow, kSW = (BN + BM) * kRow, kSX = kSW + BN * (AL ? 8 : 32);
-
-  const TileAt at = tile_at(xcd_run(static_cast<int>(blockIdx.x), a.tiles), a.tiles_m, a.tiles / a.tiles_m);
-  const int64_t m0 = static_cast<int64_t>(at.m) * BM, n0 = static_cast<int64_t>(at.n) * BN;
-  const int rows_m = static_cast<int>(min(a.M - m0, static_cast<int64_t>(BM)));
-  const int rows_n = static_cast<int>(min(a.N - n0, static_cast<int64_t>(BN)));
-  const int KB = a.KB, pitch = KB * 16, steps = (KB + 7) >> 3;
+  const int KB = a.KB, pitch = KB * 16, all = (KB + 7) >> 3, tiles = a.tiles_m * a.tiles_n;
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wv >> 1, wm = wv & 1;
-  const int r = lane & 15, g = lane >> 4;
-
-  const __amdgpu_buffer_rsrc_t rs_w = rsrc(a.w + n0 * pitch, rows_n * pitch);
-  const __amdgpu_buffer_rsrc_t rs_x = rsrc(a.x + m0 * pitch, rows_m * pitch);
-  const __amdgpu_buffer_rsrc_t rs_sw = rsrc(a.sw + n0 * KB, rows_n * KB);
-  const __amdgpu_buffer_rsrc_t rs_sx = rsrc(a.sx + m0 * KB, rows_m * KB);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = KG > 1 ? wave % NW : wave, kg = KG > 1 ? wave / NW : 0;
+  const int steps = KG > 1 ? (all + KG - 1) / KG : all, first = 8 * kg * steps;   // this group's stages; its first block
+  uint8_t *smem = smem0 + kg * L::bytes;
+  const int wn = wv / WM, wm = wv % WM;
+  const int r = lane & 31, h = lane >> 5;
   const uint32_t lds0 = lds_addr(smem);
 
-  // Staging.  A wave's load fills 8 LDS rows: lane i lands at row i / 8,
-  // position i % 8.  Rows past the tile's end and chunks from KB on lie past
-  // the buffer's range (or are sent there) and come as zeros, and so does the
-  // whole step past the last one.
-  const int lrow = lane >> 3, lpos = lane & 7;
-  const int c_w[2] = {lpos ^ w_swz<BOUT>(lrow), lpos ^ w_swz<BOUT>(lrow + 8)}, c_x = lpos ^ (lrow & 7);
-  const int p_w = (8 * TN * wv + lrow) * pitch, p_x = (8 * TM * wv + lrow) * pitch;
-  const int s_b = AL ? 4 * (lane & 1) : lpos;
-  auto issue = [&](int stage, int s) {
-    const uint32_t st = lds0 + stage * kStage;
-    const int b0 = 8 * s;
-    const bool in_w[2] = {b0 + c_w[0] < KB, b0 + c_w[1] < KB}, in_x = b0 + c_x < KB, in_s = b0 + s_b < KB;
-    const int o_w[2] = {p_w + (b0 + c_w[0]) * 16, p_w + (b0 + c_w[1]) * 16}, o_x = p_x + (b0 + c_x) * 16;
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-      dma16(rs_w, st + (TN * wv + j) * 1024, in_w[j & 1] ? o_w[j & 1] + 8 * j * pitch : kFar, 0);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) dma16(rs_x, st + kX + (TM * wv + j) * 1024, in_x ? o_x + 8 * j * pitch : kFar, 0);
-    if constexpr (AL) {
-      // lane i: dword i % 2 of row i / 2
-#pragma unroll
-      for (int q = 0; q < TN; q += 4) {
-        const int l = TN < 4 ? wv % TN : q + wv;   // TN < 4: two waves bring the same rows
-        dma4(rs_sw, st + kSW + l * 256, in_s ? (32 * l + (lane >> 1)) * KB + b0 + s_b : kFar, 0);
-      }
-#pragma unroll
-      for (int q = 0; q < TM; q += 4) {
-        const int l = TM < 4 ? wv % TM : q + wv;
-        dma4(rs_sx, st + kSX + l * 256, in_s ? (32 * l + (lane >> 1)) * KB + b0 + s_b : kFar, 0);
-      }
+  const TileAt at = tile_at(xcd_run(static_cast<int>(blockIdx.x), tiles), a.tiles_m, a.tiles_n);
+  const int64_t m0 = static_cast<int64_t>(at.m) * BM, n0 = static_cast<int64_t>(at.n) * BN;
+  const int rows_m = min(static_cast<int>(a.M - m0), BM), rows_n = min(static_cast<int>(a.N - n0), BN);
+  const __amdgpu_buffer_rsrc_t rs_w = rsrc(a.w + n0 * pitch, rows_n * pitch);
+  const __amdgpu_buffer_rsrc_t rs_x = rsrc(a.x + m0 * pitch, rows_m * pitch);
+  // whole dwords of scales: a dword with a byte of them may be read whole
+  const uint8_t *sw0 = a.sw + n0 * KB, *sx0 = a.sx + m0 * KB;
+  const int sw_odd = static_cast<int>(reinterpret_cast<uintptr_t>(sw0) & 3);
+  const int sx_odd = static_cast<int>(reinterpret_cast<uintptr_t>(sx0) & 3);
+  const __amdgpu_buffer_rsrc_t rs_sw = rsrc(sw0 - sw_odd, (sw_odd + rows_n * KB + 3) & ~3);
+  const __amdgpu_buffer_rsrc_t rs_sx = rsrc(sx0 - sx_odd, (sx_odd + rows_m * KB + 3) & ~3);
+
+  // Staging.  A load fills 8 LDS rows: lane i lands at row i / 8, position
+  // i % 8, which holds chunk (i % 8) ^ (row / 2 % 8): 16 neighbouring rows then
+  // have a chunk in the 16 different places that one clock reads.  LDS row i of the weights is row w_row32(i
+  // % 32) of its 32.  Rows past the tile's end and chunks from KB on lie past
+  // the buffer's range (or are sent there) and come as zeros, and so do whole
+  // stages past the last one.
+  // (An address worked out in vector registers is still the same in all lanes.)
+  auto uniform = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); };
+  // (The offsets are formed anew for each load: kept in registers they would
+  // not leave room for the sums.)
+  const int lrow = lane >> 3, even = (lane & 7) ^ (lrow >> 1);
+  constexpr int nW = BN / 8 / NW, nX = BM / 8 / NW;   // loads of a wave in a stage
+  static_assert(nW * 8 * NW == BN && nX * 8 * NW == BM, "whole loads");
+  auto chunk = [&](int j) { return even ^ (4 * (j & 1)); };   // of a wave's load j
+  int x_lane = lrow * pitch, w_lane = w_row32(lrow) * pitch;
+  static_assert(nW % 2 == 0 && nX % 2 == 0, "a wave's loads begin at 16 rows");
+  // LDS rows i .. i + 7 of the weights are rows w_at(i) + w_row32(0 .. 7)
+  auto w_at = [](int i) { return (i & ~31) + 4 * ((i >> 3) & 3); };
+  auto load_w = [&](int slot, int b0, int j) {
+    const int i = 8 * (nW * wv + j);
+    dma16(rs_w, uniform(lds0 + slot * L::stage + i * 128), b0 + chunk(j) < KB ? w_lane + w_at(i) * pitch + (b0 + chunk(j)) * 16 : kFar, 0);
+  };
+  auto load_x = [&](int slot, int b0, int j) {
+    const int i = 8 * (nX * wv + j);
+    dma16(rs_x, uniform(lds0 + slot * L::stage + (BN + i) * 128), b0 + chunk(j) < KB ? x_lane + i * pitch + (b0 + chunk(j)) * 16 : kFar, 0);
+  };
+  // Scales.  S16: a row a lane, 64 rows a load, every other stage.  Else lane i
+  // has dword i % 4 of row i / 4.
+  constexpr int nSw = S16 ? 1 : BN / 16 / NW, nSx = S16 ? 0 : BM / 16 / NW;
+  static_assert(S16 ? L::rows == 64 * NW : nSw * 16 * NW == BN && nSx * 16 * NW == BM, "whole loads");
+  auto w_row_at = [](int i) { return (i & ~31) + w_row32(i & 31); };
+  int sw_lane, sx_lane;
+  const __amdgpu_buffer_rsrc_t rs_s16 = 64 * wv < BN ? rs_sw : rs_sx;
+  if constexpr (S16) {
+    const bool w = 64 * wv < BN;
+    sw_lane = (w ? w_row_at(64 * wv + lane) : 64 * wv - BN + lane) * KB;
+    sx_lane = 0;
+  } else {
+    sw_lane = sw_odd + w_row32((lane >> 2) & 7) * KB + 4 * (lane >> 5) * KB;   // LDS rows 8 .. 15 come 4 rows on
+    sx_lane = sx_odd + (lane >> 2) * KB;
+  }
+  auto load_sw = [&](int s, int b0, int j) {
+    if constexpr (S16) {
+      dma16(rs_s16, uniform(lds0 + L::s + ((s >> 1) & 1) * L::s_buf + wv * 1024), b0 < KB ? sw_lane + b0 : kFar, 0);
     } else {
-      // lane i: byte i % 8 of row i / 8
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        dma1(rs_sw, st + kSW + (TN * wv + j) * 256, in_s ? (8 * (TN * wv + j) + lrow) * KB + b0 + s_b : kFar, 0);
-#pragma unroll
-      for (int j = 0; j < TM; ++j)
-        dma1(rs_sx, st + kSX + (TM * wv + j) * 256, in_s ? (8 * (TM * wv + j) + lrow) * KB + b0 + s_b : kFar, 0);
+      const int i = 16 * (nSw * wv + j), sub = 4 * (lane & 3);
+      const int o = (b0 < KB) & (sub < 12) ? ((sw_lane + w_at(i) * KB + b0) & ~3) + sub : kFar;
+      dma4(rs_sw, uniform(lds0 + L::s + (s & 1) * L::s_buf + i * 16), o, 0);
     }
   };
+  auto load_sx = [&](int s, int b0, int j) {
+    const int i = 16 * (nSx * wv + j), sub = 4 * (lane & 3);
+    const int o = (b0 < KB) & (sub < 12) ? ((sx_lane + i * KB + b0) & ~3) + sub : kFar;
+    dma4(rs_sx, uniform(lds0 + L::s + (s & 1) * L::s_buf + (BN + i) * 16), o, 0);
+  };
+  constexpr int nS = nSw + nSx, nAll = nS + nW + nX;
+  auto load = [&](int slot, int s, int j) {   // load j of stage s; slot = s % 2
+    const int b0 = first + 8 * s;
+    if (j < nSw && !(S16 && slot)) load_sw(s, b0, j);
+    else if (j < nSw) return;
+    else if (j < nS) load_sx(s, b0, j - nSw);
+    else if (j < nS + nW) load_w(slot, b0, j - nS);
+    else load_x(slot, b0, j - nS - nW);
+  };
+  const std::integral_constant<int, 0> c0;
+  const std::integral_constant<int, 1> c1;
+  const std::integral_constant<int, 2> c2;
+  const std::integral_constant<int, 3> c3;
 
-  // Fragments.  Half j (0, 1) of a stage: lane group g takes block 2 g + j.
+  // Fragments of step q of a stage, and the scales of a stage.
   struct Frags {
     uint4 w[TN], x[TM];
   };
   struct Scales {
-    uint32_t w[TN][AL ? 1 : 2], x[TM][AL ? 1 : 2];
+    uint32_t w[TN], x[TM];
   };
-  const int w_base = (16 * TN * wn + w_row<BOUT>(0, r)) * kRow, x_base = kX + (16 * TM * wm + r) * kRow;
-  const int pos[2] = {((2 * g) ^ (r & 7)) << 4, ((2 * g + 1) ^ (r & 7)) << 4};
-  auto read = [&](Frags &f, int stage, int j) {
-    const uint8_t *st = smem + stage * kStage + pos[j];
+  const int w_base = (32 * TN * wn + r) * 128, x_base = (BN + 32 * TM * wm + r) * 128;
+  auto read = [&](Frags &f, int slot, int q) {
+    const uint8_t *st = smem + slot * L::stage + (((4 * h + q) ^ ((r >> 1) & 7)) << 4);
 #pragma unroll
-    for (int t = 0; t < TN; ++t) f.w[t] = load16(st + w_base + (w_row<BOUT>(t, 0)) * kRow);
+    for (int t = 0; t < TN; ++t) f.w[t] = load16(st + w_base + t * 4096);
 #pragma unroll
-    for (int t = 0; t < TM; ++t) f.x[t] = load16(st + x_base + 16 * t * kRow);
+    for (int t = 0; t < TM; ++t) f.x[t] = load16(st + x_base + t * 4096);
   };
-  auto read_scales = [&](Scales &s, int stage) {
-    const uint8_t *st = smem + stage * kStage;
+  // A row's scales of the lane's four blocks; in the last stage the bytes past
+  // the row's end are another row's, and a NaN among them would meet the zeros
+  // there.
+  uint32_t odd[TN + TM];
 #pragma unroll
-    for (int t = 0; t < TN; ++t) {
-      const int row = 16 * TN * wn + w_row<BOUT>(t, r);
-      if constexpr (AL) {
-        s.w[t][0] = *reinterpret_cast<const uint16_t *>(st + kSW + row * 8 + 2 * g);
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(st + kSW + row * 32 + 8 * g);
-        s.w[t][0] = v.x, s.w[t][1] = v.y;
-      }
-    }
+  for (int t = 0; t < TN; ++t) odd[t] = (sw_odd + w_row_at(32 * (TN * wn + t) + r) * KB) & 3;
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      const int row = 16 * TM * wm + 16 * t + r;
-      if constexpr (AL) {
-        s.x[t][0] = *reinterpret_cast<const uint16_t *>(st + kSX + row * 8 + 2 * g);
+  for (int t = 0; t < TM; ++t) odd[TN + t] = (sx_odd + (32 * (TM * wm + t) + r) * KB) & 3;
+  auto read_scales = [&](Scales &f, int s) {
+    const int left = KB - first - 8 * s - 4 * h;
+    const uint32_t mask = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+    auto one = [&](int row, uint32_t o) {
+      if constexpr (S16) {
+        return *reinterpret_cast<const uint32_t *>(smem + L::s + ((s >> 1) & 1) * L::s_buf + row * 16 + 8 * (s & 1) + 4 * h);
       } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(st + kSX + row * 32 + 8 * g);
-        s.x[t][0] = v.x, s.x[t][1] = v.y;
+        const uint32_t *d = reinterpret_cast<const uint32_t *>(smem + L::s + (s & 1) * L::s_buf + row * 16 + 4 * h);
+        return __builtin_amdgcn_alignbyte(d[1], d[0], o) & mask;
       }
-    }
+    };
+#pragma unroll
+    for (int t = 0; t < TN; ++t) f.w[t] = one(32 * (TN * wn + t) + r, odd[t]);
+#pragma unroll
+    for (int t = 0; t < TM; ++t) f.x[t] = one(BN + 32 * (TM * wm + t) + r, odd[TN + t]);
   };
 
-  f32x4 acc[TM][TN] = {};
-  auto multiply = [&](const Frags &f, const Scales &s, auto half_c) {
-    constexpr int J = decltype(half_c)::value;
+  f32x16 acc[TM][TN] = {};
+  // Between the instructions go the loads lo .. hi - 1 of stage s.
+  auto multiply = [&](const Frags &f, const Scales &sc, auto q_c, auto slot_c, int s, auto lo_c, auto hi_c) {
+    constexpr int Q = decltype(q_c)::value, lo = decltype(lo_c)::value, n = decltype(hi_c)::value - lo;
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn) {
-        if constexpr (AL) acc[tm][tn] = mfma_mx_16x16x128<J>(f.w[tn], f.x[tm], acc[tm][tn], s.w[tn][0], s.x[tm][0]);
-        else acc[tm][tn] = mfma_mx_16x16x128<0>(f.w[tn], f.x[tm], acc[tm][tn], s.w[tn][J], s.x[tm][J]);
+        const int at = tm * TN + tn;
+        acc[tm][tn] = mfma_mx_32x32x64<Q>(f.w[tn], f.x[tm], acc[tm][tn], sc.w[tn], sc.x[tm]);
+#pragma unroll
+        for (int j = at * n / (TM * TN); j < (at + 1) * n / (TM * TN); ++j) {
+          __builtin_amdgcn_sched_barrier(0);
+          load(decltype(slot_c)::value, s, lo + j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
   };
-  // one LDS read between every few matrix instructions
-  auto interleave = [&](int reads) {
-    constexpr int per = TN * TM / (TN + TM) > 0 ? TN * TM / (TN + TM) : 1;
-#pragma unroll
-    for (int i = 0; i < reads; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, per, 0);
-    }
-  };
+  const std::integral_constant<int, 0> n0c;
+  const std::integral_constant<int, nAll / 3> n1c;
+  const std::integral_constant<int, 2 * nAll / 3> n2c;
+  const std::integral_constant<int, nAll> n3c;
 
-  // Halves in turn: while one is multiplied the next one's fragments are
-  // read.  The barrier between a stage's halves says that the next stage has
-  // landed and that this one has been read by every wave, so its place can
-  // take the stage after the next.
+  // While one step is multiplied the next one's fragments are read.  The
+  // barrier before a stage's last step says that the next stage has landed and
+  // that this one has been read by every wave, so its place can take the stage
+  // after the next.  Its loads go out in three parts, a step apart: all at
+  // once they would hold the waves up, one after the other.
   Frags f0, f1;
-  Scales sc;
-  issue(0, 0);
+  Scales sc0, sc1;
+#pragma unroll
+  for (int j = 0; j < nAll; ++j) load(0, 0, j);
+#pragma unroll
+  for (int j = 0; j < nAll / 3; ++j) load(1, 1, j);
   wait_vmcnt<0>();
   lds_barrier();
-  issue(1, 1);
-  read_scales(sc, 0);
+  read_scales(sc0, 0);
   read(f0, 0, 0);
-  for (int s = 0, c = 0; s < steps; ++s, c ^= 1) {
-    read(f1, c, 1);
-    multiply(f0, sc, std::integral_constant<int, 0>{});
-    interleave(TN + TM);
+  auto stage = [&](int s, auto slot_c, auto other_c, const Scales &sc, Scales &next) {
+    constexpr int p = decltype(slot_c)::value;
+    asm("" : "+v"(x_lane), "+v"(w_lane), "+v"(sx_lane), "+v"(sw_lane));
+    read(f1, p, 1);
+    multiply(f0, sc, c0, other_c, s + 1, n1c, n2c);
+    read(f0, p, 2);
+    multiply(f1, sc, c1, other_c, s + 1, n2c, n3c);
+    read(f1, p, 3);
+    multiply(f0, sc, c2, slot_c, 0, n0c, n0c);
     wait_vmcnt<0>();
     lds_barrier();
-    issue(c, s + 2);
-    Scales next;
-    read(f0, c ^ 1, 0);
-    read_scales(next, c ^ 1);
-    multiply(f1, sc, std::integral_constant<int, 1>{});
-    interleave(2 * (TN + TM));
-    sc = next;
+    read(f0, p ^ 1, 0);
+    read_scales(next, s + 1);
+    multiply(f1, sc, c3, slot_c, s + 2, n0c, n1c);
+  };
+  for (int s = 0; s < steps; s += 2) {
+    stage(s, c0, c1, sc0, sc1);
+    if (s + 1 < steps) stage(s + 1, c1, c0, sc1, sc0);
   }
-  wait_vmcnt<0>();   // the loads past the end land before the LDS is handed on
+  wait_vmcnt<0>();   // the loads past the end land before the LDS is used again
 
-  store_tile<TN, TM, BOUT>(a.y, a.M, a.N, m0 + 16 * TM * wm, n0 + 16 * TN * wn, acc);
+  // Stores: lane (c, h) has row c of each 32 activation rows.
+  const int64_t m1 = m0 + 32 * TM * wm + r, n1 = n0 + 32 * TN * wn + 16 * h;
+  if constexpr (KG > 1) {
+    // the groups' sums, in their order; group i takes the tiles i, i + KG ..
+    f32x16 *part = reinterpret_cast<f32x16 *>(smem0) + (wv * 64 + lane);
+    constexpr int kPart = NW * 64;
+    static_assert(TM * TN * kPart * 64 <= L::bytes, "the sums fit");
+    lds_barrier();
+#pragma unroll
+    for (int t = 0; t < TM * TN; ++t) part[(kg * TM * TN + t) * kPart] = acc[t / TN][t % TN];
+    lds_barrier();
+    for (int t = kg; t < TM * TN; t += KG) {
+      f32x16 sum = part[t * kPart];
+#pragma unroll
+      for (int i = 1; i < KG; ++i) sum += part[(i * TM * TN + t) * kPart];
+      const int64_t m = m1 + 32 * (t / TN);
+      if (m < a.M) store_16<BOUT>(a.y, m, n1 + 32 * (t % TN), a.N, sum);
+    }
+  } else {
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm)
+      if (m1 + 32 * tm < a.M) {
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) store_16<BOUT>(a.y, m1 + 32 * tm, n1 + 32 * tn, a.N, acc[tm][tn]);
+      }
+  }
 }
 
-template <int TN, int TM, bool AL, bool BOUT>
+template <int KG, int NW, int WN, int TN, int TM, bool S16, bool BOUT>
 hipError_t go(TileArgs a, hipStream_t st) {
-  constexpr int lds = 2 * stage_bytes<32 * TN, 32 * TM, AL>();
-  a.tiles_m = static_cast<int>((a.M + 32 * TM - 1) / (32 * TM));
-  a.tiles = a.tiles_m * static_cast<int>((a.N + 32 * TN - 1) / (32 * TN));
-  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(mx_tiled_w4a4<TN, TM, AL, BOUT>),
+  constexpr int BN = 32 * WN * TN, BM = 32 * (NW / WN) * TM, lds = KG * Lds<BN, BM>::bytes;
+  a.tiles_m = static_cast<int>((a.M + BM - 1) / BM);
+  a.tiles_n = static_cast<int>((a.N + BN - 1) / BN);
+  const int tiles = a.tiles_m * a.tiles_n;
+  const auto kernel = mx_tiled_w4a4<KG, NW, WN, TN, TM, S16, BOUT>;
+  static const hipError_t set = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (set != hipSuccess) return set;
-  mx_tiled_w4a4<TN, TM, AL, BOUT><<<static_cast<unsigned>(a.tiles), kThreads, lds, st>>>(a);
+  kernel<<<static_cast<unsigned>(tiles), 64 * NW * KG, lds, st>>>(a);
   return hipGetLastError();
 }
 
-template <bool AL, bool BOUT>
+// The smallest tile whose grid the CUs take at once, its K shared out among
+// the waves (a workgroup's time is its stages' latencies then); past that
+// 128 x 128, two workgroups a CU, and 256 x 256 once those fill three quarters
+// of the CUs.  Microseconds on 256 CUs, smaller tile | larger tile:
+//   N 2048 K 5632: 32 x 64 at 256 rows (9.4 | 10.6), 64 x 64 at 512 (11.4 | 15.0)
+//   N 13312 K 2048: 64 x 64 at 64 rows (6.6 | 7.4), 128 x 128 at 512 (14.4 |
+//     19.1), 256 x 256 at 1024 (24.6 | 22.3)
+template <bool S16, bool BOUT>
 hipError_t pick(const TileArgs &a, hipStream_t st) {
-  auto tiles = [&](int64_t bn, int64_t bm) { return ((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm); };
-  if (tiles(256, 256) >= 192) return go<8, 8, AL, BOUT>(a, st);
-  return go<4, 4, AL, BOUT>(a, st);
+  const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (tiles(32, 64) <= cus) return go<4, 2, 2, 1, 1, false, BOUT>(a, st);
+  if (tiles(64, 64) <= cus) return go<2, 4, 2, 1, 1, false, BOUT>(a, st);
+  if (4 * tiles(256, 256) >= 3 * cus) return go<1, 8, 2, 4, 2, S16, BOUT>(a, st);
+  return go<1, 4, 2, 2, 2, S16, BOUT>(a, st);
 }
 
 }  // namespace
 
 // Ranges of the tiles' buffers in 30 bits, tile counts in 31.
 bool mx_tiled_w4a4_ok(int64_t M, int64_t N, int64_t K) {
-  return K <= (int64_t(1) << 22) && ((M + 127) / 128) * ((N + 127) / 128) < (int64_t(1) << 30);
+  return K <= (int64_t(1) << 22) && ((M + 31) / 32) * ((N + 31) / 32) < (int64_t(1) << 30);
 }
 
 hipError_t launch_mx_tiled_w4a4(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, void *y,
                                 bool y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t st) {
   const TileArgs a = {xq, sx, wq, sw, y, M, N, static_cast<int>((K + 31) / 32), 0, 0};
-  const auto at4 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; };
-  const bool al = a.KB % 4 == 0 && at4(sx) && at4(sw);
-  if (al) return y_bf16 ? pick<true, true>(a, st) : pick<true, false>(a, st);
+  const auto at16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  if (a.KB % 16 == 0 && at16(sx) && at16(sw)) return y_bf16 ? pick<true, true>(a, st) : pick<true, false>(a, st);
   return y_bf16 ? pick<false, true>(a, st) : pick<false, false>(a, st);
 }
 

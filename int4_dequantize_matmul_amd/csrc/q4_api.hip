@@ -664,12 +664,18 @@ bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>
 // Up to this many rows the dynamic call forms the activations' codes inside
 // the product.
 constexpr int64_t kMxFusedMaxM = 16;
-// Up to this many rows a product runs by blocks of 16 weight rows.
-constexpr int64_t kMxDecodeM = 64, kMxDecodeM16 = 16;
+// Up to this many rows a product runs by blocks of 16 weight rows.  W4A4 with
+// few weight rows, to 64 (blocks | tiles, us): N 2048 K 2048 5.3 | 5.8, K 5632
+// 32 rows 6.4 | 8.6; N 4096 K 1000 4.2 | 4.8; but N 13312 K 2048 32 rows 9.3 | 5.9.
+constexpr int64_t kMxDecodeM = 16;
+int64_t mx_decode_w4a4(int64_t N) {
+  const int64_t m = (int64_t(1) << 18) / N;
+  return m < kMxDecodeM ? kMxDecodeM : m < 64 ? m : 64;
+}
 
 q4_status w4a4_mx_launch(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, void *y,
                          int yt, int64_t M, int64_t N, int64_t K, hipStream_t st) {
-  if (route(q4::mx_tiled_w4a4_ok(M, N, K), true, M, kMxDecodeM) == Q4_PATH_TILED)
+  if (route(q4::mx_tiled_w4a4_ok(M, N, K), true, M, mx_decode_w4a4(N)) == Q4_PATH_TILED)
     return finish(q4::launch_mx_tiled_w4a4(xq, sx, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_TILED);
   return finish(q4::launch_mx_gemv_w4a4(xq, sx, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_GEMV);
 }
@@ -757,7 +763,7 @@ extern "C" q4_status q4_linear_w4a16_mx(const uint16_t *x_bf16, const uint8_t *w
   if (!device_ok()) return Q4_EDEVICE;
   hipStream_t st = S(stream);
   if (K == 0) return finish(q4::launch_zero(y, u(M) * u(N) * size_of(yt), st), Q4_PATH_GENERIC);
-  if (route(q4::mx_tiled_w4a16_ok(M, N, K), true, M, kMxDecodeM16) == Q4_PATH_TILED)
+  if (route(q4::mx_tiled_w4a16_ok(M, N, K), true, M, kMxDecodeM) == Q4_PATH_TILED)
     return finish(q4::launch_mx_tiled_w4a16(x_bf16, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_TILED);
   return finish(q4::launch_mx_gemv_w4a16(x_bf16, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_GEMV);
 }
