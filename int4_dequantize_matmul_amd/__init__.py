@@ -112,8 +112,10 @@ def _check(fn: str, st: int):
         raise Q4Error(fn, st)
 
 
-def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+def _stream(t: torch.Tensor) -> int:
+    """Handle of the current stream of t's device (the call behind
+    torch.cuda.current_stream, without its Stream object: 0.1 us, not 2)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 _DUMMY = {}
@@ -126,13 +128,13 @@ def _ptr(t):
     if t is None:
         return None
     if isinstance(t, np.ndarray):
-        return ctypes.c_void_p(t.ctypes.data)
+        return t.ctypes.data
     if t.numel() == 0:
         d = _DUMMY.get(t.device)
         if d is None:
             d = _DUMMY[t.device] = torch.empty(64, dtype=torch.uint8, device=t.device)
-        return ctypes.c_void_p(d.data_ptr())
-    return ctypes.c_void_p(t.data_ptr())
+        return d.data_ptr()
+    return t.data_ptr()
 
 
 def _dev(t: torch.Tensor, name: str, dtypes, ndim: int):
@@ -380,7 +382,7 @@ def w4a8_problems(items):
     (the tensors must outlive every call that uses the array)."""
     arr = (W4A8Problem * max(len(items), 1))()
     for i, (x, wq, sw, y) in enumerate(items):
-        arr[i] = W4A8Problem(_ptr(x).value, _ptr(wq).value, _ptr(sw).value, _ptr(y).value,
+        arr[i] = W4A8Problem(_ptr(x), _ptr(wq), _ptr(sw), _ptr(y),
                              wq.shape[0], x.shape[1])
     return arr
 
@@ -435,6 +437,7 @@ def q8_linear_w8a8(xq, sx, wq, sw, y=None):
 
 _DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 _FLOATS = (torch.float32, torch.bfloat16)
+_BYTES = (torch.uint8,)
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -443,27 +446,27 @@ def _dt(t: torch.Tensor) -> int:
 
 def _mx(codes, scales, name: str) -> int:
     """Checks a pair of MX FP4 arrays; returns their blocks per row."""
-    _dev(codes, name, (torch.uint8,), 2)
-    _dev(scales, f"{name}'s scales", (torch.uint8,), 2)
+    _dev(codes, name, _BYTES, 2)
+    _dev(scales, f"{name}'s scales", _BYTES, 2)
     rows, blocks = scales.shape
-    if codes.shape[0] != rows or codes.shape[1] != 16 * blocks:
+    if codes.shape != (rows, 16 * blocks):
         raise ValueError(f"{name} has shape {tuple(codes.shape)}, expected {(rows, 16 * blocks)} for scales of "
                          f"shape {(rows, blocks)}")
-    if codes.device != scales.device:
-        raise ValueError(f"{name} and its scales are on different devices")
+    _same_device(codes, scales)
     return blocks
 
 
 def _same_device(*tensors):
+    first = tensors[0].get_device()
     for t in tensors[1:]:
-        if t.device != tensors[0].device:
+        if t.get_device() != first:
             raise ValueError(f"tensors on different devices: {tensors[0].device} and {t.device}")
 
 
 def _out(y, M: int, N: int, dtype: str, like: torch.Tensor):
     """The output tensor: y if given (checked), else a new one."""
     if y is None:
-        return torch.empty((M, N), dtype=_DTYPES[dtype], device=like.device)
+        return torch.empty(M, N, dtype=_DTYPES[dtype], device=like.device)
     _dev(y, "y", (_DTYPES[dtype],), 2)
     if y.shape != (M, N):
         raise ValueError(f"y has shape {tuple(y.shape)}, expected {(M, N)}")
@@ -476,11 +479,12 @@ def q4_mx_quantize_rows(x: torch.Tensor):
     _dev(x, "x", _FLOATS, 2)
     M, K = x.shape
     B = (K + 31) // 32
-    codes = torch.empty((M, 16 * B), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((M, B), dtype=torch.uint8, device=x.device)
+    dev = x.device
+    codes = torch.empty(M, 16 * B, dtype=torch.uint8, device=dev)
+    scales = torch.empty(M, B, dtype=torch.uint8, device=dev)
     if M and K:
-        _check("q4_mx_quantize_rows", _lib().q4_mx_quantize_rows(_ptr(x), _dt(x), M, K, _ptr(codes), _ptr(scales),
-                                                                 _stream(x)))
+        _check("q4_mx_quantize_rows", _lib().q4_mx_quantize_rows(x.data_ptr(), _dt(x), M, K, codes.data_ptr(),
+                                                                 scales.data_ptr(), _stream(x)))
     return codes, scales
 
 
@@ -493,8 +497,8 @@ def q4_mx_dequantize_rows(codes, scales, K: int | None = None, dtype: str = "f32
         raise ValueError(f"K = {K} has {(K + 31) // 32} blocks, the scales have {B}")
     y = _out(y, M, K, dtype, codes)
     if M and K:
-        _check("q4_mx_dequantize_rows", _lib().q4_mx_dequantize_rows(_ptr(codes), _ptr(scales), M, K, _ptr(y),
-                                                                     DT[dtype], _stream(codes)))
+        _check("q4_mx_dequantize_rows", _lib().q4_mx_dequantize_rows(codes.data_ptr(), scales.data_ptr(), M, K,
+                                                                     y.data_ptr(), DT[dtype], _stream(codes)))
     return y
 
 
@@ -524,17 +528,33 @@ def _mx_weights(x, wq, sw):
     return x.shape[0], wq.shape[0], K
 
 
+#: Scratch for calls that need one and leave it untouched, one a device.
+_UNUSED = {}
+
+
+def _unused(n: int, device) -> torch.Tensor:
+    t = _UNUSED.get(device)
+    if t is None or t.numel() < n:
+        t = _UNUSED[device] = torch.empty(n, dtype=torch.uint8, device=device)
+    return t
+
+
 def q4_linear_w4a4_mx_dynamic(x, wq, sw, dtype: str = "bf16", ws=None, y=None):
     """f32 or bf16 x [M, K], quantized in the call, times MX FP4 weights -> y [M, N] in dtype."""
     _dev(x, "x", _FLOATS, 2)
     M, N, K = _mx_weights(x, wq, sw)
     y = _out(y, M, N, dtype, x)
     if M and N:
+        lib = _lib()
         if ws is None:
-            ws = torch.empty(q4_w4a4_mx_dynamic_workspace(M, K), dtype=torch.uint8, device=x.device)
+            need = lib.q4_w4a4_mx_dynamic_workspace(M, K)
+            if M <= 16 and lib.q4_get_path() != PATHS["tiled"]:   # the codes are formed in the product
+                ws = _unused(max(need, 256), x.device)
+            else:
+                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
         _check("q4_linear_w4a4_mx_dynamic",
-               _lib().q4_linear_w4a4_mx_dynamic(_ptr(x), _dt(x), _ptr(wq), _ptr(sw), _ptr(y), DT[dtype], M, N, K,
-                                                _ptr(ws), ws.numel() * ws.element_size(), _stream(x)))
+               lib.q4_linear_w4a4_mx_dynamic(_ptr(x), _dt(x), _ptr(wq), _ptr(sw), _ptr(y), DT[dtype], M, N, K,
+                                             _ptr(ws), ws.numel() * ws.element_size(), _stream(x)))
     return y
 
 
@@ -598,16 +618,19 @@ def q4_qk_norm_rope(q, k, q_gain, k_gain, positions, cos_sin, eps: float = 1e-6,
                 raise TypeError("q_gain and k_gain differ in dtype")
             gt = g.dtype
     out = q.dtype if dtype is None else _DTYPES[dtype]
-    qo = torch.empty((T, Hq, D), dtype=out, device=q.device)
-    ko = None if k is None else torch.empty((T, Hk, D), dtype=out, device=q.device)
+    qo = torch.empty(T, Hq, D, dtype=out, device=q.device)
+    ko = None if k is None else torch.empty(T, Hk, D, dtype=out, device=q.device)
     if T == 0 or Hq + Hk == 0:
         return qo, ko
-    k_token, k_head = (k.stride(0), k.stride(1)) if Hk else (0, 0)
+    q_token, q_head, _ = q.stride()
+    k_token, k_head, _ = k.stride() if Hk else (0, 0, 0)
     _check("q4_qk_norm_rope",
-           _lib().q4_qk_norm_rope(_ptr(q), q.stride(0), q.stride(1), _ptr(k), k_token, k_head, _dt(q), _ptr(q_gain),
-                                  _ptr(k_gain), 1 if gt == torch.bfloat16 else 0, _ptr(positions), _ptr(cos_sin),
-                                  _ptr(qo), _ptr(ko), 1 if out == torch.bfloat16 else 0, T, Hq, Hk, D,
-                                  cos_sin.shape[1], cos_sin.shape[0], eps, ROPE_PAIRS[pairs], _stream(q)))
+           _lib().q4_qk_norm_rope(_ptr(q), q_token, q_head, _ptr(k), k_token, k_head, _dt(q),
+                                  None if q_gain is None else q_gain.data_ptr(),
+                                  None if k_gain is None else k_gain.data_ptr(), 1 if gt == torch.bfloat16 else 0,
+                                  positions.data_ptr(), _ptr(cos_sin), _ptr(qo), _ptr(ko),
+                                  1 if out == torch.bfloat16 else 0, T, Hq, Hk, D, cos_sin.shape[1],
+                                  cos_sin.shape[0], eps, ROPE_PAIRS[pairs], _stream(q)))
     return qo, ko
 
 
