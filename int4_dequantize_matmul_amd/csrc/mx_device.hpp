@@ -161,6 +161,13 @@ __device__ __forceinline__ f32x16 mfma_mx_32x32x64(uint4 a, uint4 b, f32x16 c, u
                                                          static_cast<int>(sb));
 }
 
+// acc += A B over 16 columns of 32 rows: lane (r, h) has 8 columns of row r;
+// results as above.
+__device__ __forceinline__ f32x16 mfma_bf16_32x32x16(uint4 a, uint4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                 0, 0);
+}
+
 // float32 -> bf16 pairs, round to nearest even, NaN kept.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};

@@ -273,103 +273,127 @@ __global__ __launch_bounds__(64 * NW * KG, NW * KG == 4 ? 2 : NW * KG / 4) void 
   tile_body<KG, NW, WN, TN, TM, XAL, SB, BOUT>(a, static_cast<int64_t>(at.m) * BM, static_cast<int64_t>(at.n) * BN);
 }
 
-// Large products, two workgroups a CU: three stages of both operands, one
-// barrier a stage.  Weights go to LDS in rows of 32 bytes, a stage's two
-// blocks; otherwise as above.
+// Large products, 32 x 32 x 16 instructions, two workgroups a CU: two stages of
+// activations, two pairs of stages of weights, one barrier a stage.
 template <int BN, int BM, int SB>
 struct LargeLds {
-  static constexpr int x = 0, w = BM * 128, stage = w + BN * 32;
-  static constexpr int s = 3 * stage, s_buf = BN * SB, bytes = s + 2 * s_buf;
+  static constexpr int x_stage = BM * 128, w = 2 * x_stage, w_pair = BN * 64;
+  static constexpr int s = w + 2 * w_pair, s_buf = BN * SB, bytes = s + 2 * s_buf;
 };
 
 template <int TN, int TM, int SB, bool BOUT>
 __device__ __forceinline__ void large_body(const TileArgs &a, int64_t m0, int64_t n0) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int BN = 64 * TN, BM = 16 * TM;
+  constexpr int BN = 128 * TN, BM = 32 * TM;
   using L = LargeLds<BN, BM, SB>;
-  constexpr int nX = BM / 32, nW = BN / 128;   // loads of a wave in a stage
-  static_assert(nW * 128 == BN && nX * 32 == BM, "whole loads");
+  constexpr int nX = BM / 32, nW = BN / 64;   // loads of a wave: activations in a stage, weights in a pair
+  static_assert(nX % 2 == 0, "a wave's loads begin at 16 rows");
 
   const int rows_m = min(static_cast<int>(a.M - m0), BM), rows_n = min(static_cast<int>(a.N - n0), BN);
   const int K = a.K, KB = a.KB, steps = (K + 63) >> 6;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, g = lane >> 4;
+  const int r = lane & 31, h = lane >> 5;
 
   const __amdgpu_buffer_rsrc_t rs_x = rsrc(a.x + m0 * K, rows_m * 2 * K);
   const __amdgpu_buffer_rsrc_t rs_w = rsrc(a.w + n0 * KB * 16, rows_n * KB * 16);
   const __amdgpu_buffer_rsrc_t rs_s = rsrc(a.sw + n0 * KB, rows_n * KB);
   const uint32_t lds0 = lds_addr(smem);
 
-  auto row_of = [](int t, int i) { return 32 * (t >> 1) + w_row<BOUT>(t & 1, i); };
+  // LDS row i of the weights is row w_row32(i % 32) of its 32.  Activations:
+  // lane i at row i / 8, position i % 8, which holds chunk (i % 8) ^ (row / 2 %
+  // 8).  Weights: row i / 4, position i % 4, which holds block (i % 4) ^ (row /
+  // 4 % 4).  Either way 16 rows have a chunk in the 16 different places that
+  // one clock reads.
   const int c_x = (lane & 7) ^ (lane >> 4), x_row0 = 8 * nX * wv + (lane >> 3);   // chunk c_x in even loads
-  // lane i: row i / 2 of 32, position i % 2, which holds block
-  // (i % 2) ^ (row / 8 % 2): 16 rows have a block in 16 different places
-  const int c_w = (lane & 1) ^ ((lane >> 4) & 1), w_row0 = row_of(lane >> 5, (lane >> 1) & 15) * KB;
-  auto issue = [&](int slot, int s) {
-    const uint32_t st = lds0 + slot * L::stage;
-    if ((s & (SB / 2 - 1)) == 0 && wv < BN / 64) {
-      const int b = 2 * s, o = b < KB ? row_of(4 * wv + g, r) * KB + b : kFar;
-      const uint32_t to = lds0 + L::s + ((s / (SB / 2)) & 1) * L::s_buf;
-      if constexpr (SB == 16) dma16(rs_s, to + wv * 1024, o, 0);
-      else dma4(rs_s, to + wv * 256, o, 0);
-    }
-    const int b = 2 * s + c_w;
-    static_assert(nX % 2 == 0, "a wave's loads begin at 16 rows");
+  const int c_w = (lane & 3) ^ (lane >> 4);
+  auto issue_x = [&](int s) {
 #pragma unroll
     for (int j = 0; j < nX; ++j) {
       const int k = 64 * s + 8 * (c_x ^ (4 * (j & 1)));
-      dma16(rs_x, st + (nX * wv + j) * 1024, k < K ? ((x_row0 + 8 * j) * K + k) * 2 : kFar, 0);
+      dma16(rs_x, lds0 + (s & 1) * L::x_stage + (nX * wv + j) * 1024, k < K ? ((x_row0 + 8 * j) * K + k) * 2 : kFar, 0);
     }
+  };
+  auto issue_w = [&](int d) {   // pair d
+    const int b = 4 * d + c_w;
 #pragma unroll
     for (int j = 0; j < nW; ++j) {
-      const int l = nW * wv + j;
-      dma16(rs_w, st + L::w + l * 1024, b < KB ? (w_row0 + 32 * l * KB + b) * 16 : kFar, 0);
+      const int i = 16 * (nW * wv + j), row = (i & ~31) + w_row32((i & 31) + (lane >> 2));
+      dma16(rs_w, lds0 + L::w + (d & 1) * L::w_pair + i * 64, b < KB ? (row * KB + b) * 16 : kFar, 0);
+    }
+  };
+  auto issue_s = [&](int d) {   // the scales of pair d and (SB = 16) the three after it
+    if (wv < BN / 64) {
+      const int b = 4 * d, o = b < KB ? (64 * wv + 32 * h + w_row32(r)) * KB + b : kFar;
+      const uint32_t to = lds0 + L::s + ((SB == 16 ? d >> 2 : d) & 1) * L::s_buf;
+      if constexpr (SB == 16) dma16(rs_s, to + wv * 1024, o, 0);
+      else dma4(rs_s, to + wv * 256, o, 0);
     }
   };
 
-  f32x4 acc[TM][TN] = {};
-  const int w_base = L::w + TN * wv * 512 + r * 32 + (((g >> 1) ^ (r >> 3)) << 4) + (g & 1) * 8;
-  const int s_base = L::s + (TN * wv * 16 + r) * SB + (g >> 1);
-  const int pos[2] = {((2 * g) ^ (r >> 1)) << 4, ((2 * g + 1) ^ (r >> 1)) << 4};
-  auto compute = [&](int slot, int s) {
-    const uint8_t *st = smem + slot * L::stage;
-    const uint8_t *sc = smem + s_base + ((s / (SB / 2)) & 1) * L::s_buf + 2 * (s & (SB / 2 - 1));
-    uint2 c[TN];
+  // In instruction j of a stage's four lane (r, h) has columns 32 h + 8 j .. of
+  // row r: a dword of its block h.
+  f32x16 acc[TM][TN] = {};
+  const int w_base = L::w + TN * wv * 2048 + r * 64, s_base = L::s + (32 * TN * wv + r) * SB;
+  auto compute = [&](int s, auto odd_c) {
+    constexpr int ODD = decltype(odd_c)::value;
+    const int d = s >> 1, blk = 2 * ODD + h;
+    const uint8_t *st = smem + ODD * L::x_stage + r * 128;
+    const uint8_t *sw = smem + w_base + (d & 1) * L::w_pair + ((blk ^ ((r >> 2) & 3)) << 4);
+    const uint8_t *sc = smem + s_base + (SB == 16 ? ((d >> 2) & 1) * L::s_buf + 4 * (d & 3) : (d & 1) * L::s_buf) + blk;
+    uint32_t c[TN][4];
     float scale[TN];
-    uint4 x[2][TM];
+    uint4 x[4][TM];
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
-      c[t] = *reinterpret_cast<const uint2 *>(st + w_base + t * 512);
-      scale[t] = mx_scale(sc[t * 16 * SB]);
+      const uint4 v = load16(sw + t * 2048);
+      c[t][0] = v.x, c[t][1] = v.y, c[t][2] = v.z, c[t][3] = v.w;
+      scale[t] = mx_scale(sc[t * 32 * SB]);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int t = 0; t < TM; ++t) x[j][t] = load16(st + r * 128 + pos[j] + t * 2048);
+      for (int t = 0; t < TM; ++t) x[j][t] = load16(st + (((4 * h + j) ^ ((r >> 1) & 7)) << 4) + t * 4096);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn) {
-        const uint4 wf = mx_decode8_bf16(j ? c[tn].y : c[tn].x, scale[tn]);
+        const uint4 wf = mx_decode8_bf16(c[tn][j], scale[tn]);
 #pragma unroll
-        for (int tm = 0; tm < TM; ++tm) acc[tm][tn] = mfma_bf16_16x16x32(wf, x[j][tm], acc[tm][tn]);
+        for (int tm = 0; tm < TM; ++tm) acc[tm][tn] = mfma_bf16_32x32x16(wf, x[j][tm], acc[tm][tn]);
       }
   };
 
-  // Stage s is read in step s; the barrier before it says that the stage has
-  // landed and that the one read in step s - 1 is free.
-  issue(0, 0);
-  issue(1, 1);
-  for (int s = 0, c = 0; s < steps; ++s) {
-    wait_vmcnt<nX + nW>();   // all but the loads of stage s + 1
+  // The barrier before step s says that stage s has landed and that stage
+  // s - 1 has been read, so its place can take stage s + 1; after even ones
+  // pair s / 2 + 1 takes the place of the pair before s's.
+  issue_s(0);
+  issue_w(0);
+  issue_x(0);
+  for (int s = 0; s < steps; s += 2) {
+    wait_vmcnt<0>();
     lds_barrier();
-    issue(c == 0 ? 2 : c - 1, s + 2);
-    compute(c, s);
-    c = c == 2 ? 0 : c + 1;
+    const int d = s / 2 + 1;
+    if (SB != 16 || (d & 3) == 0) issue_s(d);
+    issue_x(s + 1);
+    issue_w(d);
+    compute(s, std::integral_constant<int, 0>{});
+    if (s + 1 < steps) {
+      wait_vmcnt<nW>();   // all but the weights of the next pair
+      lds_barrier();
+      issue_x(s + 2);
+      compute(s + 1, std::integral_constant<int, 1>{});
+    }
   }
   wait_vmcnt<0>();   // the loads past the end land before the LDS is handed on
-  store_tile<TN, TM, BOUT>(a.y, a.M, a.N, m0, n0 + 16 * TN * wv, acc);
+  // lane (c, h) has row c of each 32 activation rows
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm)
+    if (m0 + 32 * tm + r < a.M) {
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+        store_16<BOUT>(a.y, m0 + 32 * tm + r, n0 + 32 * (TN * wv + tn) + 16 * h, a.N, acc[tm][tn]);
+    }
 }
 
 // Whole tiles of 128 x 256, and the last ones in quarters.
@@ -378,14 +402,14 @@ __global__ __launch_bounds__(256, 2) void mx_large_w4a16(TileArgs a) {
   const int id = static_cast<int>(blockIdx.x);
   if (id < a.whole) {
     const TileAt at = tile_at(xcd_run(id, a.whole), a.tiles_m, a.tiles_n);
-    large_body<4, 8, SB, BOUT>(a, 128 * static_cast<int64_t>(at.m), 256 * static_cast<int64_t>(at.n));
+    large_body<2, 4, SB, BOUT>(a, 128 * static_cast<int64_t>(at.m), 256 * static_cast<int64_t>(at.n));
   } else {
     const int q = xcd_run(id - a.whole, static_cast<int>(gridDim.x) - a.whole);
     const TileAt at = tile_at(a.whole + (q >> 2), a.tiles_m, a.tiles_n);
     const int64_t m0 = 128 * static_cast<int64_t>(at.m) + 64 * (q & 1);
     const int64_t n0 = 256 * static_cast<int64_t>(at.n) + 128 * ((q >> 1) & 1);
     if (m0 >= a.M || n0 >= a.N) return;   // the whole workgroup
-    large_body<2, 4, SB, BOUT>(a, m0, n0);
+    large_body<1, 2, SB, BOUT>(a, m0, n0);
   }
 }
 
