@@ -3,15 +3,17 @@
 //   w4a4:  y[m,n] = sum_b 2^(sx[m,b] + sw[n,b] - 254) sum_{k in b} cx[m,k] cw[n,k]
 //   w4a16: y[m,n] = sum_k x[m,k] cw[n,k] 2^(sw[n,k/32] - 127)
 //
-// Bound: the weights' bytes from memory (17 per block of 32).  A workgroup
-// has 16 weight rows and its four waves share out K in steps of 512 columns.
-// In a step lane (r, g) holds the four blocks 4 g .. 4 g + 3 of row r: 64
-// consecutive bytes of codes and one dword of scales, so the wave reads 256
-// consecutive bytes of each row, and the matrix instruction picks the block's
-// scale byte out of the dword.  A matrix instruction sums over whatever
-// columns its lanes hold, so the four calls on blocks 4 g + j (j = 0..3) cover
-// the step once.  The waves' sums meet in LDS in wave order: a row's result
-// does not depend on the batch.
+// Bound: the weights' bytes from memory (17 per block of 32), and the latency
+// of one round of loads.  A workgroup has 16 weight rows and its four waves
+// share out K in steps of 512 columns.  In a step lane (r, g) holds the four
+// blocks 4 j + g (j = 0..3) of row r, so that a load's four lanes of a row read
+// 64 bytes side by side, and the row's 16 scales, of which byte g of dword j is
+// block 4 j + g's.  A matrix instruction sums over whatever columns its lanes
+// hold, so the four calls on blocks 4 j + g cover the step once.  All loads of
+// a step are under way before the first is used; lanes of rows past the batch
+// load no activations (their columns of the result are not stored).  The
+// waves' sums meet in LDS in wave order: a row's result does not depend on the
+// batch.
 #include "kernels.hpp"
 #include "mx_device.hpp"
 
@@ -29,11 +31,11 @@ struct GemvArgs {
   int KB;
 };
 
-// One lane's four blocks of a row, and their scale bytes; blocks past KB are
-// zeros under 2^-127.
+// One lane's four blocks of a row, and the scale of each in byte 0 of s[j];
+// blocks past KB are zeros under 2^-127.
 struct Frag {
   uint4 c[4];
-  uint32_t s;
+  uint32_t s[4];
 };
 
 template <bool STREAM>
@@ -46,51 +48,65 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *p) {
   }
 }
 
+// The row's blocks from b0 on (16 of them if whole).
 template <bool STREAM>
-__device__ __forceinline__ Frag load_frag(const uint8_t *row, const uint8_t *srow, int b0, int KB, bool whole) {
+__device__ __forceinline__ Frag load_frag(const uint8_t *row, const uint8_t *srow, int b0, int g, int KB, bool whole) {
   Frag f;
   if (whole) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f.c[j] = load_codes<STREAM>(row + static_cast<int64_t>(b0 + j) * 16);
-    f.s = load_any<uint32_t>(srow + b0);
+    for (int j = 0; j < 4; ++j) f.c[j] = load_codes<STREAM>(row + static_cast<int64_t>(b0 + 4 * j + g) * 16);
+    const uint4 s = load_any<uint4>(srow + b0);
+    f.s[0] = s.x >> (8 * g), f.s[1] = s.y >> (8 * g), f.s[2] = s.z >> (8 * g), f.s[3] = s.w >> (8 * g);
   } else {
-    f.s = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      const int b = b0 + 4 * j + g;
       f.c[j] = make_uint4(0, 0, 0, 0);
-      if (b0 + j < KB) {
-        f.c[j] = load_codes<STREAM>(row + static_cast<int64_t>(b0 + j) * 16);
-        f.s |= static_cast<uint32_t>(srow[b0 + j]) << (8 * j);
+      f.s[j] = 0;
+      if (b < KB) {
+        f.c[j] = load_codes<STREAM>(row + static_cast<int64_t>(b) * 16);
+        f.s[j] = srow[b];
       }
     }
   }
   return f;
 }
 
-// The same four blocks quantized here from a float row (the quantizer's
-// recipe: same codes, same scale bytes).
+// The lane's 128 activations of a step: run i of block 4 j + g in v[4 j + i].
 template <bool BF16>
-__device__ __forceinline__ Frag quantize_frag(const void *x, int64_t row0, int b0, int64_t K) {
+struct Step {
+  Run8<BF16> v[16];
+  __device__ __forceinline__ void load(const void *x, int64_t row, int64_t k0, int g, int64_t K, bool whole, bool live) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i].zero();
+    if (!live) return;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i].load(x, row + k0 + 32 * (4 * (i >> 2) + g) + 8 * (i & 3));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int64_t k = k0 + 32 * (4 * (i >> 2) + g) + 8 * (i & 3);
+        if (k + 8 <= K) v[i].load(x, row + k);
+        else if (k < K) v[i].load_part(x, row + k, static_cast<int>(K - k));
+      }
+    }
+  }
+};
+
+// A step's blocks quantized here (the quantizer's recipe: same codes, same
+// scale bytes).
+template <bool BF16>
+__device__ __forceinline__ Frag quantize_step(const Step<BF16> &x) {
   Frag f;
-  f.s = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    Run8<BF16> v[4];
-    const int64_t k = 32 * static_cast<int64_t>(b0 + j);
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t ki = k + 8 * i;
-      if (ki + 8 <= K) v[i].load(x, row0 + ki);
-      else if (ki < K) v[i].load_part(x, row0 + ki, static_cast<int>(K - ki));
-      else v[i].zero();
-      top = max(top, v[i].top());
-    }
-    const uint32_t byte = mx_scale_byte(top);
+    const Run8<BF16> *v = x.v + 4 * j;
+    const uint32_t byte = mx_scale_byte(max(max(v[0].top(), v[1].top()), max(v[2].top(), v[3].top())));
     const float s = mx_scale(byte);
     f.c[j] = make_uint4(v[0].encode(s), v[1].encode(s), v[2].encode(s), v[3].encode(s));
     if (byte == 255) f.c[j] = make_uint4(0, 0, 0, 0);
-    f.s |= byte << (8 * j);
+    f.s[j] = byte;
   }
   return f;
 }
@@ -124,59 +140,53 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a4(GemvArgs a) {
   const int steps = (a.KB + 15) / 16;
   f32x4 acc[MT] = {};
   for (int s = wave; s < steps; s += kWaves) {
-    const int b0 = 16 * s + 4 * g;
-    const bool whole = 16 * s + 16 <= a.KB;
-    const Frag wf = load_frag<true>(wrow, srow, b0, a.KB, whole);
+    const int b0 = 16 * s;
+    const bool whole = b0 + 16 <= a.KB;
+    const Frag wf = load_frag<true>(wrow, srow, b0, g, a.KB, whole);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int64_t m = min(m0 + 16 * t + r, a.M - 1);
       Frag xf;
-      if constexpr (XT == kPacked)
-        xf = load_frag<false>(static_cast<const uint8_t *>(a.x) + m * a.KB * 16, a.sx + m * a.KB, b0, a.KB, whole);
-      else
-        xf = quantize_frag<XT == kBf16>(a.x, m * a.K, b0, a.K);
-      acc[t] = mfma_mx_16x16x128<0>(wf.c[0], xf.c[0], acc[t], wf.s, xf.s);
-      acc[t] = mfma_mx_16x16x128<1>(wf.c[1], xf.c[1], acc[t], wf.s, xf.s);
-      acc[t] = mfma_mx_16x16x128<2>(wf.c[2], xf.c[2], acc[t], wf.s, xf.s);
-      acc[t] = mfma_mx_16x16x128<3>(wf.c[3], xf.c[3], acc[t], wf.s, xf.s);
+      if constexpr (XT == kPacked) {
+        xf = load_frag<false>(static_cast<const uint8_t *>(a.x) + m * a.KB * 16, a.sx + m * a.KB, b0, g, a.KB, whole);
+      } else {
+        Step<XT == kBf16> x;
+        x.load(a.x, m * a.K, 32 * static_cast<int64_t>(b0), g, a.K, 32 * static_cast<int64_t>(b0) + 512 <= a.K,
+               m0 + 16 * t + r < a.M);
+        xf = quantize_step(x);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[t] = mfma_mx_16x16x128<0>(wf.c[j], xf.c[j], acc[t], wf.s[j], xf.s[j]);
     }
   }
   join_and_store<MT, BOUT>(a, acc, m0, n0);
 }
 
-template <int MT, bool BOUT>
+template <bool BOUT>
 __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a16(GemvArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t n0 = 16 * static_cast<int64_t>(blockIdx.x), m0 = 16 * MT * static_cast<int64_t>(blockIdx.y);
-  const int64_t n = min(n0 + r, a.N - 1);
+  const int64_t n0 = 16 * static_cast<int64_t>(blockIdx.x), m0 = 16 * static_cast<int64_t>(blockIdx.y);
+  const int64_t n = min(n0 + r, a.N - 1), m = min(m0 + r, a.M - 1);
   const uint8_t *wrow = a.w + n * a.KB * 16, *srow = a.sw + n * a.KB;
   const int steps = (a.KB + 15) / 16;
-  f32x4 acc[MT] = {};
+  f32x4 acc[1] = {};
   for (int s = wave; s < steps; s += kWaves) {
-    const int b0 = 16 * s + 4 * g;
     const bool whole = 512 * static_cast<int64_t>(s) + 512 <= a.K;
-    const Frag wf = load_frag<true>(wrow, srow, b0, a.KB, whole);
+    const Frag wf = load_frag<true>(wrow, srow, 16 * s, g, a.KB, whole);
+    Step<true> x;
+    x.load(a.x, m * a.K, 512 * static_cast<int64_t>(s), g, a.K, whole, m0 + r < a.M);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float sc = mx_scale((wf.s >> (8 * j)) & 255u);
+      const float sc = mx_scale(wf.s[j] & 255u);
       const uint32_t c[4] = {wf.c[j].x, wf.c[j].y, wf.c[j].z, wf.c[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 wv = mx_decode8_bf16(c[i], sc);
-        const int64_t k = 32 * static_cast<int64_t>(b0 + j) + 8 * i;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          const int64_t m = min(m0 + 16 * t + r, a.M - 1);
-          Run8<true> xv;
-          if (whole || k + 8 <= a.K) xv.load(a.x, m * a.K + k);
-          else if (k < a.K) xv.load_part(a.x, m * a.K + k, static_cast<int>(a.K - k));
-          else xv.zero();
-          acc[t] = mfma_bf16_16x16x32(wv, make_uint4(xv.v[0], xv.v[1], xv.v[2], xv.v[3]), acc[t]);
-        }
+        const uint32_t *v = x.v[4 * j + i].v;
+        acc[0] = mfma_bf16_16x16x32(mx_decode8_bf16(c[i], sc), make_uint4(v[0], v[1], v[2], v[3]), acc[0]);
       }
     }
   }
-  join_and_store<MT, BOUT>(a, acc, m0, n0);
+  join_and_store<1, BOUT>(a, acc, m0, n0);
 }
 
 template <int MT>
@@ -188,12 +198,6 @@ template <int MT, int XT>
 void run_w4a4(const GemvArgs &a, bool y_bf16, hipStream_t st) {
   if (y_bf16) mx_gemv_w4a4<MT, XT, true><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
   else mx_gemv_w4a4<MT, XT, false><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
-}
-
-template <int MT>
-void run_w4a16(const GemvArgs &a, bool y_bf16, hipStream_t st) {
-  if (y_bf16) mx_gemv_w4a16<MT, true><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
-  else mx_gemv_w4a16<MT, false><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
 }
 
 }  // namespace
@@ -218,9 +222,8 @@ hipError_t launch_mx_gemv_w4a4_fused(const void *x, bool x_bf16, const uint8_t *
 hipError_t launch_mx_gemv_w4a16(const uint16_t *x, const uint8_t *wq, const uint8_t *sw, void *y, bool y_bf16,
                                 int64_t M, int64_t N, int64_t K, hipStream_t st) {
   const GemvArgs a = {x, nullptr, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32)};
-  if (M <= 16) run_w4a16<1>(a, y_bf16, st);
-  else if (M <= 32) run_w4a16<2>(a, y_bf16, st);
-  else run_w4a16<4>(a, y_bf16, st);
+  if (y_bf16) mx_gemv_w4a16<true><<<grid_of<1>(a), 64 * kWaves, 0, st>>>(a);
+  else mx_gemv_w4a16<false><<<grid_of<1>(a), 64 * kWaves, 0, st>>>(a);
   return hipGetLastError();
 }
 

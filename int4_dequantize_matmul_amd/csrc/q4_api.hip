@@ -664,13 +664,20 @@ bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>
 // Up to this many rows the dynamic call forms the activations' codes inside
 // the product.
 constexpr int64_t kMxFusedMaxM = 16;
-// Up to this many rows a product runs by blocks of 16 weight rows.  W4A4 with
-// few weight rows, to 64 (blocks | tiles, us): N 2048 K 2048 5.3 | 5.8, K 5632
-// 32 rows 6.4 | 8.6; N 4096 K 1000 4.2 | 4.8; but N 13312 K 2048 32 rows 9.3 | 5.9.
-constexpr int64_t kMxDecodeM = 16;
+// Up to this many rows a product of N weight rows runs by blocks of 16 weight
+// rows, which reads the activations again for each block (blocks | tiles, us):
+// W4A4: N 2048 K 2048, 64 rows 4.9 | 5.8; K 5632, 32 rows 6.0 | 8.6; N 4096
+//   K 1003, 64 rows 3.8 | 4.8; N 13312 K 2048, 32 rows 8.3 | 5.9.
+// W4A16: N 2048 K 5632, 32 rows 8.8 | 13.3, 64 rows 15.0 | 13.5; K 2048, 64
+//   rows 6.8 | 7.4; N 4096 K 1003, 32 rows 6.8 | 6.9; N 13312 K 2048, 4 rows
+//   7.2 | 7.9, 16 rows 11.1 | 7.9.
 int64_t mx_decode_w4a4(int64_t N) {
   const int64_t m = (int64_t(1) << 18) / N;
-  return m < kMxDecodeM ? kMxDecodeM : m < 64 ? m : 64;
+  return m < 16 ? 16 : m < 64 ? m : 64;
+}
+int64_t mx_decode_w4a16(int64_t N) {
+  const int64_t m = (int64_t(1) << 17) / N;
+  return m < 4 ? 4 : m;
 }
 
 q4_status w4a4_mx_launch(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, void *y,
@@ -763,7 +770,7 @@ extern "C" q4_status q4_linear_w4a16_mx(const uint16_t *x_bf16, const uint8_t *w
   if (!device_ok()) return Q4_EDEVICE;
   hipStream_t st = S(stream);
   if (K == 0) return finish(q4::launch_zero(y, u(M) * u(N) * size_of(yt), st), Q4_PATH_GENERIC);
-  if (route(q4::mx_tiled_w4a16_ok(M, N, K), true, M, kMxDecodeM) == Q4_PATH_TILED)
+  if (route(q4::mx_tiled_w4a16_ok(M, N, K), true, M, mx_decode_w4a16(N)) == Q4_PATH_TILED)
     return finish(q4::launch_mx_tiled_w4a16(x_bf16, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_TILED);
   return finish(q4::launch_mx_gemv_w4a16(x_bf16, wq, sw, y, yt == Q4_DT_BF16, M, N, K, st), Q4_PATH_GEMV);
 }
