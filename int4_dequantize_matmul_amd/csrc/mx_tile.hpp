@@ -101,4 +101,59 @@ __device__ __forceinline__ void store_16(void *y, int64_t m, int64_t n, int64_t 
   }
 }
 
+// Stores of a wave's 32 TM rows by 32 TN columns of 32 x 32 results, in whole
+// lines past the caches: through LDS of the wave's own (64 TM TN 32 bytes),
+// half of the columns at a time if they are f32.  A lane's own 16 columns would
+// be 16-byte pieces of as many lines, which have to meet in L2 and are written
+// back from there when the kernel ends.
+template <int TM, int TN, bool BOUT>
+__device__ __forceinline__ void store_lines(uint8_t *lds, void *y, int64_t M, int64_t N, int64_t m0, int64_t n0,
+                                            const f32x16 (&acc)[TM][TN]) {
+  constexpr int PASSES = BOUT ? 1 : 2, T = TN / PASSES;         // column tiles of a pass
+  constexpr int W = T * 32 * (BOUT ? 2 : 4), C = W / 16, PER = BOUT ? 8 : 4;
+  static_assert(C == 8 || C == 16, "rows of 128 or 256 bytes");
+  typedef uint32_t U __attribute__((ext_vector_type(4), aligned(2)));
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  auto place = [](int row, int q) { return row * W + ((q ^ (C == 16 ? row & 15 : (row >> 1) & 7)) << 4); };
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const f32x16 &v = acc[tm][p * T + t];
+#pragma unroll
+        for (int j = 0; j < 16; j += PER) {
+          uint4 u;
+          if constexpr (BOUT)
+            u = make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]), pack_bf16(v[j + 4], v[j + 5]),
+                           pack_bf16(v[j + 6], v[j + 7]));
+          else
+            u = make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                           __float_as_uint(v[j + 3]));
+          *reinterpret_cast<uint4 *>(lds + place(32 * tm + r, (32 * t + 16 * h + j) / PER)) = u;
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 32 * TM * C / 64; ++i) {
+      const int row = i * (64 / C) + lane / C, q = lane % C;
+      const uint4 u = load16(lds + place(row, q));
+      const int64_t m = m0 + row, n = n0 + p * T * 32 + q * PER;
+      if (m >= M) continue;
+      if (n + PER <= N) {
+        uint8_t *to = static_cast<uint8_t *>(y) + (m * N + n) * (BOUT ? 2 : 4);
+        __builtin_nontemporal_store(__builtin_bit_cast(U, u), reinterpret_cast<U *>(to));
+      } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < PER - 1; ++j)
+          if (n + j < N) {
+            if constexpr (BOUT) static_cast<uint16_t *>(y)[m * N + n + j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+            else static_cast<uint32_t *>(y)[m * N + n + j] = w[j];
+          }
+      }
+    }
+  }
+}
+
 }  // namespace q4

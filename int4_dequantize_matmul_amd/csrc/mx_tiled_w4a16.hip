@@ -386,14 +386,16 @@ __device__ __forceinline__ void large_body(const TileArgs &a, int64_t m0, int64_
     }
   }
   wait_vmcnt<0>();   // the loads past the end land before the LDS is handed on
-  // lane (c, h) has row c of each 32 activation rows
+  if constexpr (TN > 1) {
+    static_assert(4 * 64 * TM * TN * 32 <= L::bytes, "the waves' results fit");
+    lds_barrier();
+    store_lines<TM, TN, BOUT>(smem + wv * (64 * TM * TN * 32), a.y, a.M, a.N, m0, n0 + 32 * TN * wv, acc);
+  } else {
+    // lane (c, h) has row c of each 32 activation rows
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm)
-    if (m0 + 32 * tm + r < a.M) {
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn)
-        store_16<BOUT>(a.y, m0 + 32 * tm + r, n0 + 32 * (TN * wv + tn) + 16 * h, a.N, acc[tm][tn]);
-    }
+    for (int tm = 0; tm < TM; ++tm)
+      if (m0 + 32 * tm + r < a.M) store_16<BOUT>(a.y, m0 + 32 * tm + r, n0 + 32 * wv + 16 * h, a.N, acc[tm][0]);
+  }
 }
 
 // Whole tiles of 128 x 256, and the last ones in quarters.

@@ -256,6 +256,9 @@ __global__ __launch_bounds__(64 * NW * KG, NW * KG <= 4 ? 2 : NW * KG / 4) void 
       const int64_t m = m1 + 32 * (t / TN);
       if (m < a.M) store_16<BOUT>(a.y, m, n1 + 32 * (t % TN), a.N, sum);
     }
+  } else if constexpr (BN == 256) {
+    lds_barrier();
+    store_lines<TM, TN, BOUT>(smem + wv * (64 * TM * TN * 32), a.y, a.M, a.N, m0 + 32 * TM * wm, n0 + 32 * TN * wn, acc);
   } else {
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm)
