@@ -3,7 +3,10 @@
 Argument marshalling only: every function calls the C entry point of the same
 name in ``lib/libq4.so`` (declared in ``include/q4.h``); all arithmetic runs
 in that library's host code or HIP kernels.  torch provides device memory and
-the current stream; outputs are allocated here with torch.
+the current stream; outputs are allocated here with torch.  The MX FP4 and
+query/key calls, whose small sizes cost more here than on the GPU, go through
+``lib/q4_torch.so`` first, which does the same in C++ (a call of 6 to 11 us
+takes about 4).
 
 The library must be built first (``python -m int4_dequantize_matmul_amd.build``);
 importing the compute functions without it raises, there is no fallback.
@@ -11,6 +14,8 @@ importing the compute functions without it raises, there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import numpy as np
@@ -100,6 +105,28 @@ def _lib():
             f.argtypes = args
         _LIB = lib
     return _LIB
+
+
+TORCH_LIB_PATH = os.path.join(_PKG, "lib", "q4_torch.so")
+_DIRECT = None
+
+
+def _direct():
+    """lib/q4_torch.so, bound to the entry points of the library in use.  Its
+    functions return None for arguments that they do not take as they are;
+    the functions here then check them, and say what is wrong."""
+    global _DIRECT
+    if _DIRECT is None:
+        if not os.path.exists(TORCH_LIB_PATH):
+            raise RuntimeError(f"{TORCH_LIB_PATH} is not built: run `python -m int4_dequantize_matmul_amd.build`")
+        loader = importlib.machinery.ExtensionFileLoader("q4_torch", TORCH_LIB_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("q4_torch", loader))
+        loader.exec_module(m)
+        lib = _lib()
+        m.bind(torch._C._cuda_getCurrentRawStream,
+               {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _SIG if "_mx" in n or "_qk_" in n})
+        _DIRECT = m
+    return _DIRECT
 
 
 def raw():
@@ -476,6 +503,9 @@ def _out(y, M: int, N: int, dtype: str, like: torch.Tensor):
 
 def q4_mx_quantize_rows(x: torch.Tensor):
     """f32 or bf16 rows [M, K] -> (codes uint8 [M, 16 ceil(K/32)], scales uint8 [M, ceil(K/32)])."""
+    out = _direct().quantize_rows(x)
+    if out is not None:
+        return out
     _dev(x, "x", _FLOATS, 2)
     M, K = x.shape
     B = (K + 31) // 32
@@ -490,6 +520,10 @@ def q4_mx_quantize_rows(x: torch.Tensor):
 
 def q4_mx_dequantize_rows(codes, scales, K: int | None = None, dtype: str = "f32", y=None):
     """Codes and scales -> the numbers they stand for, [M, K] (K: 32 a block if not given)."""
+    if y is None and K is not None:
+        y = _direct().dequantize_rows(codes, scales, K, DT[dtype])
+        if y is not None:
+            return y
     B = _mx(codes, scales, "codes")
     M = codes.shape[0]
     K = 32 * B if K is None else K
@@ -504,6 +538,10 @@ def q4_mx_dequantize_rows(codes, scales, K: int | None = None, dtype: str = "f32
 
 def q4_linear_w4a4_mx(xq, sx, wq, sw, dtype: str = "bf16", y=None):
     """MX FP4 rows xq, sx [M, ...] times MX FP4 weights wq, sw [N, ...] -> y [M, N] in dtype."""
+    if y is None:
+        y = _direct().w4a4(xq, sx, wq, sw, DT[dtype])
+        if y is not None:
+            return y
     B = _mx(xq, sx, "xq")
     if _mx(wq, sw, "wq") != B:
         raise ValueError(f"xq has {B} blocks a row, wq {sw.shape[1]}")
@@ -528,38 +566,30 @@ def _mx_weights(x, wq, sw):
     return x.shape[0], wq.shape[0], K
 
 
-#: Scratch for calls that need one and leave it untouched, one a device.
-_UNUSED = {}
-
-
-def _unused(n: int, device) -> torch.Tensor:
-    t = _UNUSED.get(device)
-    if t is None or t.numel() < n:
-        t = _UNUSED[device] = torch.empty(n, dtype=torch.uint8, device=device)
-    return t
-
-
 def q4_linear_w4a4_mx_dynamic(x, wq, sw, dtype: str = "bf16", ws=None, y=None):
     """f32 or bf16 x [M, K], quantized in the call, times MX FP4 weights -> y [M, N] in dtype."""
+    if ws is None and y is None:
+        y = _direct().w4a4_dynamic(x, wq, sw, DT[dtype])
+        if y is not None:
+            return y
     _dev(x, "x", _FLOATS, 2)
     M, N, K = _mx_weights(x, wq, sw)
     y = _out(y, M, N, dtype, x)
     if M and N:
-        lib = _lib()
         if ws is None:
-            need = lib.q4_w4a4_mx_dynamic_workspace(M, K)
-            if M <= 16 and lib.q4_get_path() != PATHS["tiled"]:   # the codes are formed in the product
-                ws = _unused(max(need, 256), x.device)
-            else:
-                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+            ws = torch.empty(q4_w4a4_mx_dynamic_workspace(M, K), dtype=torch.uint8, device=x.device)
         _check("q4_linear_w4a4_mx_dynamic",
-               lib.q4_linear_w4a4_mx_dynamic(_ptr(x), _dt(x), _ptr(wq), _ptr(sw), _ptr(y), DT[dtype], M, N, K,
-                                             _ptr(ws), ws.numel() * ws.element_size(), _stream(x)))
+               _lib().q4_linear_w4a4_mx_dynamic(_ptr(x), _dt(x), _ptr(wq), _ptr(sw), _ptr(y), DT[dtype], M, N, K,
+                                                _ptr(ws), ws.numel() * ws.element_size(), _stream(x)))
     return y
 
 
 def q4_linear_w4a16_mx(x, wq, sw, dtype: str = "bf16", y=None):
     """bf16 x [M, K] times MX FP4 weights -> y [M, N] in dtype."""
+    if y is None:
+        y = _direct().w4a16(x, wq, sw, DT[dtype])
+        if y is not None:
+            return y
     _dev(x, "x", (torch.bfloat16,), 2)
     M, N, K = _mx_weights(x, wq, sw)
     y = _out(y, M, N, dtype, x)
@@ -591,6 +621,10 @@ def q4_qk_norm_rope(q, k, q_gain, k_gain, positions, cos_sin, eps: float = 1e-6,
     slices of a fused projection as they are; gains [D] or None; positions
     int64 [T]; cos_sin f32 [P, R] -> (q_out, k_out or None) in dtype (default:
     q's)."""
+    out = _direct().qk_norm_rope(q, k, q_gain, k_gain, positions, cos_sin, eps, ROPE_PAIRS[pairs],
+                                 -1 if dtype is None else DT[dtype])
+    if out is not None:
+        return out
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [tokens, heads, D]")
     T, Hq, D = q.shape

@@ -21,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libq4.so")
+TORCH_LIB = os.path.join(LIBDIR, "q4_torch.so")      # the Python binding's small-call path
 PROBE_LIB = os.path.join(LIBDIR, "libq4_probe.so")   # the benchmark's ceilings (not the linear)
 BUILD = os.path.join(PKG, "_build")
 ARCH = "gfx950"
@@ -42,6 +43,19 @@ def _run(cmd):
     return out
 
 
+def _torch_binding(out: str) -> list:
+    """The compile of csrc/binding/q4_torch.cpp against the installed torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    return ["g++", *CXX_FLAGS, "-Wno-unused-parameter", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-isystem{i}" for i in inc), "-shared", "-o", out, os.path.join(CSRC, "binding", "q4_torch.cpp"),
+            f"-L{os.path.join(root, 'lib')}", "-lc10", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source and link lib/libq4.so; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -53,11 +67,13 @@ def build(verbose: bool = False) -> str:
     for src in sorted(glob.glob(os.path.join(CSRC, "*.cpp"))):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         jobs.append(["g++", *CXX_FLAGS, "-c", src, "-o", obj])
+    objs = [j[-1] for j in jobs]
+    jobs.append(_torch_binding(TORCH_LIB + ".tmp"))
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         for out in ex.map(_run, jobs):
             if verbose and out.strip():
                 print(out)
-    objs = [j[-1] for j in jobs]
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
     tmp = LIB + ".tmp"
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, LIB)
