@@ -73,9 +73,8 @@ __device__ __forceinline__ Frag load_frag(const uint8_t *row, const uint8_t *sro
 }
 
 // The lane's 128 activations of a step: run i of block 4 j + g in v[4 j + i].
-template <bool BF16>
 struct Step {
-  Run8<BF16> v[16];
+  Run8<true> v[16];
   __device__ __forceinline__ void load(const void *x, int64_t row, int64_t k0, int g, int64_t K, bool whole, bool live) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i].zero();
@@ -95,19 +94,55 @@ struct Step {
 };
 
 // A step's blocks quantized here (the quantizer's recipe: same codes, same
-// scale bytes).
-template <bool BF16>
-__device__ __forceinline__ Frag quantize_step(const Step<BF16> &x) {
+// scale bytes), a row at a time by the whole wave: lane l forms the codes of
+// columns 8 l .. 8 l + 7, and the lanes' blocks meet in LDS of the wave's own.
+// (Each lane quantizing its own 128 columns, most of them of rows that are not
+// there, took 3 us of a call with one row.)
+constexpr int kCodeRow = 272;   // bytes of a row of codes: 16 rows begin 16 bytes apart, modulo 256
+struct StepLds {
+  uint8_t codes[16 * kCodeRow], scales[16 * 16];
+};
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xF, 0xF, false)));
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, false)));
+}
+
+// R rows at a time, without a branch among them: past the last one it is
+// formed again, in a place that nothing reads.
+template <bool BF16, int R>
+__device__ __forceinline__ Frag quantize_step(const void *x, int64_t row0, int64_t k0, int64_t K, int rows, StepLds &lds) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int64_t k = k0 + 8 * lane;
+  for (int m = 0; m < rows; m += R) {
+    Run8<BF16> v[R];
+    if (k + 8 <= K) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) v[i].load(x, row0 + min(m + i, rows - 1) * K + k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) v[i].load_part(x, row0 + min(m + i, rows - 1) * K + k, static_cast<int>(K - k));
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const uint32_t byte = mx_scale_byte(quad_max(v[i].top()));
+      const uint32_t code = byte == 255 ? 0u : v[i].encode(mx_scale(byte));
+      *reinterpret_cast<uint32_t *>(lds.codes + (m + i) * kCodeRow + 4 * lane) = code;
+      if ((lane & 3) == 0) lds.scales[(m + i) * 16 + (lane >> 2)] = static_cast<uint8_t>(byte);
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   Frag f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const Run8<BF16> *v = x.v + 4 * j;
-    const uint32_t byte = mx_scale_byte(max(max(v[0].top(), v[1].top()), max(v[2].top(), v[3].top())));
-    const float s = mx_scale(byte);
-    f.c[j] = make_uint4(v[0].encode(s), v[1].encode(s), v[2].encode(s), v[3].encode(s));
-    if (byte == 255) f.c[j] = make_uint4(0, 0, 0, 0);
-    f.s[j] = byte;
+    f.c[j] = make_uint4(0, 0, 0, 0);
+    f.s[j] = 0;
+    if (r < rows) {
+      f.c[j] = load16(lds.codes + r * kCodeRow + (4 * j + g) * 16);
+      f.s[j] = lds.scales[r * 16 + 4 * j + g];
+    }
   }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   return f;
 }
 
@@ -131,7 +166,7 @@ __device__ __forceinline__ void join_and_store(const GemvArgs &a, f32x4 (&acc)[M
 
 enum XType { kPacked = 0, kF32 = 1, kBf16 = 2 };
 
-template <int MT, int XT, bool BOUT>
+template <int MT, int XT, bool BOUT, int R>
 __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a4(GemvArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int64_t n0 = 16 * static_cast<int64_t>(blockIdx.x), m0 = 16 * MT * static_cast<int64_t>(blockIdx.y);
@@ -145,15 +180,15 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a4(GemvArgs a) {
     const Frag wf = load_frag<true>(wrow, srow, b0, g, a.KB, whole);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const int64_t m = min(m0 + 16 * t + r, a.M - 1);
       Frag xf;
       if constexpr (XT == kPacked) {
+        const int64_t m = min(m0 + 16 * t + r, a.M - 1);
         xf = load_frag<false>(static_cast<const uint8_t *>(a.x) + m * a.KB * 16, a.sx + m * a.KB, b0, g, a.KB, whole);
       } else {
-        Step<XT == kBf16> x;
-        x.load(a.x, m * a.K, 32 * static_cast<int64_t>(b0), g, a.K, 32 * static_cast<int64_t>(b0) + 512 <= a.K,
-               m0 + 16 * t + r < a.M);
-        xf = quantize_step(x);
+        __shared__ __align__(16) StepLds lds[kWaves];
+        const int64_t m = m0 + 16 * t;
+        xf = quantize_step<XT == kBf16, R>(a.x, m * a.K, 32 * static_cast<int64_t>(b0), a.K,
+                                        static_cast<int>(min(a.M - m, static_cast<int64_t>(16))), lds[wave]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[t] = mfma_mx_16x16x128<0>(wf.c[j], xf.c[j], acc[t], wf.s[j], xf.s[j]);
@@ -173,7 +208,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a16(GemvArgs a) {
   for (int s = wave; s < steps; s += kWaves) {
     const bool whole = 512 * static_cast<int64_t>(s) + 512 <= a.K;
     const Frag wf = load_frag<true>(wrow, srow, 16 * s, g, a.KB, whole);
-    Step<true> x;
+    Step x;
     x.load(a.x, m * a.K, 512 * static_cast<int64_t>(s), g, a.K, whole, m0 + r < a.M);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -194,10 +229,18 @@ dim3 grid_of(const GemvArgs &a) {
   return dim3(static_cast<unsigned>((a.N + 15) / 16), static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)));
 }
 
-template <int MT, int XT>
+// R: rows that the kernel quantizes at a time
+template <int MT, int XT, int R = 1>
 void run_w4a4(const GemvArgs &a, bool y_bf16, hipStream_t st) {
-  if (y_bf16) mx_gemv_w4a4<MT, XT, true><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
-  else mx_gemv_w4a4<MT, XT, false><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
+  if (y_bf16) mx_gemv_w4a4<MT, XT, true, R><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
+  else mx_gemv_w4a4<MT, XT, false, R><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
+}
+
+template <int XT>
+void run_w4a4_fused(const GemvArgs &a, bool y_bf16, hipStream_t st) {
+  if (a.M == 1) run_w4a4<1, XT, 1>(a, y_bf16, st);
+  else if (a.M <= 4) run_w4a4<1, XT, 4>(a, y_bf16, st);
+  else run_w4a4<1, XT, 8>(a, y_bf16, st);
 }
 
 }  // namespace
@@ -214,8 +257,8 @@ hipError_t launch_mx_gemv_w4a4(const uint8_t *xq, const uint8_t *sx, const uint8
 hipError_t launch_mx_gemv_w4a4_fused(const void *x, bool x_bf16, const uint8_t *wq, const uint8_t *sw, void *y,
                                      bool y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t st) {
   const GemvArgs a = {x, nullptr, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32)};
-  if (x_bf16) run_w4a4<1, kBf16>(a, y_bf16, st);
-  else run_w4a4<1, kF32>(a, y_bf16, st);
+  if (x_bf16) run_w4a4_fused<kBf16>(a, y_bf16, st);
+  else run_w4a4_fused<kF32>(a, y_bf16, st);
   return hipGetLastError();
 }
 
