@@ -10,9 +10,7 @@
 // 64 bytes side by side, and the row's 16 scales, of which byte g of dword j is
 // block 4 j + g's.  A matrix instruction sums over whatever columns its lanes
 // hold, so the four calls on blocks 4 j + g cover the step once.  All loads of
-// a step are under way before the first is used; lanes of rows past the batch
-// load no activations (their columns of the result are not stored).  The
-// waves' sums meet in LDS in wave order: a row's result does not depend on the
+// a step are under way before the first is used.  The waves' sums meet in LDS in wave order: a row's result does not depend on the
 // batch.
 #include "kernels.hpp"
 #include "mx_device.hpp"
@@ -71,27 +69,6 @@ __device__ __forceinline__ Frag load_frag(const uint8_t *row, const uint8_t *sro
   }
   return f;
 }
-
-// The lane's 128 activations of a step: run i of block 4 j + g in v[4 j + i].
-struct Step {
-  Run8<true> v[16];
-  __device__ __forceinline__ void load(const void *x, int64_t row, int64_t k0, int g, int64_t K, bool whole, bool live) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i].zero();
-    if (!live) return;
-    if (whole) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i].load(x, row + k0 + 32 * (4 * (i >> 2) + g) + 8 * (i & 3));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int64_t k = k0 + 32 * (4 * (i >> 2) + g) + 8 * (i & 3);
-        if (k + 8 <= K) v[i].load(x, row + k);
-        else if (k < K) v[i].load_part(x, row + k, static_cast<int>(K - k));
-      }
-    }
-  }
-};
 
 // A step's blocks quantized here (the quantizer's recipe: same codes, same
 // scale bytes), a row at a time by the whole wave: lane l forms the codes of
@@ -197,29 +174,48 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a4(GemvArgs a) {
   join_and_store<MT, BOUT>(a, acc, m0, n0);
 }
 
-template <bool BOUT>
+// W4A16.  A step's activations come 16 bytes a lane, a row a load, and reach
+// the lanes that multiply them through LDS of the wave's own: loaded as they
+// are needed, 64 bytes apart, they took as long as the weights.  R: rows that
+// there are places for.
+constexpr int kRunRow = 1024 + 16;   // bytes of a row in LDS: 16 rows begin 16 bytes apart, modulo 256
+
+template <bool BOUT, int R>
 __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a16(GemvArgs a) {
+  extern __shared__ __align__(16) uint8_t runs0[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int64_t n0 = 16 * static_cast<int64_t>(blockIdx.x), m0 = 16 * static_cast<int64_t>(blockIdx.y);
-  const int64_t n = min(n0 + r, a.N - 1), m = min(m0 + r, a.M - 1);
+  const int64_t n = min(n0 + r, a.N - 1);
+  const int rows = static_cast<int>(min(a.M - m0, static_cast<int64_t>(R)));
   const uint8_t *wrow = a.w + n * a.KB * 16, *srow = a.sw + n * a.KB;
   const int steps = (a.KB + 15) / 16;
+  uint8_t *runs = runs0 + wave * R * kRunRow;
+  const uint8_t *mine = runs + min(r, R - 1) * kRunRow + 64 * g;   // other lanes' columns of the result are not stored
   f32x4 acc[1] = {};
   for (int s = wave; s < steps; s += kWaves) {
-    const bool whole = 512 * static_cast<int64_t>(s) + 512 <= a.K;
-    const Frag wf = load_frag<true>(wrow, srow, 16 * s, g, a.KB, whole);
-    Step x;
-    x.load(a.x, m * a.K, 512 * static_cast<int64_t>(s), g, a.K, whole, m0 + r < a.M);
+    const int64_t k = 512 * static_cast<int64_t>(s) + 8 * lane;
+    const Frag wf = load_frag<true>(wrow, srow, 16 * s, g, a.KB, 16 * s + 16 <= a.KB);
+    Run8<true> x[R];
+    if (k + 8 <= a.K) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) x[i].load(a.x, (m0 + min(i, rows - 1)) * a.K + k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) x[i].load_part(a.x, (m0 + min(i, rows - 1)) * a.K + k, static_cast<int>(a.K - k));
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      *reinterpret_cast<uint4 *>(runs + i * kRunRow + 16 * lane) = make_uint4(x[i].v[0], x[i].v[1], x[i].v[2], x[i].v[3]);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float sc = mx_scale(wf.s[j] & 255u);
       const uint32_t c[4] = {wf.c[j].x, wf.c[j].y, wf.c[j].z, wf.c[j].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t *v = x.v[4 * j + i].v;
-        acc[0] = mfma_bf16_16x16x32(mx_decode8_bf16(c[i], sc), make_uint4(v[0], v[1], v[2], v[3]), acc[0]);
-      }
+      for (int i = 0; i < 4; ++i)
+        acc[0] = mfma_bf16_16x16x32(mx_decode8_bf16(c[i], sc), load16(mine + 256 * j + 16 * i), acc[0]);
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
   join_and_store<1, BOUT>(a, acc, m0, n0);
 }
@@ -241,6 +237,22 @@ void run_w4a4_fused(const GemvArgs &a, bool y_bf16, hipStream_t st) {
   if (a.M == 1) run_w4a4<1, XT, 1>(a, y_bf16, st);
   else if (a.M <= 4) run_w4a4<1, XT, 4>(a, y_bf16, st);
   else run_w4a4<1, XT, 8>(a, y_bf16, st);
+}
+
+template <int R>
+hipError_t run_w4a16(const GemvArgs &a, bool y_bf16, hipStream_t st) {
+  constexpr int lds = kWaves * R * kRunRow;
+  const auto kernel = y_bf16 ? mx_gemv_w4a16<true, R> : mx_gemv_w4a16<false, R>;
+  if constexpr (lds > 60 * 1024) {   // beside the sums
+    static const hipError_t set[2] = {
+        hipFuncSetAttribute(reinterpret_cast<const void *>(mx_gemv_w4a16<false, R>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, lds),
+        hipFuncSetAttribute(reinterpret_cast<const void *>(mx_gemv_w4a16<true, R>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, lds)};
+    if (set[y_bf16] != hipSuccess) return set[y_bf16];
+  }
+  kernel<<<grid_of<1>(a), 64 * kWaves, lds, st>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -265,9 +277,10 @@ hipError_t launch_mx_gemv_w4a4_fused(const void *x, bool x_bf16, const uint8_t *
 hipError_t launch_mx_gemv_w4a16(const uint16_t *x, const uint8_t *wq, const uint8_t *sw, void *y, bool y_bf16,
                                 int64_t M, int64_t N, int64_t K, hipStream_t st) {
   const GemvArgs a = {x, nullptr, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32)};
-  if (y_bf16) mx_gemv_w4a16<true><<<grid_of<1>(a), 64 * kWaves, 0, st>>>(a);
-  else mx_gemv_w4a16<false><<<grid_of<1>(a), 64 * kWaves, 0, st>>>(a);
-  return hipGetLastError();
+  if (M == 1) return run_w4a16<1>(a, y_bf16, st);
+  if (M <= 4) return run_w4a16<4>(a, y_bf16, st);
+  if (M <= 8) return run_w4a16<8>(a, y_bf16, st);
+  return run_w4a16<16>(a, y_bf16, st);
 }
 
 }  // namespace q4
