@@ -9,8 +9,8 @@
 // Bound: memory; every number is read and written once.  A head's row stays
 // in the registers of a group of L lanes (L a power of two): a lane has the
 // columns of whole pairs, so the rotation crosses no lanes, and the square
-// sum takes log2 L moves.  In units of V columns (16 bytes where sizes,
-// strides and addresses allow it, one column or one pair otherwise): halves,
+// sum takes log2 L moves.  In units of V columns (up to 16 bytes, as R and
+// D allow it): halves,
 // a unit is V columns of the first half with the V opposite ones; neighbours,
 // V columns that hold V / 2 pairs; past R a unit is V plain columns.  Rows of
 // more than 64 units take turns over them, and read their row a second time
@@ -23,37 +23,31 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// V numbers from element i on, at any address.
 template <bool BF16, int V>
 __device__ __forceinline__ void load_v(const void *p, int64_t i, float (&o)[V]) {
   if constexpr (BF16) {
     const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-    if constexpr (V == 8) {
-      const uint4 t = load16(q);
-      const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+    if constexpr (V == 1) {
+      o[0] = bf16_to_f32(q[0]);
+    } else {
+      typedef uint32_t W __attribute__((ext_vector_type(V / 2)));
+      const W w = load_any<W>(q);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < V / 2; ++j) {
         o[2 * j] = __uint_as_float(w[j] << 16);
         o[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
       }
-    } else if constexpr (V == 4) {
-      const uint2 t = *reinterpret_cast<const uint2 *>(q);
-      o[0] = __uint_as_float(t.x << 16), o[1] = __uint_as_float(t.x & 0xFFFF0000u);
-      o[2] = __uint_as_float(t.y << 16), o[3] = __uint_as_float(t.y & 0xFFFF0000u);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = bf16_to_f32(q[j]);
     }
   } else {
     const float *q = static_cast<const float *>(p) + i;
-    if constexpr (V % 4 == 0) {
+    constexpr int P = V < 4 ? V : 4;   // 16 bytes a load at most
+    typedef float W __attribute__((ext_vector_type(P)));
 #pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        const float4 t = *reinterpret_cast<const float4 *>(q + j);
-        o[j] = t.x, o[j + 1] = t.y, o[j + 2] = t.z, o[j + 3] = t.w;
-      }
-    } else {
+    for (int j = 0; j < V; j += P) {
+      const W w = load_any<W>(q + j);
 #pragma unroll
-      for (int j = 0; j < V; ++j) o[j] = q[j];
+      for (int l = 0; l < P; ++l) o[j + l] = w[l];
     }
   }
 }
@@ -62,33 +56,25 @@ template <bool BF16, int V>
 __device__ __forceinline__ void store_v(void *p, int64_t i, const float (&o)[V]) {
   if constexpr (BF16) {
     uint16_t *q = static_cast<uint16_t *>(p) + i;
-    if constexpr (V % 2 == 0) {
-      uint32_t w[V / 2];
+    if constexpr (V == 1) {
+      q[0] = static_cast<uint16_t>(pack_bf16(o[0], 0.0f));
+    } else {
+      typedef uint32_t W __attribute__((ext_vector_type(V / 2)));
+      W w;
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16(o[2 * j], o[2 * j + 1]);
-      if constexpr (V == 8) {
-        *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else if constexpr (V == 4) {
-        *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          q[2 * j] = static_cast<uint16_t>(w[j]);
-          q[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) q[j] = static_cast<uint16_t>(pack_bf16(o[j], 0.0f));
+      store_any(q, w);
     }
   } else {
     float *q = static_cast<float *>(p) + i;
-    if constexpr (V % 4 == 0) {
+    constexpr int P = V < 4 ? V : 4;
+    typedef float W __attribute__((ext_vector_type(P)));
 #pragma unroll
-      for (int j = 0; j < V; j += 4) *reinterpret_cast<float4 *>(q + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-    } else {
+    for (int j = 0; j < V; j += P) {
+      W w;
 #pragma unroll
-      for (int j = 0; j < V; ++j) q[j] = o[j];
+      for (int l = 0; l < P; ++l) w[l] = o[j + l];
+      store_any(q + j, w);
     }
   }
 }
@@ -211,20 +197,16 @@ void go(const QkArgs &a, hipStream_t st) {
       a, L, static_cast<int>(units));
 }
 
-bool mult(int64_t v, int64_t m) { return v % m == 0; }
-bool at16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 template <bool IB, bool OB, bool NB>
 void pick(const QkArgs &a, hipStream_t st) {
-  // 16 bytes of the wider type a unit: every row start, half and remainder
-  // has to be a multiple of it
-  constexpr int V = IB && OB ? 8 : 4, S = NB ? 2 : 1;
-  const int64_t half = NB ? a.R : a.R / 2;
-  const bool vec = mult(half, V) && mult(a.D - a.R, V) && mult(a.q_t, V) && mult(a.q_h, V) && mult(a.k_t, V) &&
-                   mult(a.k_h, V) && at16(a.q) && at16(a.k) && at16(a.qo) && at16(a.ko) && at16(a.wq) &&
-                   at16(a.wk) && at16(a.table) && mult(a.R / 2, 4);
-  if (vec) go<IB, OB, V, NB>(a, st);
-  else go<IB, OB, S, NB>(a, st);
+  // as many columns a unit, up to 16 bytes of the wider type, as divide the
+  // halves (or the pairs' columns) and the rest; rows may start anywhere
+  constexpr int most = IB && OB ? 8 : 4;
+  const int64_t n = (NB ? a.R : a.R / 2) | (a.D - a.R);
+  if (most == 8 && n % 8 == 0) go<IB, OB, most, NB>(a, st);
+  else if (n % 4 == 0) go<IB, OB, 4, NB>(a, st);
+  else if (NB || n % 2 == 0) go<IB, OB, 2, NB>(a, st);   // R and D are even
+  else go<IB, OB, NB ? 2 : 1, NB>(a, st);
 }
 
 }  // namespace
