@@ -45,6 +45,12 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
   return e == 255 ? 255u : static_cast<uint32_t>(max(e - 2, 0));
 }
 
+// The largest of four neighbouring lanes' values, in each of them.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xF, 0xF, false)));
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, false)));
+}
+
 // Two float32 values -> two codes in byte SEL of d: v / 2^(b - 127), rounded
 // to the nearest code, ties to even, beyond 6 to 6.
 template <int SEL>

@@ -12,6 +12,11 @@
 // hold, so the four calls on blocks 4 j + g cover the step once.  All loads of
 // a step are under way before the first is used.  The waves' sums meet in LDS in wave order: a row's result does not depend on the
 // batch.
+//
+// Measured, 13312 x 2048 weights (14.5 MB): W4A4, one row quantized in the call,
+// 4.9 us (3.0 TB/s), packed rows 4.7; W4A16, one row 5.0 to 5.7, 16 rows 8.1.
+// What is left over the weights' 2.8 us at a copy's rate is the launch and one
+// round of loads from memory.
 #include "kernels.hpp"
 #include "mx_device.hpp"
 
@@ -79,11 +84,6 @@ constexpr int kCodeRow = 272;   // bytes of a row of codes: 16 rows begin 16 byt
 struct StepLds {
   uint8_t codes[16 * kCodeRow], scales[16 * 16];
 };
-
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0xB1, 0xF, 0xF, false)));
-  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, false)));
-}
 
 // R rows at a time, without a branch among them: past the last one it is
 // formed again, in a place that nothing reads.

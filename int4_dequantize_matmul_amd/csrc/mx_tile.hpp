@@ -1,6 +1,5 @@
 // Parts that the LDS-tiled MX FP4 products share: the order of tiles, the
-// order of weight rows in the matrix instructions, and the stores.  Four waves
-// (2 x 2), each 16 TN weight rows by 16 TM activation rows.
+// order of weight rows in the matrix instructions, and the stores.
 #pragma once
 
 #include "mx_device.hpp"
@@ -38,7 +37,7 @@ __device__ __forceinline__ TileAt tile_at(int i, int tiles_m, int tiles_n) {
   return {__builtin_amdgcn_readfirstlane(8 * band + at % rows), __builtin_amdgcn_readfirstlane(at / rows)};
 }
 
-// Stores of a wave: lane (c, q) has row c of each 16 activation rows, from
+// Stores of a wave of 16 TM rows by 16 TN weight rows: lane (c, q) has row c of each 16 activation rows, from
 // row m0 and column n0 on.
 template <int TN, int TM, bool BOUT>
 __device__ __forceinline__ void store_tile(void *y, int64_t M, int64_t N, int64_t m0, int64_t n0,

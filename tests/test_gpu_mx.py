@@ -378,3 +378,57 @@ def test_streams_and_graph_replays():
         calls()
         for g, y in zip(got, ys):
             assert_bitwise(g, host(y), f"replay {seed}")
+
+
+class _NoDirect:
+    """In the place of the C++ path: takes nothing."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+@pytest.mark.parametrize("M,K", [(1, 2048), (3, 33), (20, 96), (70, 640)])
+def test_both_paths_of_the_binding_agree(M, K, monkeypatch):
+    """The calls through C++ and through ctypes give the same bits, types and shapes."""
+    N, T, D = 50, M, 64
+    gen = torch.Generator(DEV).manual_seed(M)
+    x = torch.randn(M, K, device=DEV, generator=gen)
+    wq, sw = (dev(a) for a in weights(M + K, N, K))
+    heads = torch.randn(T, 6, D, device=DEV, generator=gen)
+    gain, pos = torch.ones(D, device=DEV), torch.arange(T, device=DEV) % 5
+    cs = torch.randn(5, 32, device=DEV, generator=gen)
+
+    def calls():
+        xq, sx = q4.q4_mx_quantize_rows(x)
+        out = [xq, sx]
+        for dt in ("f32", "bf16"):
+            out += [q4.q4_mx_dequantize_rows(xq, sx, K, dt), q4.q4_linear_w4a4_mx(xq, sx, wq, sw, dt),
+                    q4.q4_linear_w4a4_mx_dynamic(x, wq, sw, dt), q4.q4_linear_w4a16_mx(x.bfloat16(), wq, sw, dt)]
+            for pairs in ("halves", "neighbours"):
+                out += q4.q4_qk_norm_rope(heads[:, :4], heads[:, 4:], gain, gain, pos, cs, 1e-5, pairs, dt)
+        return out
+
+    direct = calls()
+    monkeypatch.setattr(q4, "_direct", lambda: _NoDirect())
+    for a, b in zip(direct, calls()):
+        assert a.dtype == b.dtype and a.is_contiguous()
+        assert_bitwise(host(a), host(b))
+
+
+def test_the_direct_path_leaves_what_it_does_not_take():
+    d = q4._direct()
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device=DEV)
+    c, s = q4.q4_mx_quantize_rows(x)
+    for args in ((x.cpu(), c, s, 1), (x.half(), c, s, 1), (x.t(), c, s, 1), (x[:0], c, s, 1), (x, c, s[:, :1], 1),
+                 (x, c[:, ::2], s, 1), (x, c.int(), s, 1), (x, None, s, 1), (x, c, s), (1, 2, 3, 4)):
+        assert d.w4a16(*args) is None and d.w4a4_dynamic(*args) is None
+    assert d.dequantize_rows(c, s, 65, 0) is None and d.dequantize_rows(c, s, 32, 0) is None
+    assert d.dequantize_rows(c, s, 0, 0) is None and d.dequantize_rows(c, s, -5, 0) is None
+    assert d.w4a4(c, s, c[:, :16].contiguous(), s[:, :1].contiguous(), 0) is None
+    assert d.quantize_rows(x.double()) is None and d.quantize_rows([1.0]) is None
+    h, g, p, t = x.view(2, 1, 64), x[0], torch.zeros(2, dtype=torch.int64, device=DEV), torch.zeros(4, 64, device=DEV)
+    for args in ((h, h, g, g, p.int(), t, 1e-6, 0, -1), (h, None, g, g, p, t, 1e-6, 0, -1),
+                 (h, h.float(), g, g, p, t, 1e-6, 0, -1), (h, h, g[:32], g, p, t, 1e-6, 0, -1),
+                 (h, h, g, g, p[:1], t, 1e-6, 0, -1), (h.transpose(1, 2), h, g, g, p, t, 1e-6, 0, -1),
+                 (h, h, g, g, p, t[:, :7].contiguous(), 1e-6, 0, -1)):
+        assert d.qk_norm_rope(*args) is None
