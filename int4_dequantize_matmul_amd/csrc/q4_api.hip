@@ -666,17 +666,18 @@ bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>
 constexpr int64_t kMxFusedMaxM = 16;
 // Up to this many rows a product of N weight rows runs by blocks of 16 weight
 // rows, which reads the activations again for each block (blocks | tiles, us):
-// W4A4: N 2048 K 2048, 64 rows 4.9 | 5.8; K 5632, 32 rows 6.0 | 8.6; N 4096
-//   K 1003, 64 rows 3.8 | 4.8; N 13312 K 2048, 32 rows 8.3 | 5.9.
-// W4A16: N 2048 K 5632, 64 rows 8.8 | 13.4; K 2048, 64 rows 5.1 | 7.4; N 5631
-//   K 2048, 32 rows 7.1 | 7.8, 64 rows 11.2 | 8.0; N 13312 K 2048, 8 rows 6.3 |
-//   7.4, 16 rows 8.1 | 7.6; N 4096 K 1003, 16 rows 6.6 | 7.1, 32 rows 7.8 | 6.9.
+// W4A4: N 2048 K 2048, 128 rows 5.1 | 5.6, 192 rows 7.5 | 5.7; K 5632, 128 rows
+//   9.0 | 8.6; N 512 K 1024, 256 rows 3.6 | 4.5; N 4096 K 1003, 64 rows 3.7 |
+//   4.6; N 13312 K 2048, 32 rows 8.3 | 5.9.
+// W4A16 (512 workgroups are resident): N 2048 K 5632, 64 rows 9.0 | 13.2, 96
+//   rows 15.6 | 13.3; K 2048, 64 rows 5.0 | 7.4, 128 rows 8.1 | 7.5; N 512 K
+//   1024, 256 rows 4.0 | 5.6; N 13312 K 2048, 8 rows 6.3 | 7.4, 16 rows 8.1 | 7.6.
 int64_t mx_decode_w4a4(int64_t N) {
   const int64_t m = (int64_t(1) << 18) / N;
-  return m < 16 ? 16 : m < 64 ? m : 64;
+  return m < 16 ? 16 : m < 512 ? m : 512;
 }
 int64_t mx_decode_w4a16(int64_t N) {
-  const int64_t m = (int64_t(3) << 16) / N;
+  const int64_t m = (int64_t(1) << 17) / N;
   return m < 4 ? 4 : m;
 }
 

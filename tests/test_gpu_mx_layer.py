@@ -67,7 +67,7 @@ def test_prompts_do_not_see_each_other():
     both, caches = layer.prompt(torch.cat((a, b)), [7, 12])
     ya, (ca,) = layer.prompt(a, [7])
     yb, (cb,) = layer.prompt(b, [12])
-    # up to 64 rows these products do not depend on the batch, and every other step is by row
+    # products of so few weight rows do not depend on the batch, and every other step is by row
     for got, want in ((both[:7], ya), (both[7:], yb), (caches[0][0], ca[0]), (caches[1][1], cb[1])):
         assert torch.equal(got, want)
 
