@@ -116,7 +116,11 @@ struct Unit {
   }
 };
 
-template <bool IB, bool OB, int V, bool NEIGHBOURS>
+// EARLY: a unit a lane at most, and everything that the row needs under way
+// before its square sum (4096 tokens of 40 heads of 256, neighbours: 56 -> 38 us);
+// not for two times 8 columns a lane, whose registers would leave too few waves
+// (8190 tokens of 40 heads of 128, halves: 39 against 32).
+template <bool IB, bool OB, int V, bool NEIGHBOURS, bool EARLY>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkArgs a, int L, int units) {
   const uint32_t id = blockIdx.x * static_cast<uint32_t>(kThreads / L) + threadIdx.x / L;
   const int sub = threadIdx.x & (L - 1);
@@ -132,62 +136,93 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkArgs a, int L,
   void *y = key ? a.ko : a.qo;
   const int64_t yi = (static_cast<int64_t>(t) * (key ? a.Hk : a.Hq) + hh) * a.D;
   const int D = static_cast<int>(a.D), R = static_cast<int>(a.R);
+  bool known;   // an unknown position gives NaN, not a wild read
+  const float *cs;
+  auto locate = [&] {
+    const int64_t pos = a.pos[t];
+    known = pos >= 0 && pos < a.P;
+    cs = a.table + (known ? pos : 0) * R;
+  };
 
-  float v0[V], v1[V];
+  constexpr int P = NEIGHBOURS ? V / 2 : V;   // pairs of a unit
+  float v0[V], v1[V], g0[V], g1[V], c[P], s[P];
   float ss = 0.0f;
   auto fetch = [&](const Unit<V, NEIGHBOURS> &u) {
     load_v<IB, V>(x, xi + u.c0, v0);
     if (!NEIGHBOURS && u.rotated) load_v<IB, V>(x, xi + u.c1, v1);
   };
-  if (live)
-    for (int i = sub; i < units; i += L) {
-      const Unit<V, NEIGHBOURS> u(i, R);
-      fetch(u);
-#pragma unroll
-      for (int j = 0; j < V; ++j) ss = fmaf(v0[j], v0[j], ss);
-      if (!NEIGHBOURS && u.rotated) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) ss = fmaf(v1[j], v1[j], ss);
-      }
-    }
-  for (int d = 1; d < L; d <<= 1) ss += __shfl_xor(ss, d);
-  if (!live) return;
-  const float rms = 1.0f / sqrtf(ss / static_cast<float>(D) + a.eps);
-  const int64_t pos = a.pos[t];
-  const bool known = pos >= 0 && pos < a.P;   // an unknown position gives NaN, not a wild read
-  const float *cs = a.table + (known ? pos : 0) * R;
-
-  for (int i = sub; i < units; i += L) {
-    const Unit<V, NEIGHBOURS> u(i, R);
-    if (units > L) fetch(u);   // otherwise still in registers
-    float g0[V], g1[V];
+  auto fetch_rest = [&](const Unit<V, NEIGHBOURS> &u) {
     load_gain<V>(w, a.w_bf16, u.c0, g0);
+    if (u.rotated) {
+      if constexpr (!NEIGHBOURS) load_gain<V>(w, a.w_bf16, u.c1, g1);
+      load_v<false, P>(cs, u.p0, c);
+      load_v<false, P>(cs, R / 2 + u.p0, s);
+    }
+  };
+  auto square = [&](const Unit<V, NEIGHBOURS> &u) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) ss = fmaf(v0[j], v0[j], ss);
+    if (!NEIGHBOURS && u.rotated) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) ss = fmaf(v1[j], v1[j], ss);
+    }
+  };
+  auto finish = [&](const Unit<V, NEIGHBOURS> &u, float rms) {
 #pragma unroll
     for (int j = 0; j < V; ++j) v0[j] = v0[j] * rms * g0[j];
     if (u.rotated) {
+      if (!known) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) c[j] = __builtin_nanf("");
+      }
       if constexpr (NEIGHBOURS) {
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const float c = known ? cs[u.p0 + j] : __builtin_nanf(""), s = cs[R / 2 + u.p0 + j];
+        for (int j = 0; j < P; ++j) {
           const float p = v0[2 * j], q = v0[2 * j + 1];
-          v0[2 * j] = p * c - q * s;
-          v0[2 * j + 1] = q * c + p * s;
+          v0[2 * j] = p * c[j] - q * s[j];
+          v0[2 * j + 1] = q * c[j] + p * s[j];
         }
       } else {
-        load_gain<V>(w, a.w_bf16, u.c1, g1);
-        float c[V], s[V];
-        load_v<false, V>(cs, u.p0, c);
-        load_v<false, V>(cs, R / 2 + u.p0, s);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float p = v0[j], q = v1[j] * rms * g1[j], cc = known ? c[j] : __builtin_nanf("");
-          v0[j] = p * cc - q * s[j];
-          v1[j] = q * cc + p * s[j];
+        for (int j = 0; j < P; ++j) {
+          const float p = v0[j], q = v1[j] * rms * g1[j];
+          v0[j] = p * c[j] - q * s[j];
+          v1[j] = q * c[j] + p * s[j];
         }
         store_v<OB, V>(y, yi + u.c1, v1);
       }
     }
     store_v<OB, V>(y, yi + u.c0, v0);
+  };
+
+  if constexpr (EARLY) {
+    if (live && sub < units) {
+      const Unit<V, NEIGHBOURS> u(sub, R);
+      locate();
+      fetch(u);
+      fetch_rest(u);
+      square(u);
+    }
+  } else if (live) {
+    for (int i = sub; i < units; i += L) {
+      const Unit<V, NEIGHBOURS> u(i, R);
+      fetch(u);
+      square(u);
+    }
+  }
+  for (int d = 1; d < L; d <<= 1) ss += __shfl_xor(ss, d);
+  if (!live) return;
+  const float rms = 1.0f / sqrtf(ss / static_cast<float>(D) + a.eps);
+  if constexpr (EARLY) {
+    if (sub < units) finish(Unit<V, NEIGHBOURS>(sub, R), rms);
+  } else {
+    locate();
+    for (int i = sub; i < units; i += L) {
+      const Unit<V, NEIGHBOURS> u(i, R);
+      if (units > L) fetch(u);   // otherwise still in registers
+      fetch_rest(u);
+      finish(u, rms);
+    }
   }
 }
 
@@ -197,8 +232,9 @@ void go(const QkArgs &a, hipStream_t st) {
   int L = 1;
   while (L < units && L < 64) L *= 2;
   const int64_t rows = a.T * (a.Hq + a.Hk), per = kThreads / L;
-  qk_norm_rope_kernel<IB, OB, V, NB><<<static_cast<unsigned>((rows + per - 1) / per), kThreads, 0, st>>>(
-      a, L, static_cast<int>(units));
+  const unsigned grid = static_cast<unsigned>((rows + per - 1) / per);
+  if ((NB || V < 8) && units <= L) qk_norm_rope_kernel<IB, OB, V, NB, NB || V < 8><<<grid, kThreads, 0, st>>>(a, L, static_cast<int>(units));
+  else qk_norm_rope_kernel<IB, OB, V, NB, false><<<grid, kThreads, 0, st>>>(a, L, static_cast<int>(units));
 }
 
 template <bool IB, bool OB, bool NB>
