@@ -121,8 +121,8 @@ struct Unit {
 // not for two times 8 columns a lane, whose registers would leave too few waves
 // (8190 tokens of 40 heads of 128, halves: 39 against 32).
 template <bool IB, bool OB, int V, bool NEIGHBOURS, bool EARLY>
-__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkArgs a, int L, int units) {
-  const uint32_t id = blockIdx.x * static_cast<uint32_t>(kThreads / L) + threadIdx.x / L;
+__global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(QkArgs a, int L, int units, uint32_t first) {
+  const uint32_t id = first + blockIdx.x * static_cast<uint32_t>(kThreads / L) + threadIdx.x / L;
   const int sub = threadIdx.x & (L - 1);
   const uint32_t H = static_cast<uint32_t>(a.Hq + a.Hk);
   const bool live = id < static_cast<uint32_t>(a.T) * H;
@@ -231,10 +231,14 @@ void go(const QkArgs &a, hipStream_t st) {
   const int64_t units = NB ? a.D / V : a.R / (2 * V) + (a.D - a.R) / V;
   int L = 1;
   while (L < units && L < 64) L *= 2;
-  const int64_t rows = a.T * (a.Hq + a.Hk), per = kThreads / L;
-  const unsigned grid = static_cast<unsigned>((rows + per - 1) / per);
-  if ((NB || V < 8) && units <= L) qk_norm_rope_kernel<IB, OB, V, NB, NB || V < 8><<<grid, kThreads, 0, st>>>(a, L, static_cast<int>(units));
-  else qk_norm_rope_kernel<IB, OB, V, NB, false><<<grid, kThreads, 0, st>>>(a, L, static_cast<int>(units));
+  const auto kernel = (NB || V < 8) && units <= L ? qk_norm_rope_kernel<IB, OB, V, NB, NB || V < 8>
+                                                  : qk_norm_rope_kernel<IB, OB, V, NB, false>;
+  const int64_t rows = a.T * (a.Hq + a.Hk), per = kThreads / L, most = per * max_groups(kThreads);
+  for (int64_t first = 0; first < rows; first += most) {   // rows of heads of a launch
+    const int64_t n = rows - first < most ? rows - first : most;
+    kernel<<<static_cast<unsigned>((n + per - 1) / per), kThreads, 0, st>>>(a, L, static_cast<int>(units),
+                                                                            static_cast<uint32_t>(first));
+  }
 }
 
 template <bool IB, bool OB, bool NB>
