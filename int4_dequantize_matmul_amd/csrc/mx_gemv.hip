@@ -32,6 +32,7 @@ struct GemvArgs {
   void *y;
   int64_t M, N, K;
   int KB;
+  int64_t first;   // the launch's first block of 16 weight rows
 };
 
 // One lane's four blocks of a row, and the scale of each in byte 0 of s[j];
@@ -146,7 +147,7 @@ enum XType { kPacked = 0, kF32 = 1, kBf16 = 2 };
 template <int MT, int XT, bool BOUT, int R>
 __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a4(GemvArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t n0 = 16 * static_cast<int64_t>(blockIdx.x), m0 = 16 * MT * static_cast<int64_t>(blockIdx.y);
+  const int64_t n0 = 16 * (a.first + blockIdx.x), m0 = 16 * MT * static_cast<int64_t>(blockIdx.y);
   const int64_t n = min(n0 + r, a.N - 1);
   const uint8_t *wrow = a.w + n * a.KB * 16, *srow = a.sw + n * a.KB;
   const int steps = (a.KB + 15) / 16;
@@ -184,7 +185,7 @@ template <bool BOUT, int R>
 __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a16(GemvArgs a) {
   extern __shared__ __align__(16) uint8_t runs0[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t n0 = 16 * static_cast<int64_t>(blockIdx.x), m0 = 16 * static_cast<int64_t>(blockIdx.y);
+  const int64_t n0 = 16 * (a.first + blockIdx.x), m0 = 16 * static_cast<int64_t>(blockIdx.y);
   const int64_t n = min(n0 + r, a.N - 1);
   const int rows = static_cast<int>(min(a.M - m0, static_cast<int64_t>(R)));
   const uint8_t *wrow = a.w + n * a.KB * 16, *srow = a.sw + n * a.KB;
@@ -220,16 +221,22 @@ __global__ __launch_bounds__(64 * kWaves) void mx_gemv_w4a16(GemvArgs a) {
   join_and_store<1, BOUT>(a, acc, m0, n0);
 }
 
-template <int MT>
-dim3 grid_of(const GemvArgs &a) {
-  return dim3(static_cast<unsigned>((a.N + 15) / 16), static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT)));
+// The kernel over all blocks of weight rows, in as few launches as hold them.
+template <int MT, class Kernel>
+void run_blocks(Kernel kernel, GemvArgs a, int lds, hipStream_t st) {
+  constexpr int64_t most = max_groups(64 * kWaves);
+  const int64_t blocks = (a.N + 15) / 16;
+  for (a.first = 0; a.first < blocks; a.first += most) {
+    const int64_t n = blocks - a.first < most ? blocks - a.first : most;
+    kernel<<<dim3(static_cast<unsigned>(n), static_cast<unsigned>((a.M + 16 * MT - 1) / (16 * MT))), 64 * kWaves, lds,
+             st>>>(a);
+  }
 }
 
 // R: rows that the kernel quantizes at a time
 template <int MT, int XT, int R = 1>
 void run_w4a4(const GemvArgs &a, bool y_bf16, hipStream_t st) {
-  if (y_bf16) mx_gemv_w4a4<MT, XT, true, R><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
-  else mx_gemv_w4a4<MT, XT, false, R><<<grid_of<MT>(a), 64 * kWaves, 0, st>>>(a);
+  run_blocks<MT>(y_bf16 ? mx_gemv_w4a4<MT, XT, true, R> : mx_gemv_w4a4<MT, XT, false, R>, a, 0, st);
 }
 
 template <int XT>
@@ -251,7 +258,7 @@ hipError_t run_w4a16(const GemvArgs &a, bool y_bf16, hipStream_t st) {
                             hipFuncAttributeMaxDynamicSharedMemorySize, lds)};
     if (set[y_bf16] != hipSuccess) return set[y_bf16];
   }
-  kernel<<<grid_of<1>(a), 64 * kWaves, lds, st>>>(a);
+  run_blocks<1>(kernel, a, lds, st);
   return hipGetLastError();
 }
 
@@ -259,7 +266,7 @@ hipError_t run_w4a16(const GemvArgs &a, bool y_bf16, hipStream_t st) {
 
 hipError_t launch_mx_gemv_w4a4(const uint8_t *xq, const uint8_t *sx, const uint8_t *wq, const uint8_t *sw, void *y,
                                bool y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t st) {
-  const GemvArgs a = {xq, sx, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32)};
+  const GemvArgs a = {xq, sx, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32), 0};
   if (M <= 16) run_w4a4<1, kPacked>(a, y_bf16, st);
   else if (M <= 32) run_w4a4<2, kPacked>(a, y_bf16, st);
   else run_w4a4<4, kPacked>(a, y_bf16, st);
@@ -268,7 +275,7 @@ hipError_t launch_mx_gemv_w4a4(const uint8_t *xq, const uint8_t *sx, const uint8
 
 hipError_t launch_mx_gemv_w4a4_fused(const void *x, bool x_bf16, const uint8_t *wq, const uint8_t *sw, void *y,
                                      bool y_bf16, int64_t M, int64_t N, int64_t K, hipStream_t st) {
-  const GemvArgs a = {x, nullptr, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32)};
+  const GemvArgs a = {x, nullptr, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32), 0};
   if (x_bf16) run_w4a4_fused<kBf16>(a, y_bf16, st);
   else run_w4a4_fused<kF32>(a, y_bf16, st);
   return hipGetLastError();
@@ -276,7 +283,7 @@ hipError_t launch_mx_gemv_w4a4_fused(const void *x, bool x_bf16, const uint8_t *
 
 hipError_t launch_mx_gemv_w4a16(const uint16_t *x, const uint8_t *wq, const uint8_t *sw, void *y, bool y_bf16,
                                 int64_t M, int64_t N, int64_t K, hipStream_t st) {
-  const GemvArgs a = {x, nullptr, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32)};
+  const GemvArgs a = {x, nullptr, wq, sw, y, M, N, K, static_cast<int>((K + 31) / 32), 0};
   if (M == 1) return run_w4a16<1>(a, y_bf16, st);
   if (M <= 4) return run_w4a16<4>(a, y_bf16, st);
   if (M <= 8) return run_w4a16<8>(a, y_bf16, st);

@@ -1,5 +1,8 @@
 """Calls whose launch would have more threads along an axis than a grid can
-(2^32): rows of heads past that go out in several launches.
+(2^32): rows of heads and weight rows past that go out in several launches.
+
+The inputs are zeros but for the rows that are compared: the first, the last,
+and those around the launches' borders (2^24 workgroups of 256 threads).
 """
 import numpy as np
 import pytest
@@ -7,7 +10,7 @@ import torch
 
 import int4_dequantize_matmul_amd as q4
 import oracle.mx as X
-from tests.gpu_util import DEV
+from tests.gpu_util import DEV, host
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +32,29 @@ def test_head_rows_past_a_grid(D, xt, pairs):
     assert np.all(np.abs(small.double().cpu().numpy() - ref) <= tol)
     whole = T // P * P
     assert (y[:whole].view(-1, P, H, D) == small).all() and (y[whole:] == small[:T - whole]).all()
+
+
+@pytest.mark.parametrize("op", ["w4a4", "w4a4_dynamic", "w4a16"])
+def test_weight_rows_past_a_grid(op):
+    """2^28 + 40 weight rows of one block, 16 to a workgroup."""
+    N, K, M = (1 << 28) + 40, 32, 2
+    at = np.array([0, 1, 17, (1 << 27) + 3, (1 << 28) - 17, (1 << 28) - 16, (1 << 28) - 15, (1 << 28) - 1, 1 << 28,
+                   (1 << 28) + 15, (1 << 28) + 16, N - 1])
+    rng = np.random.default_rng(11)
+    wq, sw = X.quantize_rows(rng.standard_normal((len(at), K)))
+    i = torch.from_numpy(at).to(DEV)
+    w = torch.zeros((N, 16), dtype=torch.uint8, device=DEV)
+    s = torch.full((N, 1), 127, dtype=torch.uint8, device=DEV)
+    w[i], s[i] = torch.from_numpy(wq).to(DEV), torch.from_numpy(sw).to(DEV)
+    x = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).to(DEV).bfloat16()
+    v = x.double().cpu().numpy()
+    if op == "w4a16":
+        y = q4.q4_linear_w4a16_mx(x, w, s, "f32")
+        ref, mag = X.linear_w4a16(v, wq, sw)
+    else:
+        xq, sx = q4.q4_mx_quantize_rows(x)
+        y = q4.q4_linear_w4a4_mx(xq, sx, w, s, "f32") if op == "w4a4" else q4.q4_linear_w4a4_mx_dynamic(x, w, s, "f32")
+        ref, mag = X.linear_w4a4(*X.quantize_rows(v), wq, sw)
+    assert np.all(np.abs(host(y[:, i]) - ref) <= (K + 8) * 2.0 ** -24 * mag)
+    y[:, i] = 0
+    assert not y.any()
