@@ -12,6 +12,11 @@ namespace q4 {
 // before every launch.)
 bool device_is_gfx950();
 
+// Workgroups of `threads` threads that one launch can have along x: a grid axis
+// holds fewer than 2^32 threads.  The runtime does not refuse more, it starts
+// their number modulo 2^32 and reports success.
+constexpr int64_t max_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
+
 // Stored-nibble encodings, as in q4_enc.
 enum Enc : int { kTwos = 0, kExcess8 = 1 };
 
@@ -115,11 +120,6 @@ bool tiled_w4a16_ok(const void *x, const void *wq, int64_t M, int64_t N, int64_t
 hipError_t launch_tiled_w4a16(const uint16_t *x, const uint8_t *wq, const uint16_t *s, float *yf,
                               uint16_t *yb, int64_t M, int64_t N, int64_t K, int64_t G, int enc,
                               hipStream_t st, const uint8_t *zp = nullptr);
-
-// Workgroups of `threads` threads that one launch can have along x: a grid axis
-// holds fewer than 2^32 threads.  The runtime does not refuse more, it starts
-// their number modulo 2^32 and reports success.
-constexpr int64_t max_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
 
 // MX FP4 (blocks of 32 E2M1 codes under one E8M0 byte).  packed and wq, xq
 // are 16-byte aligned, rows of 16 ceil(K/32) bytes; scales rows of ceil(K/32).

@@ -141,10 +141,12 @@ __global__ void zero_bytes(uint8_t *__restrict__ p, size_t n) {
 }  // namespace
 
 hipError_t launch_zero(void *p, size_t bytes, hipStream_t st) {
-  if (bytes == 0) return hipSuccess;
-  const size_t per_block = 256 * 16;
-  const unsigned blocks = static_cast<unsigned>((bytes + per_block - 1) / per_block);
-  zero_bytes<<<blocks, 256, 0, st>>>(static_cast<uint8_t *>(p), bytes);
+  const size_t per_block = 256 * 16, most = per_block * max_groups(256);
+  for (size_t at = 0; at < bytes; at += most) {
+    const size_t n = bytes - at < most ? bytes - at : most;
+    zero_bytes<<<static_cast<unsigned>((n + per_block - 1) / per_block), 256, 0, st>>>(static_cast<uint8_t *>(p) + at,
+                                                                                        n);
+  }
   return hipGetLastError();
 }
 
@@ -152,14 +154,12 @@ hipError_t launch_quantize_rows(const void *x, bool x_bf16, int64_t M, int64_t K
                                 float *sx, hipStream_t st) {
   const bool vec = (K % 8 == 0) && (reinterpret_cast<uintptr_t>(x) % 16 == 0) &&
                    (reinterpret_cast<uintptr_t>(xq) % 8 == 0);
-  const dim3 grid(static_cast<unsigned>(M));
-  if (vec) {
-    if (x_bf16) quantize_rows_vec<true><<<grid, kThreads, 0, st>>>(x, K, xq, sx);
-    else quantize_rows_vec<false><<<grid, kThreads, 0, st>>>(x, K, xq, sx);
-  } else {
-    if (x_bf16) quantize_rows_any<true><<<grid, kThreads, 0, st>>>(x, K, xq, sx);
-    else quantize_rows_any<false><<<grid, kThreads, 0, st>>>(x, K, xq, sx);
-  }
+  const auto kernel = vec ? (x_bf16 ? quantize_rows_vec<true> : quantize_rows_vec<false>)
+                          : (x_bf16 ? quantize_rows_any<true> : quantize_rows_any<false>);
+  constexpr int64_t most = max_groups(kThreads);   // rows of a launch
+  for (int64_t m = 0; m < M; m += most)
+    kernel<<<static_cast<unsigned>(M - m < most ? M - m : most), kThreads, 0, st>>>(
+        static_cast<const uint8_t *>(x) + m * K * (x_bf16 ? 2 : 4), K, xq + m * K, sx + m);
   return hipGetLastError();
 }
 

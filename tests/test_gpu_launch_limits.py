@@ -58,3 +58,26 @@ def test_weight_rows_past_a_grid(op):
     assert np.all(np.abs(host(y[:, i]) - ref) <= (K + 8) * 2.0 ** -24 * mag)
     y[:, i] = 0
     assert not y.any()
+
+
+@pytest.mark.parametrize("K,xt", [(8, torch.float32), (8, torch.bfloat16), (3, torch.float32)])
+def test_int8_rows_past_a_grid(K, xt):
+    """2^24 + 1000 activation rows, a workgroup each."""
+    P, M = 11, (1 << 24) + 1000
+    gen = torch.Generator(DEV).manual_seed(K)
+    x = torch.randn(P, K, device=DEV, generator=gen).to(xt)
+    q, s = q4.q8_quantize_rows(x)
+    whole = M // P * P
+    qm, sm = q4.q8_quantize_rows(x[torch.arange(M, device=DEV) % P])
+    assert (qm[:whole].view(-1, P, K) == q).all() and (qm[whole:] == q[:M - whole]).all()
+    assert (sm[:whole].view(-1, P) == s).all() and (sm[whole:] == s[:M - whole]).all()
+
+
+def test_zeros_past_a_grid():
+    """A result of 2^36 bytes and more that is all zeros (no columns to sum)."""
+    M, N = 16400, 1 << 20
+    z = torch.zeros((N, 0), dtype=torch.uint8, device=DEV)
+    y = torch.full((M, N), float("nan"), device=DEV)
+    q4.q4_linear_w4a4_mx(z[:M], z[:M], z, z, "f32", y=y)
+    for part in y.split(1024):
+        assert (part == 0).all()
