@@ -56,9 +56,9 @@ template <bool XBF16, bool SBF16>
 __global__ __launch_bounds__(kWaves * 64) void generic_float(
     const void *__restrict__ x, const uint8_t *__restrict__ wq, const uint16_t *__restrict__ s,
     float *__restrict__ yf, uint16_t *__restrict__ yb, int64_t M, int64_t N, int64_t K,
-    int64_t G, int enc, const uint8_t *__restrict__ zp) {
+    int64_t G, int enc, const uint8_t *__restrict__ zp, int64_t n_first) {
   const int lane = threadIdx.x & 63;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int64_t n = n_first + static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
   if (n >= N) return;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kMB;
   const int Mb = static_cast<int>(M - m0 < kMB ? M - m0 : kMB);
@@ -103,9 +103,9 @@ template <bool W8>
 __global__ __launch_bounds__(kWaves * 64) void generic_int(
     const int8_t *__restrict__ xq, const float *__restrict__ sx, const void *__restrict__ w,
     const float *__restrict__ sw, float *__restrict__ y, int64_t M, int64_t N, int64_t K,
-    int64_t G, int enc, const uint8_t *__restrict__ zp) {
+    int64_t G, int enc, const uint8_t *__restrict__ zp, int64_t n_first) {
   const int lane = threadIdx.x & 63;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int64_t n = n_first + static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
   if (n >= N) return;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kMB;
   const int Mb = static_cast<int>(M - m0 < kMB ? M - m0 : kMB);
@@ -175,9 +175,10 @@ __global__ __launch_bounds__(kWaves * 64) void generic_int(
 template <bool XBF16>
 __global__ __launch_bounds__(kWaves * 64) void generic_w8_float(
     const void *__restrict__ x, const int8_t *__restrict__ wq, const float *__restrict__ s,
-    float *__restrict__ yf, uint16_t *__restrict__ yb, int64_t M, int64_t N, int64_t K) {
+    float *__restrict__ yf, uint16_t *__restrict__ yb, int64_t M, int64_t N, int64_t K,
+    int64_t n_first) {
   const int lane = threadIdx.x & 63;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int64_t n = n_first + static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
   if (n >= N) return;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kMB;
   const int Mb = static_cast<int>(M - m0 < kMB ? M - m0 : kMB);
@@ -209,9 +210,15 @@ __global__ __launch_bounds__(kWaves * 64) void generic_w8_float(
   }
 }
 
-dim3 generic_grid(int64_t M, int64_t N) {
-  return dim3(static_cast<unsigned>((N + kWaves - 1) / kWaves),
-              static_cast<unsigned>((M + kMB - 1) / kMB));
+// run(grid, n_first) for all weight rows, in as few launches as hold them.
+template <class Run>
+hipError_t launch_all(int64_t M, int64_t N, Run run) {
+  constexpr int64_t most = max_groups(kWaves * 64) * kWaves;
+  for (int64_t n = 0; n < N; n += most)
+    run(dim3(static_cast<unsigned>(((N - n < most ? N - n : most) + kWaves - 1) / kWaves),
+             static_cast<unsigned>((M + kMB - 1) / kMB)),
+        n);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -219,33 +226,29 @@ dim3 generic_grid(int64_t M, int64_t N) {
 hipError_t launch_generic_float(const void *x, bool x_bf16, const uint8_t *wq, const uint16_t *s,
                                 bool s_bf16, float *yf, uint16_t *yb, int64_t M, int64_t N,
                                 int64_t K, int64_t G, int enc, hipStream_t st, const uint8_t *zp) {
-  const dim3 grid = generic_grid(M, N);
-  if (x_bf16 && s_bf16)
-    generic_float<true, true><<<grid, kWaves * 64, 0, st>>>(x, wq, s, yf, yb, M, N, K, G, enc, zp);
-  else if (!x_bf16 && !s_bf16)
-    generic_float<false, false><<<grid, kWaves * 64, 0, st>>>(x, wq, s, yf, yb, M, N, K, G, enc, zp);
-  else
-    return hipErrorInvalidValue;
-  return hipGetLastError();
+  if (x_bf16 != s_bf16) return hipErrorInvalidValue;
+  const auto kernel = x_bf16 ? generic_float<true, true> : generic_float<false, false>;
+  return launch_all(M, N, [&](dim3 grid, int64_t n_first) {
+    kernel<<<grid, kWaves * 64, 0, st>>>(x, wq, s, yf, yb, M, N, K, G, enc, zp, n_first);
+  });
 }
 
 hipError_t launch_generic_int(const int8_t *xq, const float *sx, const void *w, bool w_int8,
                               const float *sw, float *y, int64_t M, int64_t N, int64_t K,
                               int64_t G, int enc, hipStream_t st, const uint8_t *zp) {
-  const dim3 grid = generic_grid(M, N);
-  if (w_int8)
-    generic_int<true><<<grid, kWaves * 64, 0, st>>>(xq, sx, w, sw, y, M, N, K, 0, enc, nullptr);
-  else
-    generic_int<false><<<grid, kWaves * 64, 0, st>>>(xq, sx, w, sw, y, M, N, K, G, enc, zp);
-  return hipGetLastError();
+  const auto kernel = w_int8 ? generic_int<true> : generic_int<false>;
+  if (w_int8) G = 0, zp = nullptr;
+  return launch_all(M, N, [&](dim3 grid, int64_t n_first) {
+    kernel<<<grid, kWaves * 64, 0, st>>>(xq, sx, w, sw, y, M, N, K, G, enc, zp, n_first);
+  });
 }
 
 hipError_t launch_generic_w8_float(const void *x, bool x_bf16, const int8_t *wq, const float *s, float *yf,
                                    uint16_t *yb, int64_t M, int64_t N, int64_t K, hipStream_t st) {
-  const dim3 grid = generic_grid(M, N);
-  if (x_bf16) generic_w8_float<true><<<grid, kWaves * 64, 0, st>>>(x, wq, s, yf, yb, M, N, K);
-  else generic_w8_float<false><<<grid, kWaves * 64, 0, st>>>(x, wq, s, yf, yb, M, N, K);
-  return hipGetLastError();
+  const auto kernel = x_bf16 ? generic_w8_float<true> : generic_w8_float<false>;
+  return launch_all(M, N, [&](dim3 grid, int64_t n_first) {
+    kernel<<<grid, kWaves * 64, 0, st>>>(x, wq, s, yf, yb, M, N, K, n_first);
+  });
 }
 
 }  // namespace q4

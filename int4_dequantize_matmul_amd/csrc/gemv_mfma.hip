@@ -597,6 +597,7 @@ bool plan(Args &a, int64_t M, int64_t N, int64_t K, int64_t G, size_t *lds, int 
   a.Mbmax = static_cast<int>(M < 16 ? M : 16);
   *nw = waves_for(a.nC);
   if (a.nC > 16 * kNB) return false;                       // more chunks than 16 waves hold
+  if ((N + 15) / 16 > max_groups(*nw * 64)) return false;  // more blocks of weight rows than a grid holds
   const size_t win_bytes = static_cast<size_t>(T::ND) * 4 * a.Mbmax * 16 + a.Mbmax * 4;  // per chunk
   int slab = static_cast<int>(kSlabBytes / win_bytes);
   if (slab < 1) slab = 1;
@@ -662,13 +663,13 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 }  // namespace
 
-bool gemv_w4a16_ok(const void *x, const void *wq, int64_t K, int64_t G) {
+bool gemv_w4a16_ok(const void *x, const void *wq, int64_t K, int64_t G, int64_t N) {
   (void)x;
   if (G <= 0 || G % 128 != 0 || K % G != 0 || !aligned16(wq)) return false;
   Args a{};
   size_t lds;
   int nw;
-  return plan<Fmt::W4A16>(a, 16, 16, K, G, &lds, &nw);
+  return plan<Fmt::W4A16>(a, 16, N, K, G, &lds, &nw);
 }
 
 hipError_t launch_gemv_w4a16(const uint16_t *x, const uint8_t *wq, const uint16_t *s, float *yf,
@@ -680,13 +681,13 @@ hipError_t launch_gemv_w4a16(const uint16_t *x, const uint8_t *wq, const uint16_
   return launch<Fmt::W4A16>(a, M, N, K, G, st);
 }
 
-bool gemv_w4a8_ok(const void *wq, int64_t K, int64_t G) {
+bool gemv_w4a8_ok(const void *wq, int64_t K, int64_t G, int64_t N) {
   if (!aligned16(wq) || ((K + 1) / 2) % 16 != 0) return false;
   if (G != 0 && (G % 128 != 0 || K % G != 0)) return false;
   Args a{};
   size_t lds;
   int nw;
-  return plan<Fmt::W4A8>(a, 16, 16, K, G, &lds, &nw);
+  return plan<Fmt::W4A8>(a, 16, N, K, G, &lds, &nw);
 }
 
 hipError_t launch_gemv_w4a8(const int8_t *xq, const float *sx, const uint8_t *wq, const float *sw,
@@ -729,12 +730,12 @@ hipError_t launch_gemv_w4a8_fused(const void *x, bool x_bf16, const uint8_t *wq,
                  : launch_xv<Fmt::W4A8, false, false, 1>(a, nw, lds, st);
 }
 
-bool gemv_w8a8_ok(const void *wq, int64_t K) {
+bool gemv_w8a8_ok(const void *wq, int64_t K, int64_t N) {
   if (!aligned16(wq) || K % 16 != 0) return false;
   Args a{};
   size_t lds;
   int nw;
-  return plan<Fmt::W8A8>(a, 16, 16, K, 0, &lds, &nw);
+  return plan<Fmt::W8A8>(a, 16, N, K, 0, &lds, &nw);
 }
 
 hipError_t launch_gemv_w8a8(const int8_t *xq, const float *sx, const int8_t *wq, const float *sw,

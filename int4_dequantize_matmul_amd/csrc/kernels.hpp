@@ -17,6 +17,10 @@ bool device_is_gfx950();
 // their number modulo 2^32 and reports success.
 constexpr int64_t max_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
 
+// Weight rows that one launch of a streaming or matrix-core decode kernel can
+// have: 16 to 256 threads (4 to 64).  The general kernels serve more.
+constexpr int64_t kDecodeMaxN = 16 * max_groups(256);
+
 // Stored-nibble encodings, as in q4_enc.
 enum Enc : int { kTwos = 0, kExcess8 = 1 };
 
@@ -57,7 +61,7 @@ hipError_t launch_gemv_stream_w4a32(const float *x, const uint8_t *wq, const uin
 
 // Decode GEMV on MFMA (M in blocks of 16).  *_ok says whether the fast
 // kernel serves a shape / alignment; the launcher must only be called then.
-bool gemv_w4a16_ok(const void *x, const void *wq, int64_t K, int64_t G);
+bool gemv_w4a16_ok(const void *x, const void *wq, int64_t K, int64_t G, int64_t N = 16);
 hipError_t launch_gemv_w4a16(const uint16_t *x, const uint8_t *wq, const uint16_t *s, float *yf,
                              uint16_t *yb, int64_t M, int64_t N, int64_t K, int64_t G, int enc,
                              hipStream_t st, const uint8_t *zp = nullptr);
@@ -94,7 +98,7 @@ int64_t gemv_chan_w4a8_multi_max();
 int64_t gemv_chan_w4a8_multi_tiles(int64_t N);
 hipError_t launch_gemv_chan_w4a8_multi(const ChanProblem *pr, int count, int64_t M, bool x_bf16,
                                        hipStream_t st);
-bool gemv_w4a8_ok(const void *wq, int64_t K, int64_t G);
+bool gemv_w4a8_ok(const void *wq, int64_t K, int64_t G, int64_t N = 16);
 hipError_t launch_gemv_w4a8(const int8_t *xq, const float *sx, const uint8_t *wq, const float *sw,
                             float *y, int64_t M, int64_t N, int64_t K, int64_t G, int enc,
                             hipStream_t st, const uint8_t *zp = nullptr);
@@ -104,7 +108,7 @@ bool gemv_w4a8_fused_ok(const void *wq, int64_t M, int64_t K, int64_t G, bool x_
 hipError_t launch_gemv_w4a8_fused(const void *x, bool x_bf16, const uint8_t *wq, const float *sw, float *y,
                                   int64_t M, int64_t N, int64_t K, int64_t G, int enc, hipStream_t st,
                                   const uint8_t *zp = nullptr);
-bool gemv_w8a8_ok(const void *wq, int64_t K);
+bool gemv_w8a8_ok(const void *wq, int64_t K, int64_t N = 16);
 hipError_t launch_gemv_w8a8(const int8_t *xq, const float *sx, const int8_t *wq, const float *sw,
                             float *y, int64_t M, int64_t N, int64_t K, hipStream_t st);
 

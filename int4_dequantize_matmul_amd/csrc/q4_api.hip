@@ -165,10 +165,10 @@ q4_path path_of(Kern k) {
 // takes no zero points; such calls take the default decode kernels.
 Kern pick_w4a16(const void *x, const void *wq, int64_t M, int64_t N, int64_t K, int64_t G, bool zp) {
   if (!zp && g_path.load(std::memory_order_relaxed) == Q4_PATH_GEMV_MC)
-    return q4::gemv_mc_w4a16_ok(x, wq, M, K, G) ? Kern::GEMV_MC : Kern::GENERIC;
+    return N <= q4::kDecodeMaxN && q4::gemv_mc_w4a16_ok(x, wq, M, K, G) ? Kern::GEMV_MC : Kern::GENERIC;
   const bool tiled = q4::tiled_w4a16_ok(x, wq, M, N, K, G);
-  const bool valu = q4::gemv_stream_w4a16_ok(x, wq, M, K, G);
-  const bool mfma = q4::gemv_w4a16_ok(x, wq, K, G);
+  const bool valu = N <= q4::kDecodeMaxN && q4::gemv_stream_w4a16_ok(x, wq, M, K, G);
+  const bool mfma = q4::gemv_w4a16_ok(x, wq, K, G, N);
   const q4_path p = route(tiled, valu || mfma, M, decode_max(Op::W4A16, N, K));
   if (p == Q4_PATH_TILED) return Kern::TILED;
   if (p == Q4_PATH_GEMV) return valu ? Kern::GEMV_STREAM : Kern::GEMV_MFMA;
@@ -185,8 +185,8 @@ constexpr int64_t kChanStreamMaxM = 1;
 // W4A8, per channel (G == 0) or grouped; xq and wq only for alignment.
 Kern pick_w4a8(const void *xq, const void *wq, int64_t M, int64_t N, int64_t K, int64_t G) {
   const bool tiled = q4::tiled_w4a8_ok(xq, wq, M, N, K, G);
-  const bool mfma = q4::gemv_w4a8_ok(wq, K, G);
-  const bool chan = G == 0 && q4::gemv_chan_w4a8_ok(wq, M, K);
+  const bool mfma = q4::gemv_w4a8_ok(wq, K, G, N);
+  const bool chan = G == 0 && N <= q4::kDecodeMaxN && q4::gemv_chan_w4a8_ok(wq, M, K);
   const q4_path p = route(tiled, mfma || chan, M, decode_max(G ? Op::W4A8_GROUPED : Op::W4A8_CHANNEL, N, K));
   if (p == Q4_PATH_TILED) return Kern::TILED;
   if (p != Q4_PATH_GEMV) return Kern::GENERIC;
@@ -243,14 +243,14 @@ extern "C" q4_status q4_route_plan(q4_op op_arg, int64_t M, int64_t N, int64_t K
     const void *al = reinterpret_cast<const void *>(uintptr_t{4096});
     Kern k = Kern::GENERIC;
     if (op == Q4_OP_W4A32) {
-      k = route(false, q4::gemv_stream_w4a32_ok(al, al, M, K, G), M, INT64_MAX) == Q4_PATH_GEMV ? Kern::GEMV_STREAM
-                                                                                                 : Kern::GENERIC;
+      const bool gemv = N <= q4::kDecodeMaxN && q4::gemv_stream_w4a32_ok(al, al, M, K, G);
+      k = route(false, gemv, M, INT64_MAX) == Q4_PATH_GEMV ? Kern::GEMV_STREAM : Kern::GENERIC;
     } else if (op == Q4_OP_W4A16 || op == Q4_OP_W4A16_ZP) {
       k = pick_w4a16(al, al, M, N, K, G, op == Q4_OP_W4A16_ZP);
     } else if (op == Q4_OP_W4A8 || op == Q4_OP_W4A8_ZP) {
       k = pick_w4a8(al, al, M, N, K, G);
     } else {
-      k = route(false, q4::gemv_w8a8_ok(al, K), M, INT64_MAX) == Q4_PATH_GEMV ? Kern::GEMV_MFMA : Kern::GENERIC;
+      k = route(false, q4::gemv_w8a8_ok(al, K, N), M, INT64_MAX) == Q4_PATH_GEMV ? Kern::GEMV_MFMA : Kern::GENERIC;
     }
     p.path = path_of(k);
     if (k == Kern::TILED && (op == Q4_OP_W4A8 || op == Q4_OP_W4A8_ZP)) {
@@ -302,7 +302,7 @@ extern "C" q4_status q4_linear_w4a32(const float *x, const uint8_t *wq, const ui
   if (!device_ok()) return Q4_EDEVICE;
   if (K == 0) return finish(q4::launch_zero(y, u(M) * u(N) * 4, S(stream)), Q4_PATH_GENERIC);
   // one streaming kernel for every batch size (no tiled f32-activation kernel)
-  const bool gemv = q4::gemv_stream_w4a32_ok(x, wq, M, K, G);
+  const bool gemv = N <= q4::kDecodeMaxN && q4::gemv_stream_w4a32_ok(x, wq, M, K, G);
   const q4_path p = route(false, gemv, M, INT64_MAX);
   if (p == Q4_PATH_GEMV)
     return finish(q4::launch_gemv_stream_w4a32(x, wq, scales_f16, y, M, N, K, G, enc, S(stream)), p);
@@ -612,7 +612,7 @@ q4_status w8_float_impl(const void *x, bool x_bf16, const int8_t *wq, const floa
     return finish(e, Q4_PATH_GENERIC);
   }
   // one streaming kernel for every batch size (no tiled int8-weight kernel)
-  const bool gemv = q4::gemv_stream_w8_ok(x, wq, M, K);
+  const bool gemv = N <= q4::kDecodeMaxN && q4::gemv_stream_w8_ok(x, wq, M, K);
   const q4_path p = route(false, gemv, M, INT64_MAX);
   if (p == Q4_PATH_GEMV)
     return finish(q4::launch_gemv_stream_w8(x, x_bf16, wq, sw, y_f32, y_bf16, M, N, K, st), p);
@@ -645,7 +645,7 @@ extern "C" q4_status q8_linear_w8a8(const int8_t *xq, const float *sx, const int
   if (!device_ok()) return Q4_EDEVICE;
   hipStream_t st = S(stream);
   if (K == 0) return finish(q4::launch_zero(y, u(M) * u(N) * 4, st), Q4_PATH_GENERIC);
-  const bool gemv = q4::gemv_w8a8_ok(wq, K);
+  const bool gemv = q4::gemv_w8a8_ok(wq, K, N);
   const q4_path p = route(false, gemv, M, INT64_MAX);
   if (p == Q4_PATH_GEMV) return finish(q4::launch_gemv_w8a8(xq, sx, wq, sw, y, M, N, K, st), p);
   return finish(q4::launch_generic_int(xq, sx, wq, true, sw, y, M, N, K, 0, Q4_ENC_EXCESS8, st), p);

@@ -60,6 +60,12 @@ def test_weight_rows_past_a_grid(op):
     assert not y.any()
 
 
+@pytest.fixture
+def _auto_path():
+    yield
+    q4.q4_set_path("auto")
+
+
 @pytest.mark.parametrize("K,xt", [(8, torch.float32), (8, torch.bfloat16), (3, torch.float32)])
 def test_int8_rows_past_a_grid(K, xt):
     """2^24 + 1000 activation rows, a workgroup each."""
@@ -81,3 +87,48 @@ def test_zeros_past_a_grid():
     q4.q4_linear_w4a4_mx(z[:M], z[:M], z, z, "f32", y=y)
     for part in y.split(1024):
         assert (part == 0).all()
+
+
+@pytest.mark.parametrize("N,path", [((1 << 26) + 21, "generic"), ((1 << 28) + 21, "auto")])
+@pytest.mark.parametrize("op", ["w4a32", "w4a16", "w4a16_zp", "w4a8", "w4a8_grouped", "w4a8_dynamic", "w8a8", "w8a16"])
+def test_int4_and_int8_weight_rows_past_a_grid(op, N, path, _auto_path):
+    """Weight rows past a launch of the general kernels (2^26) and past one of
+    the decode kernels (2^28): 13 rows over and over, so the results repeat."""
+    P, M = 13, 1
+    K, G = (32, 32) if path == "auto" else (8, 4)
+    if op in ("w4a8_grouped", "w4a16_zp"):
+        G = K
+    rng = np.random.default_rng(K + len(op))
+    x = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).to(DEV)
+    wide = 1 if op.startswith("w8") else 2
+    w = torch.from_numpy(rng.integers(0, 256, (P, K // wide), dtype=np.uint8)).to(DEV)
+    s = torch.from_numpy(rng.uniform(0.5, 2, (P, K // G)).astype(np.float32)).to(DEV)
+    z = torch.from_numpy(rng.integers(0, 16, (P, K // G), dtype=np.uint8)).to(DEV)
+    xq, sx = q4.q8_quantize_rows(x)
+
+    def call(n):
+        # (not by an index: torch's own launch for so many rows wraps as well)
+        wn, sn, zn = (t.repeat(-(-n // P), 1)[:n] for t in (w, s, z))
+        if op == "w4a32":
+            return q4.q4_linear_w4a32(x, wn, sn.half(), G)
+        if op == "w4a16":
+            return q4.q4_linear_w4a16(x.bfloat16(), wn, sn.bfloat16(), G)[0]
+        if op == "w4a16_zp":
+            return q4.q4_linear_w4a16_zp(x.bfloat16(), wn, sn.bfloat16(), zn, G)[0]
+        if op == "w4a8":
+            return q4.q4_linear_w4a8(xq, sx, wn, sn[:, 0].contiguous(), 0)
+        if op == "w4a8_grouped":
+            return q4.q4_linear_w4a8(xq, sx, wn, sn, G)
+        if op == "w4a8_dynamic":
+            return q4.q4_linear_w4a8_dynamic(x, wn, sn[:, 0].contiguous(), 0)
+        if op == "w8a8":
+            return q4.q8_linear_w8a8(xq, sx, wn.view(torch.int8), sn[:, 0].contiguous())
+        return q4.q8_linear_w8a16(x.bfloat16(), wn.view(torch.int8), sn[:, 0].contiguous())[0]
+
+    q4.q4_set_path("generic")   # the kernels that serve what is past the decode kernels' launches
+    small = call(P)
+    q4.q4_set_path(path)
+    y = call(N)
+    assert y.shape == (M, N)
+    whole = N // P * P
+    assert (y[:, :whole].view(M, -1, P) == small[:, None]).all() and (y[:, whole:] == small[:, :N - whole]).all()

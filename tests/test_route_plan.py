@@ -158,3 +158,12 @@ def test_plan_argument_rules():
     assert status("w4a8", 1, 16, q4.W4A8_MAX_K + 2, G=0) == q4.ESHAPE
     assert status("w8a8", 1, 16, q4.W8A8_MAX_K + 1) == q4.ESHAPE
     assert status("w4a8", 1, 16, 1023, G=0) == q4.OK
+
+
+@pytest.mark.parametrize("op,K,G", [("w4a32", 32, 32), ("w4a16", 32, 32), ("w4a16", 128, 128), ("w4a8", 32, 0),
+                                    ("w4a8", 128, 128), ("w8a8", 64, 0)])
+def test_weight_rows_past_a_decode_launch_go_to_the_general_kernels(op, K, G):
+    """16 threads a weight row, fewer than 2^32 in a launch (the general kernels take several)."""
+    most = 16 * ((2 ** 32 - 1) // 256)
+    assert q4.q4_route_plan(op, 1, most, K, G, cus=256)["path"] == "gemv"
+    assert q4.q4_route_plan(op, 1, most + 1, K, G, cus=256)["path"] == "generic"
