@@ -6,10 +6,11 @@ in that library's host code or HIP kernels.  torch provides device memory and
 the current stream; outputs are allocated here with torch.  The MX FP4 and
 query/key calls, whose small sizes cost more here than on the GPU, go through
 ``lib/q4_torch.so`` first, which does the same in C++ (a call of 6 to 11 us
-takes about 4).
+takes about 4); where that file is missing or was built for another torch or
+Python, they warn once and go through ctypes like the others.
 
 The library must be built first (``python -m int4_dequantize_matmul_amd.build``);
-importing the compute functions without it raises, there is no fallback.
+calling the compute functions without it raises, there is no fallback.
 """
 from __future__ import annotations
 
@@ -17,6 +18,8 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sys
+import warnings
 
 import numpy as np
 import torch  # loaded before libq4 so both share torch's HIP runtime
@@ -111,21 +114,40 @@ TORCH_LIB_PATH = os.path.join(_PKG, "lib", "q4_torch.so")
 _DIRECT = None
 
 
+class _NoDirect:
+    """In the place of lib/q4_torch.so: takes nothing."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _load_direct():
+    lib = _lib()
+    if not os.path.exists(TORCH_LIB_PATH):
+        raise ImportError(f"{TORCH_LIB_PATH} is not built")
+    loader = importlib.machinery.ExtensionFileLoader("q4_torch", TORCH_LIB_PATH)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader("q4_torch", loader))
+    loader.exec_module(m)
+    here = f"torch {torch.__version__.split('+')[0]}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+    if m.built_for != here:
+        raise ImportError(f"{TORCH_LIB_PATH} was built for {m.built_for}, this is {here}")
+    m.bind(torch._C._cuda_getCurrentRawStream,
+           {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _SIG if "_mx" in n or "_qk_" in n})
+    return m
+
+
 def _direct():
     """lib/q4_torch.so, bound to the entry points of the library in use.  Its
     functions return None for arguments that they do not take as they are;
     the functions here then check them, and say what is wrong."""
     global _DIRECT
     if _DIRECT is None:
-        if not os.path.exists(TORCH_LIB_PATH):
-            raise RuntimeError(f"{TORCH_LIB_PATH} is not built: run `python -m int4_dequantize_matmul_amd.build`")
-        loader = importlib.machinery.ExtensionFileLoader("q4_torch", TORCH_LIB_PATH)
-        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("q4_torch", loader))
-        loader.exec_module(m)
-        lib = _lib()
-        m.bind(torch._C._cuda_getCurrentRawStream,
-               {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _SIG if "_mx" in n or "_qk_" in n})
-        _DIRECT = m
+        try:
+            _DIRECT = _load_direct()
+        except ImportError as e:
+            warnings.warn(f"MX FP4 and query/key calls go through ctypes, which takes some microseconds more: {e}; "
+                          "run `python -m int4_dequantize_matmul_amd.build`", RuntimeWarning, stacklevel=3)
+            _DIRECT = _NoDirect()
     return _DIRECT
 
 

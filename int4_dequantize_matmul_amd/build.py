@@ -1,6 +1,11 @@
 """Build libq4.so in-tree: hipcc for the gfx950 kernels, g++ for host code.
 
     python -m int4_dequantize_matmul_amd.build
+    python int4_dequantize_matmul_amd/build.py      (the same, without the package)
+
+Where torch can be imported, g++ also compiles the Python binding's small-call
+path against its headers (lib/q4_torch.so); libq4.so needs neither torch nor
+Python.
 
 Every HIP file is compiled with -ffp-contract=off (no implicit FMA) and
 with the packed-FP32 instructions switched off; the host quantizers are
@@ -43,11 +48,14 @@ def _run(cmd):
     return out
 
 
-def _torch_binding(out: str) -> list:
-    """The compile of csrc/binding/q4_torch.cpp against the installed torch."""
+def _torch_binding(out: str) -> list | None:
+    """The compile of csrc/binding/q4_torch.cpp against the installed torch, if there is one."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return None
     root = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
            os.path.join(root, "include", "torch", "csrc", "api", "include")]
@@ -68,19 +76,26 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         jobs.append(["g++", *CXX_FLAGS, "-c", src, "-o", obj])
     objs = [j[-1] for j in jobs]
-    jobs.append(_torch_binding(TORCH_LIB + ".tmp"))
+    binding = _torch_binding(TORCH_LIB + ".tmp")
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        for out in ex.map(_run, jobs):
+        results = [ex.submit(_run, j) for j in jobs]
+        bound = ex.submit(_run, binding) if binding else None
+        for r in results:
+            out = r.result()
             if verbose and out.strip():
                 print(out)
-    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
-    tmp = LIB + ".tmp"
-    _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
-    probe_src = os.path.join(CSRC, "probe", "q4_probe.hip")
-    tmp = PROBE_LIB + ".tmp"
-    _run([HIPCC, *HIP_FLAGS, "-shared", "-o", tmp, probe_src])
-    os.replace(tmp, PROBE_LIB)
+        tmp = LIB + ".tmp"
+        _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
+        os.replace(tmp, LIB)
+        probe_src = os.path.join(CSRC, "probe", "q4_probe.hip")
+        tmp = PROBE_LIB + ".tmp"
+        _run([HIPCC, *HIP_FLAGS, "-shared", "-o", tmp, probe_src])
+        os.replace(tmp, PROBE_LIB)
+        if bound:
+            bound.result()
+            os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+        else:
+            print("no torch: libq4.so is built, the Python binding's lib/q4_torch.so is not")
     return LIB
 
 

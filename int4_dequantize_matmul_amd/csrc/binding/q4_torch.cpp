@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/headeronly/version.h>
 
 #include <cstdint>
 
@@ -227,4 +228,15 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "q4_torch", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_q4_torch() { return PyModule_Create(&module); }
+// built_for: the torch and Python whose headers this was compiled with; the
+// binding does not call a module that was built for others.
+PyMODINIT_FUNC PyInit_q4_torch() {
+  PyObject *m = PyModule_Create(&module);
+  PyObject *v = m ? PyUnicode_FromFormat("torch %d.%d.%d, Python %d.%d", TORCH_VERSION_MAJOR, TORCH_VERSION_MINOR,
+                                         TORCH_VERSION_PATCH, PY_MAJOR_VERSION, PY_MINOR_VERSION)
+                  : nullptr;
+  const bool ok = v && PyObject_SetAttrString(m, "built_for", v) == 0;
+  Py_XDECREF(v);
+  if (!ok) Py_CLEAR(m);
+  return m;
+}
