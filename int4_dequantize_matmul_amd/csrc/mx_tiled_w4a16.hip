@@ -10,8 +10,9 @@
 // 16 g .. 16 g + 15 of row r, 8 for each of two matrix instructions (which sum
 // over whatever columns their lanes hold), all in block g / 2 of the stage's
 // two.  Loads that write LDS bring activations three stages ahead, weights by
-// pairs of stages and scales by up to eight: what these loads cost is the
-// rows they touch, not the bytes, so a row's bytes come many at a time.
+// pairs of stages and scales by pairs or (in the large tiles) by eight: what
+// these loads cost is the rows they touch, not the bytes, so a row's bytes come
+// many at a time.
 // Activation rows that do not start on 16 bytes go through registers.
 //
 // Measured: 2048 x 13312 x 2048 89 us (1.26 PFLOP/s; a library bf16 product of
@@ -39,14 +40,14 @@ struct TileArgs {
 };
 
 // LDS of a group of waves: three stages of activation rows of 128 bytes; two
-// pairs of stages of weight rows of 64 bytes; two buffers of scales.  SB: the
-// bytes of a row's scales that one lane loads: 16 (eight stages; rows of
-// scales that start on 16 bytes), 4 (a pair of stages), 1 (any rows; slots of
-// 4 bytes).
+// pairs of stages of weight rows of 64 bytes; two buffers of the scales of a
+// pair.  SB: the bytes of a row's scales that one lane loads: 4 (rows of scales
+// that start on 4 bytes), 1 (any rows; slots of 4 bytes).
 template <int BN, int BM, int SB>
 struct Lds {
   static constexpr int x = 0, x_stage = BM * 128;
   static constexpr int w = x + 3 * x_stage, w_pair = BN * 64;
+  static_assert(SB == 4 || SB == 1, "scales by the dword or by the byte");
   static constexpr int s = w + 2 * w_pair, s_row = SB == 4 ? 4 : 16, s_buf = BN * s_row;
   static constexpr int bytes = s + 2 * s_buf;
 };
@@ -111,10 +112,9 @@ __device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t
       dma16(rs_w, lds0 + L::w + (d & 1) * L::w_pair + t * 1024, b < KB ? (row_of(t, lane >> 2) * KB + b) * 16 : kFar, 0);
     }
   };
-  // Scales, for the pair d and (SB = 16) the three after it.
-  auto issue_s = [&](int d) {
+  auto issue_s = [&](int d) {   // the scales of pair d
     const int b = 2 * first + 4 * d;
-    const uint32_t to = lds0 + L::s + ((SB == 16 ? d >> 2 : d) & 1) * L::s_buf;
+    const uint32_t to = lds0 + L::s + (d & 1) * L::s_buf;
     if constexpr (SB == 1) {
       // lane i: byte i % 4 of row i / 4
       const int i = b + (lane & 3);
@@ -126,8 +126,7 @@ __device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t
     } else if (wv < BN / 64) {   // a row a lane
       static_assert(BN / 64 <= NW, "a load a wave");
       const int o = b < KB ? row_of(4 * wv + g, r) * KB + b : kFar;
-      if constexpr (SB == 16) dma16(rs_s, to + wv * 1024, o, 0);
-      else dma4(rs_s, to + wv * 256, o, 0);
+      dma4(rs_s, to + wv * 256, o, 0);
     }
   };
   // Activations through registers (XAL false); rows past the end are the last
@@ -171,8 +170,8 @@ __device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t
   auto read_w = [&](Weights &f, int s) {   // s: stage of the group
     const int blk = 2 * (s & 1) + (g >> 1);
     const uint8_t *w = smem + L::w + ((s >> 1) & 1) * L::w_pair + TN * wn * 1024 + r * 64 + ((blk ^ (r >> 2)) << 4) + 8 * (g & 1);
-    const uint8_t *sc = smem + L::s + ((SB == 16 ? s >> 3 : s >> 1) & 1) * L::s_buf + (TN * wn * 16 + r) * L::s_row +
-                        (SB == 16 ? 2 * (s & 7) + (g >> 1) : SB == 4 ? blk : 4 * blk);
+    const uint8_t *sc = smem + L::s + ((s >> 1) & 1) * L::s_buf + (TN * wn * 16 + r) * L::s_row +
+                        (SB == 4 ? blk : 4 * blk);
 #pragma unroll
     for (int t = 0; t < TN; ++t) {
       f.c[t] = *reinterpret_cast<const uint2 *>(w + t * 1024);
@@ -196,7 +195,7 @@ __device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t
   uint4 x0[TM], x1[TM];
   Weights w0, w1;
   issue_s(0);
-  if constexpr (SB != 16) issue_s(1);
+  issue_s(1);
   issue_w(0);
   if constexpr (XAL) {
     issue_x(0, first);
@@ -229,10 +228,7 @@ __device__ __forceinline__ void tile_body(const TileArgs &a, int64_t m0, int64_t
       put(c == 0 ? 2 : c - 1);   // stage s + 2
     }
     lds_barrier();
-    if constexpr (ODD) {
-      if constexpr (SB != 16) issue_s((s >> 1) + 2);
-      else if ((s & 7) == 1) issue_s(4 * ((s >> 3) + 1));
-    }
+    if constexpr (ODD) issue_s((s >> 1) + 2);
     if constexpr (XAL) issue_x(c, first + s + 3);
     if constexpr (ODD) issue_w((s >> 1) + 2);
     if constexpr (!XAL) fetch(first + s + 3);
@@ -459,7 +455,7 @@ hipError_t go_large(TileArgs a, int cus, hipStream_t st) {
 // a cut of K, three and more a CU (the same at 256 rows: 19.1 against 21.7).
 template <bool XAL, int SB, bool BOUT>
 hipError_t pick(const TileArgs &a, hipStream_t st) {
-  constexpr int SK = SB == 16 ? 4 : SB;
+  constexpr int SK = SB == 1 ? 1 : 4;   // of the tiles that do not take scales 16 at a time
   const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
   const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   if (tiles(32, 64) <= cus) return go<4, 4, 2, 2, 1, XAL, SK, BOUT>(a, st);
