@@ -23,6 +23,7 @@
 
 #include "kernels.hpp"
 #include "mx_device.hpp"
+#include "mx_plan.hpp"
 #include "mx_tile.hpp"
 #include "q4_lds_dma.hpp"
 
@@ -443,27 +444,20 @@ hipError_t go_large(TileArgs a, int cus, hipStream_t st) {
   return launch<mx_large_w4a16<SB, BOUT>, LargeLds<256, 128, SB>::bytes>(a, a.whole + 4 * (tiles - a.whole), 256, st);
 }
 
-// The smallest tile whose grid the CUs take at once, its K shared out among
-// the waves (a workgroup's time is its stages' latencies then); past that the
-// large tiles.  Microseconds on 256 CUs, smaller tile | larger tile:
-//   N 2048 K 5632: 32 x 64 up to 256 rows (14.7 | 19.3), 64 x 64 at 512
-//     (21.2 | 26.8), 64 x 128 at 1024 (28.3 | 35.0)
-//   N 13312 K 2048: 32 x 64 at 32 rows (8.1 | 9.2), 64 x 64 at 64 (9.6 |
-//     12.0), 64 x 128 at 128 (12.6 | 15.5)
-// Between them and one round of 128 x 256: 128 x 128 where those are more than
-// the CUs (N 13312 K 2048, 512 rows: 30.6 against 35.2), else 64 x 128 without
-// a cut of K, three and more a CU (the same at 256 rows: 19.1 against 21.7).
 template <bool XAL, int SB, bool BOUT>
 hipError_t pick(const TileArgs &a, hipStream_t st) {
   constexpr int SK = SB == 1 ? 1 : 4;   // of the tiles that do not take scales 16 at a time
-  const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
-  const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  if (tiles(32, 64) <= cus) return go<4, 4, 2, 2, 1, XAL, SK, BOUT>(a, st);
-  if (tiles(64, 64) <= cus) return go<2, 4, 2, 2, 2, XAL, SK, BOUT>(a, st);
-  if (tiles(64, 128) <= cus) return go<2, 4, 4, 2, 4, XAL, SK, BOUT>(a, st);
-  if constexpr (XAL && SB > 1)
-    if (tiles(128, 256) >= cus || tiles(128, 128) <= cus) return go_large<SB, BOUT>(a, static_cast<int>(cus), st);
-  return go<1, 4, 4, 2, 8, XAL, SK, BOUT>(a, st);
+  constexpr bool large = XAL && SB > 1;
+  const int cus = device_cu_count() > 0 ? device_cu_count() : 256;
+  switch (mx_w4a16_tile(a.M, a.N, cus, large)) {
+    case MxW4A16Tile::k32x64: return go<4, 4, 2, 2, 1, XAL, SK, BOUT>(a, st);
+    case MxW4A16Tile::k64x64: return go<2, 4, 2, 2, 2, XAL, SK, BOUT>(a, st);
+    case MxW4A16Tile::k64x128: return go<2, 4, 4, 2, 4, XAL, SK, BOUT>(a, st);
+    case MxW4A16Tile::kLarge:
+      if constexpr (large) return go_large<SB, BOUT>(a, cus, st);
+      return hipErrorInvalidValue;   // not chosen
+    default: return go<1, 4, 4, 2, 8, XAL, SK, BOUT>(a, st);
+  }
 }
 
 }  // namespace

@@ -20,6 +20,7 @@
 
 #include "kernels.hpp"
 #include "mx_device.hpp"
+#include "mx_plan.hpp"
 #include "mx_tile.hpp"
 #include "q4_lds_dma.hpp"
 
@@ -288,21 +289,14 @@ hipError_t go(TileArgs a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The smallest tile whose grid the CUs take at once, its K shared out among
-// the waves (a workgroup's time is its stages' latencies then); past that
-// 128 x 128, two workgroups a CU, and 256 x 256 once those fill three quarters
-// of the CUs.  Microseconds on 256 CUs, smaller tile | larger tile:
-//   N 2048 K 5632: 32 x 64 at 256 rows (9.4 | 10.6), 64 x 64 at 512 (11.4 | 15.0)
-//   N 13312 K 2048: 64 x 64 at 64 rows (6.6 | 7.4), 128 x 128 at 512 (14.4 |
-//     19.1), 256 x 256 at 1024 (24.6 | 22.3)
 template <bool S16, bool BOUT>
 hipError_t pick(const TileArgs &a, hipStream_t st) {
-  const int64_t cus = device_cu_count() > 0 ? device_cu_count() : 256;
-  const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  if (tiles(32, 64) <= cus) return go<4, 2, 2, 1, 1, false, BOUT>(a, st);
-  if (tiles(64, 64) <= cus) return go<2, 4, 2, 1, 1, false, BOUT>(a, st);
-  if (4 * tiles(256, 256) >= 3 * cus) return go<1, 8, 2, 4, 2, S16, BOUT>(a, st);
-  return go<1, 4, 2, 2, 2, S16, BOUT>(a, st);
+  switch (mx_w4a4_tile(a.M, a.N, device_cu_count() > 0 ? device_cu_count() : 256)) {
+    case MxW4A4Tile::k32x64: return go<4, 2, 2, 1, 1, false, BOUT>(a, st);
+    case MxW4A4Tile::k64x64: return go<2, 4, 2, 1, 1, false, BOUT>(a, st);
+    case MxW4A4Tile::k256x256: return go<1, 8, 2, 4, 2, S16, BOUT>(a, st);
+    default: return go<1, 4, 2, 2, 2, S16, BOUT>(a, st);
+  }
 }
 
 }  // namespace
