@@ -289,6 +289,12 @@ q4_status q8_linear_w8a16(const uint16_t *x_bf16, const int8_t *wq, const float 
  * stands for 2^(s - 127); 255 is NaN.  Codes past column K of a row's last
  * block are 0.  Arrays: codes uint8 [rows, 16 B], 16-byte aligned (EINVAL
  * otherwise); scales uint8 [rows, B].
+ *
+ * Sizes: up to 2^30 rows of up to 2^30 columns, in products up to 1048560
+ * activation rows; more is ESHAPE.  Routes: the products have kernels for few
+ * rows (Q4_PATH_GEMV) and LDS-tiled ones (Q4_PATH_TILED) and no general ones:
+ * any forced route but TILED takes the kernels for few rows.  q4_route_plan
+ * does not cover them.
  * ---------------------------------------------------------------------- */
 
 /* Quantize rows.  x: [M, K] f32 or bf16 (xt).  Per block, with t = max|x|:
@@ -329,8 +335,9 @@ q4_status q4_linear_w4a4_mx_dynamic(const void *x, q4_dtype xt, const uint8_t *w
                                     size_t ws_bytes, void *stream);
 
 /* y = x W^T with bf16 x [M, K] and MX FP4 weights, summed in f32 and rounded
- * once to f32 or bf16 (yt).  The weights are exact in bf16, so the matrix
- * products see them unrounded.  Any K >= 0. */
+ * once to f32 or bf16 (yt).  Weights below 2^128 are exact in bf16, the
+ * smallest (2^-128) included, so the matrix products see them unrounded; larger
+ * ones, possible with scales above 252, count as infinity.  Any K >= 0. */
 q4_status q4_linear_w4a16_mx(const uint16_t *x_bf16, const uint8_t *wq, const uint8_t *sw, void *y,
                              q4_dtype yt, int64_t M, int64_t N, int64_t K, void *stream);
 
@@ -365,8 +372,8 @@ q4_status q4_qk_norm_rope(const void *q, int64_t q_token, int64_t q_head, const 
 
 /* Process-wide route override for A/B tests and benchmarks ([int8] "Tier
  * law": routes are chosen by measurement and can be forced).  A forced route
- * that cannot serve a shape falls back to the generic kernels.  EINVAL for
- * an unknown value. */
+ * that cannot serve a shape falls back to the generic kernels (MX FP4
+ * products: to their kernels for few rows).  EINVAL for an unknown value. */
 q4_status q4_set_path(q4_path path);
 q4_path q4_get_path(void);
 
