@@ -18,12 +18,15 @@ inline int64_t mx_tiles(int64_t M, int64_t N, int64_t bm, int64_t bn) {
 //   N 2048 K 5632: 32 x 64 at 256 rows (9.4 | 10.6), 64 x 64 at 512 (11.4 | 15.0)
 //   N 13312 K 2048: 64 x 64 at 64 rows (6.6 | 7.4), 128 x 128 at 512 (14.4 |
 //     19.1), 256 x 256 at 1024 (24.6 | 22.3)
+// large: not for f32 results whose scales do not start on 16 bytes: 256 x 256
+// would spill 142 of its registers there (2048 rows, N 13312 K 2080: 169 us
+// against 87 with 128 x 128; 8192 rows, N 2048 K 5600: 194 against 103).
 enum class MxW4A4Tile : int { k32x64, k64x64, k128x128, k256x256 };
 
-inline MxW4A4Tile mx_w4a4_tile(int64_t M, int64_t N, int64_t cus) {
+inline MxW4A4Tile mx_w4a4_tile(int64_t M, int64_t N, int64_t cus, bool large) {
   if (mx_tiles(M, N, 32, 64) <= cus) return MxW4A4Tile::k32x64;
   if (mx_tiles(M, N, 64, 64) <= cus) return MxW4A4Tile::k64x64;
-  if (4 * mx_tiles(M, N, 256, 256) >= 3 * cus) return MxW4A4Tile::k256x256;
+  if (large && 4 * mx_tiles(M, N, 256, 256) >= 3 * cus) return MxW4A4Tile::k256x256;
   return MxW4A4Tile::k128x128;
 }
 

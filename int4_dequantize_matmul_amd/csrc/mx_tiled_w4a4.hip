@@ -291,10 +291,13 @@ hipError_t go(TileArgs a, hipStream_t st) {
 
 template <bool S16, bool BOUT>
 hipError_t pick(const TileArgs &a, hipStream_t st) {
-  switch (mx_w4a4_tile(a.M, a.N, device_cu_count() > 0 ? device_cu_count() : 256)) {
+  constexpr bool large = S16 || BOUT;
+  switch (mx_w4a4_tile(a.M, a.N, device_cu_count() > 0 ? device_cu_count() : 256, large)) {
     case MxW4A4Tile::k32x64: return go<4, 2, 2, 1, 1, false, BOUT>(a, st);
     case MxW4A4Tile::k64x64: return go<2, 4, 2, 1, 1, false, BOUT>(a, st);
-    case MxW4A4Tile::k256x256: return go<1, 8, 2, 4, 2, S16, BOUT>(a, st);
+    case MxW4A4Tile::k256x256:
+      if constexpr (large) return go<1, 8, 2, 4, 2, S16, BOUT>(a, st);
+      return hipErrorInvalidValue;   // not chosen
     default: return go<1, 4, 2, 2, 2, S16, BOUT>(a, st);
   }
 }

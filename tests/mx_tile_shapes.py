@@ -24,13 +24,24 @@ K_W4A16 = {"scales by 16": 1536, "scales by 4": 1408, "scales by 1": 1432, "rows
            "odd": 37}
 
 
+def large_w4a4(K, yt):
+    """Whether 256 x 256 tiles are allowed: not for f32 results with scales at any address."""
+    return yt == "bf16" or -(-K // 32) % 16 == 0
+
+
 def variants_w4a4():
-    """(tile, scales by 16 bytes) that pick() in mx_tiled_w4a4.hip can choose."""
-    return {(t, s) for t in W4A4 for s in (False, True) if t in ("k128x128", "k256x256") or not s}
+    """(tile, scales by 16 bytes, result type) that pick() in mx_tiled_w4a4.hip can choose."""
+    return {(t, s, yt) for t in W4A4 for s in (False, True) for yt in ("f32", "bf16")
+            if (t in ("k128x128", "k256x256") or not s) and (t != "k256x256" or s or yt == "bf16")}
 
 
-def variant_w4a4(tile, K):
-    return tile, tile in ("k128x128", "k256x256") and -(-K // 32) % 16 == 0
+def tile_w4a4(tile, K, yt):
+    return "k128x128" if tile == "k256x256" and not large_w4a4(K, yt) else tile
+
+
+def variant_w4a4(tile, K, yt):
+    tile = tile_w4a4(tile, K, yt)
+    return tile, tile in ("k128x128", "k256x256") and -(-K // 32) % 16 == 0, yt
 
 
 def variants_w4a16():
