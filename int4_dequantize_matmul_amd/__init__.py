@@ -512,6 +512,15 @@ def _same_device(*tensors):
             raise ValueError(f"tensors on different devices: {tensors[0].device} and {t.device}")
 
 
+def _workspace(ws, like: torch.Tensor):
+    """Checks a given workspace: device memory without gaps, next to `like`."""
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda:
+        raise TypeError("ws must be a CUDA (HIP) tensor")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    _same_device(like, ws)
+
+
 def _out(y, M: int, N: int, dtype: str, like: torch.Tensor):
     """The output tensor: y if given (checked), else a new one."""
     if y is None:
@@ -600,6 +609,8 @@ def q4_linear_w4a4_mx_dynamic(x, wq, sw, dtype: str = "bf16", ws=None, y=None):
     if M and N:
         if ws is None:
             ws = torch.empty(q4_w4a4_mx_dynamic_workspace(M, K), dtype=torch.uint8, device=x.device)
+        else:
+            _workspace(ws, x)
         _check("q4_linear_w4a4_mx_dynamic",
                _lib().q4_linear_w4a4_mx_dynamic(_ptr(x), _dt(x), _ptr(wq), _ptr(sw), _ptr(y), DT[dtype], M, N, K,
                                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(x)))

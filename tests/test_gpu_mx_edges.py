@@ -150,3 +150,17 @@ def test_calls_follow_the_current_stream(M, N, K):
         ref, mag = X.qk_norm_rope(x[:, :4 * D].reshape(M, 4, D), None, angles[:, :D // 2], angles[:, D // 2:], 1e-6, True)
         for t in (k, q):
             assert np.all(np.abs(values(t) - ref) <= (D / 2 + 16) * 2.0 ** -24 * mag)
+
+
+def test_given_workspaces():
+    """Host memory and strided views are refused; a longer one of another type serves."""
+    x = torch.randn(40, 64, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    c, s = q4.q4_mx_quantize_rows(x[:8])
+    need = q4.q4_w4a4_mx_dynamic_workspace(40, 64)
+    for ws in (torch.empty(need, dtype=torch.uint8), np.empty(need, np.uint8), need):
+        with pytest.raises(TypeError):
+            q4.q4_linear_w4a4_mx_dynamic(x, c, s, ws=ws)
+    with pytest.raises(ValueError):
+        q4.q4_linear_w4a4_mx_dynamic(x, c, s, ws=torch.empty(2 * need, dtype=torch.uint8, device=DEV)[::2])
+    y = q4.q4_linear_w4a4_mx_dynamic(x, c, s, "f32", ws=torch.empty(need, dtype=torch.float32, device=DEV))
+    assert_bitwise(host(y), host(q4.q4_linear_w4a4_mx_dynamic(x, c, s, "f32")))

@@ -108,3 +108,28 @@ def test_python_checks_need_device_tensors():
         with pytest.raises(TypeError):
             call()
     assert np.all(u.numpy() == 0)
+
+
+class _Recorder:
+    """In the place of the library: every call is noted and succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append(name) or 0
+
+
+def test_a_workspace_has_to_be_contiguous_device_memory(monkeypatch):
+    """A host tensor's address, or a strided view's, never reaches the kernels."""
+    import torch
+    lib = _Recorder()
+    monkeypatch.setattr(q4, "_dev", lambda t, *rest: t)       # host tensors stand in for the other arguments
+    monkeypatch.setattr(q4, "_direct", lambda: None)
+    monkeypatch.setattr(q4, "_lib", lambda: lib)
+    monkeypatch.setattr(q4, "_stream", lambda t: 0)
+    x, w, s = torch.zeros(20, 32), torch.zeros(3, 16, dtype=torch.uint8), torch.zeros(3, 1, dtype=torch.uint8)
+    for ws in (torch.zeros(4096, dtype=torch.uint8), np.zeros(4096, np.uint8), 4096):
+        with pytest.raises(TypeError):
+            q4.q4_linear_w4a4_mx_dynamic(x, w, s, ws=ws)
+    assert not lib.calls
