@@ -11,9 +11,10 @@
 // long run of blocks and no lane is idle; otherwise each row is cut by itself
 // and its last, short run is read element by element.
 //
-// Measured: 8192 x 5632 bf16 to codes 19.8 us (117 MB, 5.9 TB/s; a copy of 2 GiB
-// runs at 5.2); 2048 x 5632 6.9 us there and 6.1 us back; 2048 x 1023 f32, rows
-// cut one by one, 3.9 and 4.7 us.
+// Measured, from memory | input met just before: 8192 x 5632 bf16 to codes 24 to
+// 26 us (117 MB, 4.5 to 4.9 TB/s; a copy of 1 GiB runs at 5.2) | 19.7; 2048 x 5632
+// 8.7 | 7.0 us there and 6.6 | 6.9 back; 2048 x 1023 f32, rows cut one by one,
+// 5.0 | 4.0 and 4.8 | 4.9 us.
 #include "kernels.hpp"
 #include "mx_device.hpp"
 

@@ -12,11 +12,12 @@
 // two.  Loads that write LDS bring activations three stages ahead, weights by
 // pairs of stages and scales by pairs or (in the large tiles) by eight: what
 // these loads cost is the rows they touch, not the bytes, so a row's bytes come
-// many at a time.
-// Activation rows that do not start on 16 bytes go through registers.
+// many at a time.  Activation rows that do not start on 16 bytes go through
+// registers.
 //
-// Measured: 2048 x 13312 x 2048 89 us (1.26 PFLOP/s; a library bf16 product of
-// that shape, weights unpacked before, 87), 2048 x 8192 x 4096 106 us (1.29).
+// Measured: 2048 x 13312 x 2048 89 to 93 us (1.2 to 1.26 PFLOP/s; a library bf16
+// product of that shape, weights unpacked before, 87), 2048 x 8192 x 4096 106 us
+// (1.29).
 // A stage of a workgroup takes 1900 clocks of which 1100 are its matrix
 // instructions; two workgroups a CU fill some of the rest.
 #include <type_traits>

@@ -12,10 +12,11 @@
 // instructions deep: in step q lane (r, h) takes block 4 h + q of row r, whose
 // scale is byte q of a dword.
 //
-// Measured: 2048 x 13312 x 2048 38 us (2.9 PFLOP/s), 8192 x 2048 x 5632 49 us (3.9
-// PFLOP/s; the instruction alone 8.2).  In the second one a stage takes 3100
-// clocks of which the matrix instructions need 2400; the first loads, the
-// stores and the launch take 12 us more.
+// Measured, operands met just before | from memory: 2048 x 13312 x 2048 38 us
+// (2.9 PFLOP/s) | 45, 8192 x 2048 x 5632 50 us (3.8 PFLOP/s; the instruction alone
+// 8.2) | 53.  In the second one a stage takes 3100 clocks of which the matrix
+// instructions need 2400; the first loads, the stores and the launch take 12 us
+// more.
 #include <type_traits>
 
 #include "kernels.hpp"

@@ -662,10 +662,19 @@ uint64_t size_of(int dt) { return dt == Q4_DT_BF16 ? 2 : 4; }
 bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 // Up to this many rows the dynamic call forms the activations' codes inside
-// the product.
+// the product (inside | by a launch of its own before it, us, bf16 rows):
+//   N 2048 K 2048: one row 2.8 | 4.3, 16 rows 4.8 | 5.1
+//   N 13312 K 2048: one row 4.6 | 6.3, 8 rows 6.2 | 7.3, 16 rows 8.5 | 8.1, 32
+//     rows 12.8 | 8.3
+//   N 2048 K 5632: one row 4.6 | 6.0, 4 rows 5.5 | 6.2, 5 rows 6.9 | 6.2, 16
+//     rows 9.9 | 6.9
+// (so above K 2048 a launch of its own is faster from 5 rows on, which this rule
+// does not know).
 constexpr int64_t kMxFusedMaxM = 16;
 // Up to this many rows a product of N weight rows runs by blocks of 16 weight
-// rows, which reads the activations again for each block (blocks | tiles, us):
+// rows, which reads the activations again for each block (blocks | tiles, us).
+// K moves the border little and is left out: at most 1.6 us of what was measured
+// (W4A4, N 2048 K 8192, 64 rows 14.2 | 12.6; K 2048 5.1 | 5.6).
 // W4A4: N 2048 K 2048, 128 rows 5.1 | 5.6, 192 rows 7.5 | 5.7; K 5632, 128 rows
 //   9.0 | 8.6; N 512 K 1024, 256 rows 3.6 | 4.5; N 4096 K 1003, 64 rows 3.7 |
 //   4.6; N 13312 K 2048, 32 rows 8.3 | 5.9.

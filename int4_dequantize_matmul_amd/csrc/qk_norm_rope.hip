@@ -16,9 +16,10 @@
 // more than 64 units take turns over them, and read their row a second time
 // for the result.
 //
-// Measured: 8190 tokens of 32 + 8 heads of 128 in bf16 32 us (172 MB, 5.4 TB/s);
-// one token 3.1 us.  Where only 1 or 2 columns a unit are possible the number
-// of loads bounds it: 4096 tokens of 40 heads of 130 88 us (1 TB/s).
+// Measured, from memory | input met just before: 8190 tokens of 32 + 8 heads of
+// 128 in bf16 41 us (172 MB, 4.2 TB/s) | 32; one token 4.4 | 3.2 us.  Where only 1
+// or 2 columns a unit are possible the number of loads bounds it: 4096 tokens of
+// 40 heads of 130 88 us (1 TB/s).
 #include "kernels.hpp"
 #include "mx_device.hpp"
 
