@@ -370,6 +370,133 @@ q4_status q4_qk_norm_rope(const void *q, int64_t q_token, int64_t q_head, const 
                           q4_dtype yt, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t P,
                           float eps, q4_rope_pairs pairs, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Between the linears of a decoder layer: rows normalised to int8, a paged
+ * 8-bit cache of keys and values, and the attention that reads it.
+ * ---------------------------------------------------------------------- */
+
+/* Rows in front of int8 linears (q4_linear_w4a8, q8_linear_w8a8) in one pass:
+ *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * gain,
+ *   scale = max|y| / 127,  code = y / scale, rounded to the nearest, ties to even.
+ *   x, residual: [M, K] f32 or bf16 (xt); residual may be NULL (h = x).
+ *   gain: [K] f32 or bf16 (gt), NULL for 1.
+ *   sum: [M, K] of type xt, NULL or, with a residual, h in f32 rounded once; it
+ *     may be x or residual itself.
+ *   xq: [M, K], sx: [M] as in q8_quantize_rows.
+ * The root cancels out of y / scale, so a code is that of the exact h gain /
+ * max|h gain| (with h rounded to 53 bits); sums are f32 and sx is accurate to
+ * 1e-6 of itself.  A row of zeros gives scale 0 and codes 0; one with a NaN or
+ * an infinity, or whose sum of squares or products pass the range of f32, scale
+ * NaN and codes 0.  EINVAL also for eps < 0 or NaN, or a sum without a
+ * residual; ESHAPE for M or K beyond 2^30. */
+q4_status q8_rmsnorm_rows(const void *x, const void *residual, q4_dtype xt, const void *gain, q4_dtype gt, float eps,
+                          int64_t M, int64_t K, void *sum, int8_t *xq, float *sx, void *stream);
+
+#define Q8_KV_BLOCK 16
+#define Q8_KV_MAX_D 256
+
+/* A paged cache of keys and values in 8 bits (device pointers; the struct
+ * itself is the host's, read before a call returns).
+ * A page holds `page` tokens (a power of two from 16 to 65536) of each of
+ * `heads` key heads, cut into blocks of 16 tokens; a block of a head has one
+ * scale byte b for its keys and one for its values, which stand for 2^(b - 127)
+ * (255: the whole block is NaN).  D, the numbers of a head, is a multiple of 16
+ * up to Q8_KV_MAX_D.
+ *   k: int8 [n_pages, heads, page/16, D/16, 16 tokens, 16 columns], 16-byte aligned
+ *   v: int8 [n_pages, heads, page/16, D, 16 tokens], 16-byte aligned
+ *   k_scale, v_scale: uint8 [n_pages, heads, page/16]
+ *   pages: int32 [sequences, table]: tokens p page .. p page + page - 1 of
+ *     sequence i are on page pages[i, p] of the pool.  Entries past a sequence's
+ *     last page are not looked at.
+ * n_pages heads page / 16 is at most 2^31 - 1.
+ *
+ * The calls on a cache take `sequences` sequences with T rows in all (a row a
+ * token): starts, int32 [sequences + 1], does not decrease; rows starts[i] ..
+ * starts[i + 1] - 1 are the last tokens of sequence i, which has lengths[i]
+ * (int32 [sequences]) tokens with them, so that row starts[i] + t stands at
+ * position lengths[i] - (starts[i + 1] - starts[i]) + t.  Rows of no sequence,
+ * in front of starts[0] or behind the last sequence, are not read and their
+ * results are left as they were.  Both arrays are the device's and are not
+ * checked on the host: what they and the table say is kept within the buffers.
+ * Tokens on a page that is not in the table or not in the pool read as NaN and
+ * are dropped when written.  ESHAPE: the sizes above, heads, n_pages or table
+ * < 1, T or sequences beyond 2^31 - 1. */
+typedef struct {
+  int8_t *k, *v;
+  uint8_t *k_scale, *v_scale;
+  const int32_t *pages;
+  int64_t n_pages, page, heads, D;
+  int64_t sequences, table;
+} q8_kv_cache;
+
+/* New tokens into the cache, and their queries beside them, in one launch.
+ *   k, v: T rows of `heads` heads of D numbers, f32 or bf16 (xt), strided as in
+ *     q4_qk_norm_rope (slices of a fused projection); q: T rows of Hq heads,
+ *     Hq == 0 for none (q and q_out may then be NULL).
+ *   norm != 0: keys and queries become x / sqrt(mean(x^2) + eps) * gain per
+ *     head; k_gain, q_gain: [D], f32 or bf16 (gt), NULL for 1.
+ *   cos_sin: f32 [P, R] as in q4_qk_norm_rope; the first R columns of a key or
+ *     query are rotated by its position's row, after the norm.  NULL: no
+ *     rotation.  A position not in 0 .. P - 1 gives NaN in the rotated columns.
+ *   q_out: [T, Hq, D] f32 or bf16 (yt), computed in f32, rounded once.
+ * Keys are computed in f64.  The scale of a block is the smallest power of two
+ * 2^e, e >= -127, with max|x| <= 127 2^e; codes are x / 2^e rounded to the
+ * nearest, ties to even.  Where a block has tokens in front of the first new
+ * one, its scale is at least what it was, and their codes are rounded to a
+ * larger one (each doubling rounds once more, so less than one step of the last
+ * scale in all); other content of the block is forgotten.  A NaN or an infinity
+ * makes its block NaN until the block's first token is written again.  A block
+ * that is written belongs to one sequence: two that write the same one at a time
+ * give undefined codes.  Tokens at positions below 0 (more rows than tokens) are
+ * dropped.
+ * EINVAL also for eps < 0 or NaN with norm, a negative stride, or an output (the
+ * cache's four arrays and q_out) overlapping an input or another output; ESHAPE
+ * also for R odd or outside 2 .. D, P < 1, or T Hq beyond 2^31 - 1. */
+q4_status q8_kv_append(const q8_kv_cache *cache, const int32_t *starts, const int32_t *lengths, int64_t T,
+                       const void *k, int64_t k_token, int64_t k_head, const void *v, int64_t v_token,
+                       int64_t v_head, const void *q, int64_t q_token, int64_t q_head, int64_t Hq, q4_dtype xt,
+                       const float *cos_sin, int64_t P, int64_t R, q4_rope_pairs pairs, int32_t norm,
+                       const void *k_gain, const void *q_gain, q4_dtype gt, float eps, void *q_out, q4_dtype yt,
+                       void *stream);
+
+/* The numbers that the cache holds of the sequences' last tokens: k_out, v_out
+ * [T, heads, D], f32 or bf16 (yt), exact in both (numbers past the type's range
+ * become infinity; those below 2^-126 keep their bits).  Rows at positions below
+ * 0 are left as they were. */
+q4_status q8_kv_read(const q8_kv_cache *cache, const int32_t *starts, const int32_t *lengths, int64_t T, void *k_out,
+                     void *v_out, q4_dtype yt, void *stream);
+
+/* Bytes of device workspace that q8_attention needs, from sizes alone; 0 for
+ * sizes that it refuses.  It depends on q4_set_path. */
+size_t q8_attention_workspace(int64_t T, int64_t sequences, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len,
+                              int64_t window, int64_t sinks);
+
+/* Causal attention of the sequences' last tokens over the cache, which holds
+ * them already:
+ *   y = softmax(scale q K^T) V over the keys j <= p of the row at position p,
+ *   with window > 0 only those with j > p - window or j < sinks.
+ *   q: T rows of Hq heads of D numbers, f32 or bf16 (xt), strided; query head g
+ *     reads key head g / (Hq / heads).
+ *   max_len: a bound of lengths (pages of the table times page will do); how the
+ *     keys are shared out goes by it, results do not need it to hold.
+ *   y: [T, Hq, D] contiguous, f32 or bf16 (yt).
+ *   ws: device memory, 256-byte aligned, of q8_attention_workspace bytes (NULL
+ *     if that is 0); calls that may run at a time need one each.
+ * Scores, softmax and sums are f32.  With bf16 queries and results the weights
+ * are rounded to 11 bits before the product with the values; otherwise queries
+ * and weights have 22 bits.  A row that sees no key is 0; one that sees a NaN,
+ * in itself, a key or a value, is NaN.  What a row does not see does not touch
+ * it.  A row's result depends on the split of the keys, so on T, sequences and
+ * max_len, to its rounding.
+ * EINVAL also for a scale that is not finite, window, sinks or max_len < 0, a
+ * negative stride, a small or misaligned workspace, or an output overlapping an
+ * input; ESHAPE also for Hq not a multiple of heads, T Hq or max_len beyond
+ * 2^31 - 1. */
+q4_status q8_attention(const void *q, int64_t q_token, int64_t q_head, q4_dtype xt, const q8_kv_cache *cache,
+                       const int32_t *starts, const int32_t *lengths, int64_t T, int64_t Hq, int64_t max_len,
+                       float scale, int64_t window, int64_t sinks, void *y, q4_dtype yt, void *ws, size_t ws_bytes,
+                       void *stream);
+
 /* Process-wide route override for A/B tests and benchmarks ([int8] "Tier
  * law": routes are chosen by measurement and can be forced).  A forced route
  * that cannot serve a shape falls back to the generic kernels (MX FP4

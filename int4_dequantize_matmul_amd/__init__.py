@@ -3,8 +3,8 @@
 Argument marshalling only: every function calls the C entry point of the same
 name in ``lib/libq4.so`` (declared in ``include/q4.h``); all arithmetic runs
 in that library's host code or HIP kernels.  torch provides device memory and
-the current stream; outputs are allocated here with torch.  The MX FP4 and
-query/key calls, whose small sizes cost more here than on the GPU, go through
+the current stream; outputs are allocated here with torch.  The MX FP4,
+query/key, row norm, cache and attention calls, whose small sizes cost more here than on the GPU, go through
 ``lib/q4_torch.so`` first, which does the same in C++ (a call of 6 to 11 us
 takes about 4); where that file is missing or was built for another torch or
 Python, they warn once and go through ctypes like the others.
@@ -20,6 +20,7 @@ import importlib.util
 import os
 import sys
 import warnings
+from typing import NamedTuple
 
 import numpy as np
 import torch  # loaded before libq4 so both share torch's HIP runtime
@@ -86,6 +87,14 @@ _SIG = {
     "q4_linear_w4a16_mx": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _I, _I, _I, _P]),
     "q4_qk_norm_rope": (ctypes.c_int, [_P, _I, _I, _P, _I, _I, ctypes.c_int, _P, _P, ctypes.c_int, _P, _P, _P, _P,
                                        ctypes.c_int, _I, _I, _I, _I, _I, _I, ctypes.c_float, ctypes.c_int, _P]),
+    "q8_rmsnorm_rows": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_float, _I, _I, _P, _P, _P, _P]),
+    "q8_kv_append": (ctypes.c_int, [_P, _P, _P, _I, _P, _I, _I, _P, _I, _I, _P, _I, _I, _I, ctypes.c_int, _P, _I, _I,
+                                    ctypes.c_int, ctypes.c_int32, _P, _P, ctypes.c_int, ctypes.c_float, _P,
+                                    ctypes.c_int, _P]),
+    "q8_kv_read": (ctypes.c_int, [_P, _P, _P, _I, _P, _P, ctypes.c_int, _P]),
+    "q8_attention_workspace": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "q8_attention": (ctypes.c_int, [_P, _I, _I, ctypes.c_int, _P, _P, _P, _I, _I, _I, ctypes.c_float, _I, _I, _P,
+                                    ctypes.c_int, _P, ctypes.c_size_t, _P]),
     "q4_set_path": (ctypes.c_int, [ctypes.c_int]),
     "q4_get_path": (ctypes.c_int, []),
     "q4_last_path": (ctypes.c_int, []),
@@ -132,7 +141,8 @@ def _load_direct():
     if m.built_for != here:
         raise ImportError(f"{TORCH_LIB_PATH} was built for {m.built_for}, this is {here}")
     m.bind(torch._C._cuda_getCurrentRawStream,
-           {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _SIG if "_mx" in n or "_qk_" in n})
+           {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _SIG
+            if any(w in n for w in ("_mx", "_qk_", "_rmsnorm", "_kv_", "_attention"))})
     return m
 
 
@@ -145,7 +155,7 @@ def _direct():
         try:
             _DIRECT = _load_direct()
         except ImportError as e:
-            warnings.warn(f"MX FP4 and query/key calls go through ctypes, which takes some microseconds more: {e}; "
+            warnings.warn(f"MX FP4, query/key, row norm, cache and attention calls go through ctypes, which takes some microseconds more: {e}; "
                           "run `python -m int4_dequantize_matmul_amd.build`", RuntimeWarning, stacklevel=3)
             _DIRECT = _NoDirect()
     return _DIRECT
@@ -699,6 +709,220 @@ def q4_qk_norm_rope(q, k, q_gain, k_gain, positions, cos_sin, eps: float = 1e-6,
                                   1 if out == torch.bfloat16 else 0, T, Hq, Hk, D, cos_sin.shape[1],
                                   cos_sin.shape[0], eps, ROPE_PAIRS[pairs], _stream(q)))
     return qo, ko
+
+
+# ---------------------------------------------------------------------------
+# between the linears: rows to int8, the paged 8-bit cache, attention
+# ---------------------------------------------------------------------------
+
+def q8_rmsnorm_rows(x, gain=None, residual=None, eps: float = 1e-6, total=None):
+    """f32 or bf16 rows x [M, K] (plus residual, of x's type) -> (codes int8 [M, K],
+    f32 scales [M], the sum x + residual or None): the rows' root-mean-square
+    norm times gain [K], as q4_linear_w4a8 and q8_linear_w8a8 take them.  The
+    sum goes to `total` if given, which may be x or residual itself."""
+    out = _direct().rmsnorm_rows(x, gain, residual, eps, total)
+    if out is not None:
+        return out
+    _dev(x, "x", _FLOATS, 2)
+    M, K = x.shape
+    for t, name in ((residual, "residual"), (total, "total")):
+        if t is not None:
+            _dev(t, name, (x.dtype,), 2)
+            if t.shape != x.shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(M, K)}")
+            _same_device(x, t)
+    if gain is not None:
+        _dev(gain, "gain", _FLOATS, 1)
+        _same_device(x, gain)
+        if gain.shape[0] != K:
+            raise ValueError(f"gain has {gain.shape[0]} entries for rows of {K}")
+    if total is not None and residual is None:
+        raise ValueError("a total without a residual")
+    xq = torch.empty(M, K, dtype=torch.int8, device=x.device)
+    sx = torch.empty(M, dtype=torch.float32, device=x.device)
+    if residual is not None and total is None:
+        total = torch.empty_like(x)
+    if M:
+        _check("q8_rmsnorm_rows",
+               _lib().q8_rmsnorm_rows(_ptr(x), _ptr(residual), _dt(x), _ptr(gain), 0 if gain is None else _dt(gain), eps,
+                                      M, K, _ptr(total), _ptr(xq), _ptr(sx), _stream(x)))
+    return xq, sx, total
+
+
+KV_BLOCK = 16
+KV_MAX_D = 256
+
+
+class KVCache(NamedTuple):
+    """The pool of a paged 8-bit cache (q8_kv_cache of include/q4.h): codes int8
+    k [pages, heads, page/16, D/16, 16, 16], v [pages, heads, page/16, D, 16] and
+    their scale bytes [pages, heads, page/16]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def q8_kv_cache(pages: int, heads: int, page: int, D: int, device="cuda:0") -> KVCache:
+    """A new pool of `pages` pages of `page` tokens (a power of two from 16 up) of `heads` heads."""
+    if page % KV_BLOCK or D % 16:
+        raise ValueError(f"pages of {page} tokens of {D} numbers: both have to be multiples of 16")
+    blocks = page // KV_BLOCK
+    k = torch.zeros(pages, heads, blocks, D // 16, 16, 16, dtype=torch.int8, device=device)
+    v = torch.zeros(pages, heads, blocks, D, 16, dtype=torch.int8, device=device)
+    return KVCache(k, v, *(torch.zeros(pages, heads, blocks, dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+class KVCacheC(ctypes.Structure):
+    """q8_kv_cache."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("pages", _P), ("n_pages", _I), ("page", _I),
+                ("heads", _I), ("D", _I), ("sequences", _I), ("table", _I)]
+
+
+def _kv(cache, pages, starts, lengths):
+    """Checks a cache and a call's sequences -> (q8_kv_cache, heads, D)."""
+    k, v, ks, vs = cache
+    _dev(k, "the cache's k", (torch.int8,), 6)
+    _dev(v, "the cache's v", (torch.int8,), 5)
+    P, H, B, C = k.shape[:4]
+    if k.shape[4:] != (16, 16) or v.shape != (P, H, B, 16 * C, 16):
+        raise ValueError(f"the cache's k and v have shapes {tuple(k.shape)} and {tuple(v.shape)}")
+    for t, name in ((ks, "k_scale"), (vs, "v_scale")):
+        _dev(t, f"the cache's {name}", _BYTES, 3)
+        if t.shape != (P, H, B):
+            raise ValueError(f"the cache's {name} has shape {tuple(t.shape)}, expected {(P, H, B)}")
+    _dev(pages, "pages", (torch.int32,), 2)
+    _dev(starts, "starts", (torch.int32,), 1)
+    _dev(lengths, "lengths", (torch.int32,), 1)
+    N = lengths.shape[0]
+    if pages.shape[0] != N or starts.shape[0] != N + 1:
+        raise ValueError(f"{N} lengths, {pages.shape[0]} rows of pages, {starts.shape[0]} starts (one more wanted)")
+    _same_device(k, v, ks, vs, pages, starts, lengths)
+    return KVCacheC(_ptr(k), _ptr(v), _ptr(ks), _ptr(vs), _ptr(pages), P, 16 * B, H, 16 * C, N, pages.shape[1])
+
+
+def q8_kv_append(cache, pages, starts, lengths, k, v, q=None, cos_sin=None, k_gain=None, q_gain=None,
+                 eps: float | None = None, pairs: str = "halves", dtype: str | None = None, q_out=None):
+    """New tokens k, v [T, heads, D] (slices of a fused projection as they are)
+    into the cache, the keys normalised if eps is given (times k_gain [D]) and
+    rotated if cos_sin f32 [P, R] is, by their positions; the queries q [T, Hq, D]
+    with q_gain likewise -> the queries [T, Hq, D] in dtype (default: q's), or
+    None.  pages int32 [N, table], starts int32 [N + 1], lengths int32 [N] (new
+    tokens included): see q8_kv_cache in include/q4.h."""
+    out = _direct().kv_append(cache, pages, starts, lengths, k, v, q, cos_sin, k_gain, q_gain, eps, ROPE_PAIRS[pairs],
+                              -1 if dtype is None else DT[dtype], q_out)
+    if out is not None:
+        return out[0]
+    c = _kv(cache, pages, starts, lengths)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [tokens, heads, D]")
+    T = k.shape[0]
+    for t, name in ((k, "k"), (v, "v"), (q, "q")):
+        if t is None and name == "q":
+            continue
+        _heads(t, name, T, c.D)
+        if t.dtype != k.dtype:
+            raise TypeError(f"k and {name} differ in dtype: {k.dtype} and {t.dtype}")
+        if name != "q" and t.shape[1] != c.heads:
+            raise ValueError(f"{name} has {t.shape[1]} heads, the cache {c.heads}")
+        _same_device(cache[0], t)
+    gt = None
+    if eps is None and (k_gain is not None or q_gain is not None):
+        raise ValueError("a gain without eps, which asks for the norm")
+    for g, name in ((k_gain, "k_gain"), (q_gain, "q_gain")):
+        if g is not None:
+            _dev(g, name, _FLOATS, 1)
+            _same_device(k, g)
+            if g.shape[0] != c.D:
+                raise ValueError(f"{name} has {g.shape[0]} entries for heads of {c.D}")
+            if gt is not None and gt != g.dtype:
+                raise TypeError("k_gain and q_gain differ in dtype")
+            gt = g.dtype
+    P = R = 0
+    if cos_sin is not None:
+        _dev(cos_sin, "cos_sin", (torch.float32,), 2)
+        _same_device(k, cos_sin)
+        P, R = cos_sin.shape
+    Hq, strides = 0, (0, 0)
+    if q is not None:
+        Hq, strides = q.shape[1], q.stride()[:2]
+        want = q.dtype if dtype is None else _DTYPES[dtype]
+        if q_out is None:
+            q_out = torch.empty(T, Hq, c.D, dtype=want, device=q.device)
+        else:
+            _dev(q_out, "q_out", (want,), 3)
+            _same_device(q, q_out)
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if T and c.sequences:
+        _check("q8_kv_append",
+               _lib().q8_kv_append(ctypes.byref(c), _ptr(starts), _ptr(lengths), T, _ptr(k), k.stride(0), k.stride(1),
+                                   _ptr(v), v.stride(0), v.stride(1), _ptr(q), *strides, Hq, _dt(k), _ptr(cos_sin), P, R,
+                                   ROPE_PAIRS[pairs], 0 if eps is None else 1, _ptr(k_gain), _ptr(q_gain),
+                                   1 if gt == torch.bfloat16 else 0, 0.0 if eps is None else eps, _ptr(q_out),
+                                   _dt(q_out) if Hq else 0, _stream(k)))
+    return q_out
+
+
+def q8_kv_read(cache, pages, starts, lengths, T: int, dtype: str = "bf16"):
+    """What the cache holds of the sequences' last tokens, T rows in all -> (k, v) [T, heads, D] in dtype."""
+    out = _direct().kv_read(cache, pages, starts, lengths, T, DT[dtype])
+    if out is not None:
+        return out
+    c = _kv(cache, pages, starts, lengths)
+    k, v = (torch.empty(T, c.heads, c.D, dtype=_DTYPES[dtype], device=cache[0].device) for _ in range(2))
+    if T and c.sequences:
+        _check("q8_kv_read", _lib().q8_kv_read(ctypes.byref(c), _ptr(starts), _ptr(lengths), T, _ptr(k), _ptr(v),
+                                               DT[dtype], _stream(k)))
+    return k, v
+
+
+def q8_attention_workspace(T: int, sequences: int, Hq: int, Hk: int, D: int, max_len: int, window: int = 0,
+                           sinks: int = 0) -> int:
+    return int(_lib().q8_attention_workspace(T, sequences, Hq, Hk, D, max_len, window, sinks))
+
+
+def q8_attention(q, cache, pages, starts, lengths, scale: float | None = None, window: int = 0, sinks: int = 0,
+                 max_len: int | None = None, dtype: str | None = None, ws=None, y=None):
+    """Causal attention of the sequences' last tokens q [T, Hq, D] (f32 or bf16)
+    over the cache, which holds them already -> y [T, Hq, D] in dtype (default:
+    q's).  scale: D ** -0.5 if not given.  window > 0: a row sees the last
+    `window` tokens up to its own and the sequence's first `sinks`.  max_len: a
+    bound of lengths, if one is known below the table's."""
+    out = _direct().attention(q, cache, pages, starts, lengths, scale, window, sinks, max_len,
+                              -1 if dtype is None else DT[dtype], ws, y)
+    if out is not None:
+        return out
+    c = _kv(cache, pages, starts, lengths)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [tokens, heads, D]")
+    T, Hq = q.shape[:2]
+    _heads(q, "q", T, c.D)
+    _same_device(cache[0], q)
+    want = q.dtype if dtype is None else _DTYPES[dtype]
+    if y is None:
+        y = torch.empty(T, Hq, c.D, dtype=want, device=q.device)
+    else:
+        _dev(y, "y", (want,), 3)
+        _same_device(q, y)
+        if y.shape != q.shape:
+            raise ValueError(f"y has shape {tuple(y.shape)}, expected {tuple(q.shape)}")
+    if T == 0 or c.sequences == 0 or Hq == 0:
+        return y
+    scale = c.D ** -0.5 if scale is None else scale
+    max_len = c.page * c.table if max_len is None else max_len
+    if ws is None:
+        need = q8_attention_workspace(T, c.sequences, Hq, c.heads, c.D, max_len, window, sinks)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    else:
+        _workspace(ws, q)
+    _check("q8_attention",
+           _lib().q8_attention(_ptr(q), q.stride(0), q.stride(1), _dt(q), ctypes.byref(c), _ptr(starts), _ptr(lengths),
+                               T, Hq, max_len, scale, window, sinks, _ptr(y), _dt(y), _ptr(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), _stream(q)))
+    return y
 
 
 def q4_selftest(device="cuda:0") -> str:

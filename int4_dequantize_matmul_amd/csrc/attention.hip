@@ -1,0 +1,436 @@
+// Attention over the paged 8-bit cache: for a query row at position p and the
+// keys j <= p with j > p - window or j < sinks,
+//   s_j = scale q . k_j,  y = sum_j exp(s_j) v_j / sum_j exp(s_j)
+// in one pass over the keys with the running maximum and sum of the softmax.
+//
+// Products go through the f16 matrix instructions: int8 codes are halves
+// exactly; a query row is scaled by a power of two to a maximum between 2^14
+// and 2^15 and rounded to halves (11 bits, exact for bf16 down to 2^-25 of the
+// row's maximum), and so are the weights exp(s), to at most 2^15 (11 bits; what
+// is below 2^-39 of the largest weight is lost).  For f32 queries or results
+// both come as two halves, 22 bits, at twice the products.  A block's scales
+// are powers of two: the keys' goes into the factor of the scores, the values'
+// into the exponent of the weights.  Maximum, sum and results are f32; the
+// maximum that is subtracted may lag behind the true one by a power of two, so
+// that results are seldom rescaled.
+//
+// S^T = K Q^T and Y^T = V^T P^T on 32 x 32 x 16 instructions, a lane (c, h) for
+// query row c.  Row 8 a + 4 h + b of the first product's keys is key 16 h + 4 a
+// + b of the 32, so a lane ends with the 16 scores of block h, in order, and
+// those are, rounded, its operand of the second product: neither the weights
+// nor the values change lanes.
+#include "attn_device.hpp"
+
+namespace q4 {
+namespace {
+
+constexpr int kThreads = 256, kWaves = 4, kRows = 32;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Types {
+  bool in_bf16, out_bf16;
+};
+
+// A query row's 16 columns at a time, as operands: f[2 s], f[2 s + 1] are the
+// columns 32 s + 16 h .. + 15.
+template <int ND, bool TWO>
+struct Query {
+  uint4 hi[2 * ND], lo[TWO ? 2 * ND : 1];
+  float factor;   // what a product's result is multiplied with: scores in powers of two, without the key's scale
+  __device__ __forceinline__ void load(const AttnArgs &a, const Types &t, int64_t at, bool live, int h) {
+    const int D = static_cast<int>(a.pool.D);
+    float x[ND][16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < ND; ++s) {
+      const int c = 32 * s + 16 * h;
+      const bool in = live && c < D;
+#pragma unroll
+      for (int u = 0; u < 16; u += 8) {
+        if (t.in_bf16) {
+          Run8<true> r;
+          if (in) r.load(a.q, at + c + u);
+          else r.zero();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[s][u + j] = __uint_as_float(j & 1 ? r.v[j / 2] & 0xFFFF0000u : r.v[j / 2] << 16);
+        } else {
+          Run8<false> r;
+          if (in) r.load(a.q, at + c + u);
+          else r.zero();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[s][u + j] = r.v[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
+    }
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+    // exponent of the largest: top in [2^e, 2^(e + 1)); a NaN or an infinity makes the whole row NaN
+    const bool bad = top >= 0x7F800000u;
+    const int e = bad || top == 0 ? 0 : ilogbf(__uint_as_float(top));
+    factor = bad ? __builtin_nanf("") : ldexpf(fabsf(a.scale) * kLog2e, e - 14);
+#pragma unroll
+    for (int s = 0; s < ND; ++s)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t w[4], v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float n = a.scale < 0.0f ? -1.0f : 1.0f;
+          const float p = bad ? 0.0f : n * ldexpf(x[s][8 * u + 2 * j], 14 - e);
+          const float q = bad ? 0.0f : n * ldexpf(x[s][8 * u + 2 * j + 1], 14 - e);
+          w[j] = pack_f16(p, q);
+          v[j] = pack_f16(rest_f16(p), rest_f16(q));
+        }
+        hi[2 * s + u] = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (TWO) lo[2 * s + u] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+  }
+};
+
+// Running softmax of one query row a lane: m what is subtracted from the scores
+// (in powers of two), l the sum of this half's weights, y the results, which
+// count 2^(e - 127 - kOffset) each.
+template <int ND, bool TWO>
+struct State {
+  static constexpr int kLag = TWO ? 1 : 6, kOffset = TWO ? 14 : 9;
+  float m = -__builtin_inff(), l = 0.0f;
+  int e = -1;
+  f32x16 y[ND];
+  __device__ __forceinline__ State() {
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[d][j] = 0.0f;
+  }
+  __device__ __forceinline__ void scale_results(float f) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[d][j] *= f;
+  }
+  // values of scale bytes up to to follow (the same in all lanes)
+  __device__ __forceinline__ void raise(int to) {
+    if (to <= e) return;
+    if (e >= 0) scale_results(ldexpf(1.0f, e - to));
+    e = to;
+  }
+  // The weights of 16 scores x, times f, under the scale byte kb of their keys
+  // and vb of their values, as operands; hidden(j): whether the row does not see key j.
+  template <bool MASK, class F>
+  __device__ __forceinline__ void weights(f32x16 x, float f, int kb, int vb, F hidden, uint4 (&p)[2], uint4 (&rest)[2]) {
+    f *= kb == 255 ? __builtin_nanf("") : __uint_as_float(kb ? static_cast<uint32_t>(kb) << 23 : 0x400000u);
+    float top;
+    if constexpr (MASK) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = hidden(j) ? -__builtin_inff() : x[j] * f;
+      f = 1.0f;
+    }
+    top = x[0];
+#pragma unroll
+    for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
+    top = max_xor32(top * f);
+    if (__any(top > m + static_cast<float>(kLag))) {
+      const float n = fmaxf(m, top);
+      const float g = m == n ? 1.0f : exp2_fast(m - n);   // from nothing (-inf): 0
+      m = n;
+      l *= g;
+      scale_results(g);
+    }
+    // exponent of the weights: at least 2^-60 of what counts, so that their sum stays right
+    const int d = max(vb - e + kOffset, -60);
+    // nothing seen so far: any finite number will do
+    const float add = vb == 255 ? __builtin_nanf("") : static_cast<float>(d) - (m == -__builtin_inff() ? 0.0f : m);
+    float sum = 0.0f;
+    float w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float t = fmaf(x[j], f, add);
+      if constexpr (MASK) t = x[j] == -__builtin_inff() ? x[j] : t;
+      w[j] = exp2_fast(t);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum += w[j];
+    l = fmaf(sum, power2(vb == 255 ? 0 : -d), l);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[j] = pack_f16(w[8 * u + 2 * j], w[8 * u + 2 * j + 1]);
+        b[j] = pack_f16(rest_f16(w[8 * u + 2 * j]), rest_f16(w[8 * u + 2 * j + 1]));
+      }
+      p[u] = make_uint4(a[0], a[1], a[2], a[3]);
+      if constexpr (TWO) rest[u] = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+  }
+};
+
+// Where the results begin behind m and l of `splits` parts of `all` rows, on 16 bytes.
+__host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { return (2 * splits * all + 3) / 4 * 4; }
+
+// What sums and results under the maximum m count under the maximum `to`; l is
+// their sum: a part that saw nothing counts 0, one with NaN keys alone its NaN.
+__device__ __forceinline__ float rescale(float m, float l, float to) {
+  if (m == -__builtin_inff()) return l == 0.0f ? 0.0f : 1.0f;
+  return exp2_fast(m - to);
+}
+
+// Four results of one row from column d on.
+__device__ __forceinline__ void store4(void *y, bool bf16, int64_t i, float a, float b, float c, float d) {
+  if (bf16) store_any(static_cast<uint16_t *>(y) + i, make_uint2(pack_bf16(a, b), pack_bf16(c, d)));
+  else store_any(static_cast<float *>(y) + i, make_float4(a, b, c, d));
+}
+
+// Few rows a sequence: a workgroup has 32 rows of one key head and a share of
+// their keys; its four waves share those out again, 32 keys a step straight from
+// the cache to registers, and meet in LDS.  parts: splits x rows of m, l and
+// results for combine_kernel, or null with one split.
+template <int ND, bool TWO>
+__global__ __launch_bounds__(kThreads, ND <= 4 && !TWO ? 2 : 1) void attention_rows_kernel(AttnArgs a, Types types,
+                                                                                         int splits, float *parts,
+                                                                                         int64_t first) {
+  constexpr int kMeet = ND < 4 ? ND : 4;   // tiles of 32 columns that meet in LDS at a time
+  __shared__ float ms[kWaves][kRows], ls[kWaves][kRows];
+  __shared__ __attribute__((aligned(16))) float meet[kWaves - 1][kRows][32 * kMeet + 4];
+  const int64_t id = first + blockIdx.x;
+  const int split = static_cast<int>(id % splits);
+  const int64_t head = id / splits % a.pool.Hk, slot = id / splits / a.pool.Hk;
+  const int64_t G = a.Hq / a.pool.Hk;
+  const RowTile tile(a.seqs, slot, G, kRows);
+  if (tile.i < 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
+  const int D = static_cast<int>(a.pool.D);
+  const int rows = tile.rows - tile.r0 < kRows ? static_cast<int>(tile.rows - tile.r0) : kRows;
+  const int64_t r = tile.r0 + (c < rows ? c : rows - 1), t = r / G;
+  const int64_t row = tile.s.row + t, qh = head * G + (r - t * G);
+  const int64_t p0 = tile.s.first + tile.r0 / G, p1 = tile.s.first + (tile.r0 + rows - 1) / G;
+  const int pos = static_cast<int>(tile.s.first + t);   // int32 lengths
+  const KeyBlocks keys(p0, p1, a.window, a.sinks);
+  const int64_t window = a.window > 0 ? a.window : INT64_C(1) << 40;
+
+  const int steps = (keys.count + 1) / 2;
+  const int w0 = static_cast<int>(static_cast<int64_t>(steps) * (split * kWaves + wave) / (splits * kWaves));
+  const int w1 = static_cast<int>(static_cast<int64_t>(steps) * (split * kWaves + wave + 1) / (splits * kWaves));
+
+  Query<ND, TWO> q;
+  q.load(a, types, row * a.q_t + qh * a.q_h, true, h);
+  State<ND, TWO> st;
+
+  struct Tile {
+    uint4 k[ND], v[ND];
+  };
+  for (int g0 = w0; g0 < w1; g0 += 32) {   // 32 steps: a block a lane
+    const int n = w1 - g0 < 32 ? w1 - g0 : 32;
+    const int v = 2 * g0 + lane, blk = keys.block(v);
+    const bool in = lane < 2 * n && v < keys.count;
+    int at = 0, bytes = 0;
+    if (in) {
+      const int64_t b = block_at(a.pool, tile.i, blk, head);
+      at = b < 0 ? 0 : static_cast<int>(b);
+      bytes = b < 0 ? 0xFFFF : a.pool.ks[b] | a.pool.vs[b] << 8;
+    }
+    int top = bytes >> 8 == 255 ? 0 : bytes >> 8;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = max(top, __shfl_xor(top, d));
+    st.raise(__builtin_amdgcn_readfirstlane(top));
+
+    auto load = [&](Tile &x, int s) {
+      const int b0 = __builtin_amdgcn_readlane(at, 2 * s), b1 = __builtin_amdgcn_readlane(at, 2 * s + 1);
+      // row c of the first product is key 16 (c / 4 mod 2) + 4 (c / 8) + c mod 4
+      const int8_t *kp = a.pool.k + static_cast<int64_t>(c & 4 ? b1 : b0) * (kKvBlock * D) + (4 * (c >> 3) + (c & 3)) * 16;
+      const int8_t *vp = a.pool.v + static_cast<int64_t>(h ? b1 : b0) * (kKvBlock * D);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const bool kin = 32 * d + 16 * h < D, vin = 32 * d + c < D;
+        x.k[d] = kin ? load16(kp + (2 * d + h) * 256) : make_uint4(0, 0, 0, 0);
+        x.v[d] = vin ? load16(vp + (32 * d + c) * 16) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto compute = [&](const Tile &x, int s) {
+      f32x16 acc = {};
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const uint4 k0 = codes_to_f16(x.k[d].x, x.k[d].y), k1 = codes_to_f16(x.k[d].z, x.k[d].w);
+        acc = mfma_f16_32x32x16(k0, q.hi[2 * d], acc);
+        acc = mfma_f16_32x32x16(k1, q.hi[2 * d + 1], acc);
+        if constexpr (TWO) {
+          acc = mfma_f16_32x32x16(k0, q.lo[2 * d], acc);
+          acc = mfma_f16_32x32x16(k1, q.lo[2 * d + 1], acc);
+        }
+      }
+      const int by0 = __builtin_amdgcn_readlane(bytes, 2 * s), by1 = __builtin_amdgcn_readlane(bytes, 2 * s + 1);
+      const int bk0 = __builtin_amdgcn_readlane(blk, 2 * s) * kKvBlock;
+      const int bk1 = __builtin_amdgcn_readlane(blk, 2 * s + 1) * kKvBlock;
+      const int by = h ? by1 : by0, k0 = h ? bk1 : bk0;
+      auto whole = [&](int b) { return b + 15 <= p0 && (b > p1 - window || b + 15 < a.sinks); };
+      uint4 p[2], rest[2];
+      if (whole(bk0) && whole(bk1)) {
+        st.template weights<false>(acc, q.factor, by & 255, by >> 8, [](int) { return false; }, p, rest);
+      } else {
+        st.template weights<true>(acc, q.factor, by & 255, by >> 8,
+                                  [&](int j) {
+                                    const int k = k0 + j;
+                                    return k > pos || (k <= pos - window && k >= a.sinks);
+                                  },
+                                  p, rest);
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const uint4 v0 = codes_to_f16(x.v[d].x, x.v[d].y), v1 = codes_to_f16(x.v[d].z, x.v[d].w);
+        st.y[d] = mfma_f16_32x32x16(v0, p[0], st.y[d]);
+        st.y[d] = mfma_f16_32x32x16(v1, p[1], st.y[d]);
+        if constexpr (TWO) {
+          st.y[d] = mfma_f16_32x32x16(v0, rest[0], st.y[d]);
+          st.y[d] = mfma_f16_32x32x16(v1, rest[1], st.y[d]);
+        }
+      }
+    };
+    Tile x, z;
+    load(x, 0);
+    for (int s = 0; s < n; s += 2) {
+      if (s + 1 < n) load(z, s + 1);
+      compute(x, s);
+      if (s + 1 < n) {
+        if (s + 2 < n) load(x, s + 2);
+        compute(z, s + 1);
+      }
+    }
+  }
+
+  // the four waves' parts to one maximum, then their sums in order, by the first wave
+  st.l = add_xor32(st.l);
+  if (h == 0) ms[wave][c] = st.m, ls[wave][c] = st.l;
+  __syncthreads();
+  float m = ms[0][c], l = 0.0f;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, ms[w][c]);
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) l += ls[w][c] * rescale(ms[w][c], ls[w][c], m);
+  const float f = rescale(st.m, st.l, m);
+  const int e = st.e - 127 - State<ND, TWO>::kOffset;
+  const int64_t all = a.seqs.T * a.Hq, out = row * a.Hq + qh;
+  const float n = l == 0.0f ? 0.0f : 1.0f / l;   // a row that sees nothing is 0
+#pragma unroll
+  for (int d0 = 0; d0 < ND; d0 += kMeet) {
+    if (d0 > 0) __syncthreads();
+#pragma unroll
+    for (int d = d0; d < ND && d < d0 + kMeet; ++d)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) st.y[d][j] = ldexpf(st.y[d][j] * f, e);
+    if (wave > 0 && c < rows) {
+#pragma unroll
+      for (int d = d0; d < ND && d < d0 + kMeet; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4 *>(&meet[wave - 1][c][32 * (d - d0) + 2 * j + 4 * h]) =
+              make_float4(st.y[d][j], st.y[d][j + 1], st.y[d][j + 2], st.y[d][j + 3]);
+    }
+    __syncthreads();
+    if (wave == 0 && c < rows) {
+#pragma unroll
+      for (int d = d0; d < ND && d < d0 + kMeet; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const int col = 32 * d + 2 * j + 4 * h;
+          float4 sum = make_float4(st.y[d][j], st.y[d][j + 1], st.y[d][j + 2], st.y[d][j + 3]);
+#pragma unroll
+          for (int w = 0; w < kWaves - 1; ++w) {
+            const float4 o = *reinterpret_cast<const float4 *>(&meet[w][c][32 * (d - d0) + 2 * j + 4 * h]);
+            sum.x += o.x, sum.y += o.y, sum.z += o.z, sum.w += o.w;
+          }
+          if (col >= D) continue;
+          if (parts)
+            *reinterpret_cast<float4 *>(parts + results_at(splits, all) + (split * all + out) * D + col) = sum;
+          else
+            store4(a.y, types.out_bf16, out * D + col, sum.x * n, sum.y * n, sum.z * n, sum.w * n);
+        }
+    }
+  }
+  if (parts && wave == 0 && h == 0 && c < rows) {
+    parts[split * all + out] = m;
+    parts[(splits + split) * all + out] = l;
+  }
+}
+
+// Joins the splits of a row in order.
+__global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types types, int splits, const float *parts,
+                                                           int64_t first) {
+  const int64_t all = a.seqs.T * a.Hq;
+  const int D = static_cast<int>(a.pool.D), quads = D / 4;
+  const int64_t u = first + blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
+  const int64_t out = u / quads;
+  const int col = 4 * static_cast<int>(u - out * quads);
+  if (out >= all) return;
+  const int64_t t = out / a.Hq;
+  // rows in front of the first sequence or behind the last are left as they were
+  if (t < Sequence::clamp(a.seqs.starts[0], a.seqs.T) || t >= Sequence::clamp(a.seqs.starts[a.seqs.N], a.seqs.T)) return;
+  float m = -__builtin_inff();
+  for (int s = 0; s < splits; ++s) m = fmaxf(m, parts[s * all + out]);
+  float l = 0.0f;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int s = 0; s < splits; ++s) {
+    const float ms = parts[s * all + out], ls = parts[(splits + s) * all + out];
+    if (ls == 0.0f) continue;             // saw nothing
+    const float f = rescale(ms, ls, m);
+    const float4 o = *reinterpret_cast<const float4 *>(parts + results_at(splits, all) + (s * all + out) * D + col);
+    l = fmaf(ls, f, l);
+    sum.x = fmaf(o.x, f, sum.x), sum.y = fmaf(o.y, f, sum.y), sum.z = fmaf(o.z, f, sum.z), sum.w = fmaf(o.w, f, sum.w);
+  }
+  const float n = l == 0.0f ? 0.0f : 1.0f / l;
+  store4(a.y, types.out_bf16, out * D + col, sum.x * n, sum.y * n, sum.z * n, sum.w * n);
+}
+
+template <int ND, bool TWO>
+void go_rows(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hipStream_t st) {
+  const int64_t G = a.Hq / a.pool.Hk, all = tile_slots(a.seqs.T, a.seqs.N, G, kRows) * a.pool.Hk * p.splits;
+  const int64_t most = max_groups(kThreads);
+  for (int64_t first = 0; first < all; first += most)
+    attention_rows_kernel<ND, TWO><<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, 0, st>>>(
+        a, t, p.splits, p.splits > 1 ? ws : nullptr, first);
+  if (p.splits == 1) return;
+  const int64_t quads = a.seqs.T * a.Hq * (a.pool.D / 4), per = most * kThreads;
+  for (int64_t first = 0; first < quads; first += per) {
+    const int64_t n = quads - first < per ? quads - first : per;
+    combine_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(a, t, p.splits, ws, first);
+  }
+}
+
+template <bool TWO>
+void go(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hipStream_t st) {
+  switch ((a.pool.D + 31) / 32) {
+    case 1: return go_rows<1, TWO>(a, t, p, ws, st);
+    case 2: return go_rows<2, TWO>(a, t, p, ws, st);
+    case 3: return go_rows<3, TWO>(a, t, p, ws, st);
+    case 4: return go_rows<4, TWO>(a, t, p, ws, st);
+    case 5: return go_rows<5, TWO>(a, t, p, ws, st);
+    case 6: return go_rows<6, TWO>(a, t, p, ws, st);
+    case 7: return go_rows<7, TWO>(a, t, p, ws, st);
+    default: return go_rows<8, TWO>(a, t, p, ws, st);
+  }
+}
+
+}  // namespace
+
+AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len, int64_t window,
+                        int64_t sinks, int) {
+  AttnPlan p = {};
+  const int64_t G = Hq / Hk, groups = tile_slots(T, N, G, kRows) * Hk;
+  int64_t keys = max_len;
+  if (window > 0 && window + sinks + 32 < keys) keys = window + sinks + 32;
+  // two workgroups a CU, a wave at least 64 keys of what a sequence may have
+  int64_t s = 512 / groups, most = keys / 256;
+  s = s < most ? s : most;
+  p.splits = static_cast<int>(s < 1 ? 1 : s > 64 ? 64 : s);
+  p.ws = p.splits > 1 ? (results_at(p.splits, T * Hq) + p.splits * T * Hq * D) * sizeof(float) : 0;
+  return p;
+}
+
+hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, bool bf16, bool out_bf16, void *ws, hipStream_t st) {
+  const Types t = {bf16, out_bf16};
+  if (bf16 && out_bf16) go<false>(a, t, p, static_cast<float *>(ws), st);
+  else go<true>(a, t, p, static_cast<float *>(ws), st);
+  return hipGetLastError();
+}
+
+}  // namespace q4

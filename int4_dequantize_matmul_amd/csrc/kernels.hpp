@@ -162,4 +162,73 @@ struct QkArgs {
 };
 hipError_t launch_qk_norm_rope(const QkArgs &a, bool in_bf16, bool out_bf16, bool neighbours, hipStream_t st);
 
+// Rows x + r, normalised and quantised to int8 with an f32 scale a row.  r, g and
+// sum may be null; x, r and sum have one type.
+struct NormArgs {
+  const void *x, *r, *g;
+  bool g_bf16;
+  void *sum;
+  int8_t *xq;
+  float *sx;
+  int64_t M, K;
+  float eps;
+};
+hipError_t launch_rmsnorm_rows(const NormArgs &a, bool bf16, hipStream_t st);
+
+// The paged 8-bit cache (layout: kv_device.hpp) and the rows of a call: row
+// starts[i] + t of sequence i is its token lengths[i] - (starts[i + 1] -
+// starts[i]) + t.
+struct KvPool {
+  int8_t *k, *v;
+  uint8_t *ks, *vs;
+  const int32_t *pages;         // [N, width]
+  int64_t n_pages, width, Hk, D;
+  int page_blocks_log2;         // blocks of 16 tokens a page
+};
+struct KvSeqs {
+  const int32_t *starts;        // [N + 1]
+  const int32_t *lengths;       // [N]
+  int64_t N, T;                 // sequences, rows that the row arrays have
+};
+// Keys and values into the cache, keys (and queries into qo) normalised and
+// rotated on the way.  Strides in elements; q, gains and the table may be null.
+struct AppendArgs {
+  KvPool pool;
+  KvSeqs seqs;
+  const void *q, *k, *v;
+  int64_t q_t, q_h, k_t, k_h, v_t, v_h;
+  const void *gq, *gk;
+  bool g_bf16;
+  const float *table;           // [P, R], or null: no rotation
+  int64_t P, R;
+  bool neighbours, norm;
+  float eps;
+  void *qo;                     // [T, Hq, D]
+  int64_t Hq;
+};
+hipError_t launch_kv_append(const AppendArgs &a, bool bf16, bool out_bf16, hipStream_t st);
+// ko, vo: [T, Hk, D]
+hipError_t launch_kv_read(const KvPool &pool, const KvSeqs &seqs, void *ko, void *vo, bool out_bf16, hipStream_t st);
+
+// Attention of the rows of a call over the cache.  q strided, y [T, Hq, D].
+struct AttnArgs {
+  KvPool pool;
+  KvSeqs seqs;
+  const void *q;
+  int64_t q_t, q_h;
+  void *y;
+  int64_t Hq;
+  float scale;
+  int64_t window, sinks;        // window 0: none
+};
+// How a call is shared out; from sizes alone, so that the workspace is known before.
+struct AttnPlan {
+  bool tiled;      // LDS-tiled kernel for many rows a sequence, else waves that share out the keys
+  int splits;      // workgroups that share out a sequence's keys
+  size_t ws;       // bytes of workspace
+};
+AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len, int64_t window,
+                        int64_t sinks, int path);
+hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, bool bf16, bool out_bf16, void *ws, hipStream_t st);
+
 }  // namespace q4

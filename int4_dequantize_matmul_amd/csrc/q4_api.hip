@@ -836,3 +836,163 @@ extern "C" q4_status q4_qk_norm_rope(const void *q, int64_t q_token, int64_t q_h
                                         S(stream)),
                 Q4_PATH_GEMV);
 }
+
+// ---- rows in front of int8 linears, the 8-bit cache, attention -----------------
+
+extern "C" q4_status q8_rmsnorm_rows(const void *x, const void *residual, q4_dtype xt_arg, const void *gain,
+                                     q4_dtype gt_arg, float eps, int64_t M, int64_t K, void *sum, int8_t *xq,
+                                     float *sx, void *stream) {
+  const int xt = enum_bits(xt_arg), gt = enum_bits(gt_arg);
+  if (!x || !xq || !sx || M < 0 || K < 0 || bad_dt(xt) || bad_dt(gt)) return Q4_EINVAL;
+  if (!(eps >= 0.0f) || (sum && !residual)) return Q4_EINVAL;
+  if (M > kMaxNK || K > kMaxNK) return Q4_ESHAPE;
+  const uint64_t in = u(M) * u(K) * size_of(xt), gb = u(K) * size_of(gt);
+  const Buf xb = {x, in}, rb = {residual, in}, g = {gain, gb}, sb = {sum, in};
+  if (any_overlap({{xq, u(M) * u(K)}, {sx, u(M) * 4}}, {xb, rb, g, sb})) return Q4_EINVAL;
+  // the sum may take the place of x or of the residual, row by row
+  if (overlap(sb, g) || (sum != x && overlap(sb, xb)) || (sum != residual && overlap(sb, rb))) return Q4_EINVAL;
+  if (M == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  if (K == 0) return finish(q4::launch_zero(sx, u(M) * 4, S(stream)), Q4_PATH_GENERIC);
+  const q4::NormArgs a = {x, residual, gain, gt == Q4_DT_BF16, sum, xq, sx, M, K, eps};
+  return finish(q4::launch_rmsnorm_rows(a, xt == Q4_DT_BF16, S(stream)), Q4_PATH_GEMV);
+}
+
+namespace {
+
+constexpr int64_t kMaxRows = INT32_MAX;   // starts and lengths are int32
+
+// Pointers and sizes of a cache and of a call's sequences.
+q4_status cache_bad(const q8_kv_cache *c, const int32_t *starts, const int32_t *lengths, int64_t T) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->pages || !starts || !lengths) return Q4_EINVAL;
+  if (c->n_pages < 0 || c->page < 0 || c->heads < 0 || c->D < 0 || c->sequences < 0 || c->table < 0 || T < 0)
+    return Q4_EINVAL;
+  if (misaligned(c->k, 16) || misaligned(c->v, 16)) return Q4_EINVAL;
+  if (c->D % 16 != 0 || c->D < 16 || c->D > Q8_KV_MAX_D) return Q4_ESHAPE;
+  if (c->page < 16 || c->page > 65536 || (c->page & (c->page - 1)) != 0) return Q4_ESHAPE;
+  if (c->heads < 1 || c->n_pages < 1 || c->table < 1) return Q4_ESHAPE;
+  if (c->heads > kMaxRows || c->n_pages > kMaxRows || c->n_pages * c->heads > kMaxRows / (c->page / 16)) return Q4_ESHAPE;
+  if (T > kMaxRows || c->sequences > kMaxRows || c->table > kMaxRows) return Q4_ESHAPE;
+  return Q4_OK;
+}
+
+uint64_t pool_blocks(const q8_kv_cache &c) { return u(c.n_pages) * u(c.heads) * u(c.page / 16); }
+
+struct CacheBufs {
+  Buf k, v, ks, vs, pages, starts, lengths;
+  CacheBufs(const q8_kv_cache &c, const int32_t *st, const int32_t *len)
+      : k{c.k, pool_blocks(c) * 16 * u(c.D)}, v{c.v, pool_blocks(c) * 16 * u(c.D)}, ks{c.k_scale, pool_blocks(c)},
+        vs{c.v_scale, pool_blocks(c)}, pages{c.pages, u(c.sequences) * u(c.table) * 4},
+        starts{st, (u(c.sequences) + 1) * 4}, lengths{len, u(c.sequences) * 4} {}
+};
+
+q4::KvPool pool_of(const q8_kv_cache &c) {
+  int log2 = 0;
+  while ((int64_t(16) << log2) < c.page) ++log2;
+  return {c.k, c.v, c.k_scale, c.v_scale, c.pages, c.n_pages, c.table, c.heads, c.D, log2};
+}
+
+}  // namespace
+
+extern "C" q4_status q8_kv_append(const q8_kv_cache *cache, const int32_t *starts, const int32_t *lengths, int64_t T,
+                                  const void *k, int64_t k_token, int64_t k_head, const void *v, int64_t v_token,
+                                  int64_t v_head, const void *q, int64_t q_token, int64_t q_head, int64_t Hq,
+                                  q4_dtype xt_arg, const float *cos_sin, int64_t P, int64_t R,
+                                  q4_rope_pairs pairs_arg, int32_t norm, const void *k_gain, const void *q_gain,
+                                  q4_dtype gt_arg, float eps, void *q_out, q4_dtype yt_arg, void *stream) {
+  const int xt = enum_bits(xt_arg), gt = enum_bits(gt_arg), yt = enum_bits(yt_arg), pairs = enum_bits(pairs_arg);
+  const q4_status bad = cache_bad(cache, starts, lengths, T);
+  if (bad == Q4_EINVAL) return bad;
+  if (!k || !v || Hq < 0 || (Hq > 0 && (!q || !q_out)) || P < 0 || R < 0) return Q4_EINVAL;
+  if (bad_dt(xt) || bad_dt(gt) || bad_dt(yt) || (pairs != Q4_ROPE_HALVES && pairs != Q4_ROPE_NEIGHBOURS))
+    return Q4_EINVAL;
+  if (k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0 || (Hq > 0 && (q_token < 0 || q_head < 0)))
+    return Q4_EINVAL;
+  if (norm && !(eps >= 0.0f)) return Q4_EINVAL;
+  if (bad != Q4_OK) return bad;
+  const q8_kv_cache &c = *cache;
+  if (cos_sin && (R % 2 != 0 || R < 2 || R > c.D || P < 1 || P > kMaxNK)) return Q4_ESHAPE;
+  if (!cos_sin) P = R = 0;
+  if (Hq > kMaxRows || (T > 0 && Hq > kMaxRows / T)) return Q4_ESHAPE;
+  if (Hq == 0) q = q_out = nullptr, q_token = q_head = 0;
+  if (!norm) k_gain = q_gain = nullptr;
+  uint64_t qb, kb, vb;
+  if (!span(T, c.heads, c.D, k_token, k_head, size_of(xt), &kb) || !span(T, c.heads, c.D, v_token, v_head, size_of(xt), &vb) ||
+      !span(T, Hq, c.D, q_token, q_head, size_of(xt), &qb))
+    return Q4_ESHAPE;
+  const CacheBufs b(c, starts, lengths);
+  const uint64_t gb = u(c.D) * size_of(gt);
+  if (any_overlap({b.k, b.v, b.ks, b.vs, {q_out, u(T) * u(Hq) * u(c.D) * size_of(yt)}},
+                  {{k, kb}, {v, vb}, {q, qb}, {k_gain, gb}, {q_gain, gb}, {cos_sin, u(P) * u(R) * 4}, b.pages,
+                   b.starts, b.lengths}))
+    return Q4_EINVAL;
+  if (T == 0 || c.sequences == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  const q4::AppendArgs a = {pool_of(c), {starts, lengths, c.sequences, T}, q, k, v, q_token, q_head, k_token, k_head,
+                            v_token, v_head, q_gain, k_gain, gt == Q4_DT_BF16, cos_sin, P, R,
+                            pairs == Q4_ROPE_NEIGHBOURS, norm != 0, eps, q_out, Hq};
+  return finish(q4::launch_kv_append(a, xt == Q4_DT_BF16, yt == Q4_DT_BF16, S(stream)), Q4_PATH_GEMV);
+}
+
+extern "C" q4_status q8_kv_read(const q8_kv_cache *cache, const int32_t *starts, const int32_t *lengths, int64_t T,
+                                void *k_out, void *v_out, q4_dtype yt_arg, void *stream) {
+  const int yt = enum_bits(yt_arg);
+  const q4_status bad = cache_bad(cache, starts, lengths, T);
+  if (bad == Q4_EINVAL || !k_out || !v_out || bad_dt(yt)) return Q4_EINVAL;
+  if (bad != Q4_OK) return bad;
+  const q8_kv_cache &c = *cache;
+  const CacheBufs b(c, starts, lengths);
+  uint64_t out;
+  if (!span(T, c.heads, c.D, c.heads * c.D, c.D, size_of(yt), &out)) return Q4_ESHAPE;
+  if (any_overlap({{k_out, out}, {v_out, out}}, {b.k, b.v, b.ks, b.vs, b.pages, b.starts, b.lengths})) return Q4_EINVAL;
+  if (T == 0 || c.sequences == 0) return Q4_OK;
+  if (!device_ok()) return Q4_EDEVICE;
+  return finish(q4::launch_kv_read(pool_of(c), {starts, lengths, c.sequences, T}, k_out, v_out, yt == Q4_DT_BF16,
+                                   S(stream)),
+                Q4_PATH_GEMV);
+}
+
+namespace {
+
+// Sizes that attention takes beside those of the cache.
+bool attention_shape_bad(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
+  if (D % 16 != 0 || D < 16 || D > Q8_KV_MAX_D || Hk < 1 || Hq < 1 || Hq % Hk != 0) return true;
+  return T > kMaxRows || N > kMaxRows || Hq > kMaxRows || (T > 0 && Hq > kMaxRows / T) || max_len > kMaxRows;
+}
+
+}  // namespace
+
+extern "C" size_t q8_attention_workspace(int64_t T, int64_t sequences, int64_t Hq, int64_t Hk, int64_t D,
+                                         int64_t max_len, int64_t window, int64_t sinks) {
+  if (T <= 0 || sequences <= 0 || max_len < 0 || window < 0 || sinks < 0) return 0;
+  if (attention_shape_bad(T, sequences, Hq, Hk, D, max_len)) return 0;
+  return q4::attention_plan(T, sequences, Hq, Hk, D, max_len, window, sinks, g_path.load(std::memory_order_relaxed)).ws;
+}
+
+extern "C" q4_status q8_attention(const void *q, int64_t q_token, int64_t q_head, q4_dtype xt_arg,
+                                  const q8_kv_cache *cache, const int32_t *starts, const int32_t *lengths, int64_t T,
+                                  int64_t Hq, int64_t max_len, float scale, int64_t window, int64_t sinks, void *y,
+                                  q4_dtype yt_arg, void *ws, size_t ws_bytes, void *stream) {
+  const int xt = enum_bits(xt_arg), yt = enum_bits(yt_arg);
+  const q4_status bad = cache_bad(cache, starts, lengths, T);
+  if (bad == Q4_EINVAL || !q || !y || bad_dt(xt) || bad_dt(yt) || Hq < 0 || q_token < 0 || q_head < 0) return Q4_EINVAL;
+  if (max_len < 0 || window < 0 || sinks < 0 || !std::isfinite(scale) || misaligned(ws, 256)) return Q4_EINVAL;
+  if (bad != Q4_OK) return bad;
+  const q8_kv_cache &c = *cache;
+  if (Hq == 0) return Q4_OK;
+  if (attention_shape_bad(T, c.sequences, Hq, c.heads, c.D, max_len)) return Q4_ESHAPE;
+  uint64_t qb;
+  if (!span(T, Hq, c.D, q_token, q_head, size_of(xt), &qb)) return Q4_ESHAPE;
+  if (T == 0 || c.sequences == 0) return Q4_OK;
+  const q4::AttnPlan p = q4::attention_plan(T, c.sequences, Hq, c.heads, c.D, max_len, window, sinks,
+                                            g_path.load(std::memory_order_relaxed));
+  if (p.ws > 0 && (!ws || ws_bytes < p.ws)) return Q4_EINVAL;
+  const CacheBufs b(c, starts, lengths);
+  if (any_overlap({{y, u(T) * u(Hq) * u(c.D) * size_of(yt)}, {ws, p.ws}},
+                  {{q, qb}, b.k, b.v, b.ks, b.vs, b.pages, b.starts, b.lengths}))
+    return Q4_EINVAL;
+  if (!device_ok()) return Q4_EDEVICE;
+  const q4::AttnArgs a = {pool_of(c), {starts, lengths, c.sequences, T}, q, q_token, q_head, y, Hq, scale, window, sinks};
+  return finish(q4::launch_attention(a, p, xt == Q4_DT_BF16, yt == Q4_DT_BF16, ws, S(stream)),
+                p.tiled ? Q4_PATH_TILED : Q4_PATH_GEMV);
+}

@@ -1,0 +1,245 @@
+// Rows in front of int8 linears in one pass: the residual's addition, the
+// root-mean-square norm and the int8 codes of the result with their scale.
+//   h = x + r,  u = h g,  y = u / sqrt(mean(h^2) + eps)
+//   code = rint(127 y / max|y|) = rint(127 u / max|u|),  scale = max|y| / 127
+// The root cancels out of the codes, so they need nothing that is summed: they
+// are the nearest ones of the exact quotients (ties to even, up to a sum x + r
+// past 53 bits), on every route.  Sums and products go in f32; an element whose
+// f32 quotient, off by at most 6 roundings of 2^-24, lies next to a border is
+// divided again in f64, as is the maximum formed.
+//
+// Bound: memory; x and r are read, the sum and the codes written once.  A row
+// stays in the registers of one wave or of four, 8 columns a lane at a time;
+// rows past that are read three times.
+#include "kernels.hpp"
+#include "mx_device.hpp"
+
+namespace q4 {
+namespace {
+
+template <bool BF16>
+__device__ __forceinline__ float at(const Run8<BF16> &r, int j) {
+  if constexpr (BF16) return __uint_as_float(j & 1 ? r.v[j / 2] & 0xFFFF0000u : r.v[j / 2] << 16);
+  else return r.v[j];
+}
+
+// The 8 columns from c on of a row of K, zeros past its end.
+template <bool BF16>
+__device__ __forceinline__ void fetch(Run8<BF16> &v, const void *p, int64_t row, int64_t c, int64_t K) {
+  if (c + 8 <= K) v.load(p, row + c);
+  else if (c < K) v.load_part(p, row + c, static_cast<int>(K - c));
+  else v.zero();
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+template <int W>
+__device__ __forceinline__ void join(float &ss, uint32_t &top, float *sums, uint32_t *tops) {
+  // magnitudes order as their bits; NaN and infinity come last
+  ss = add_xor32(add_xor16(dpp_row_sum_f32<16>(ss)));
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = ss, tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+    ss = 0.0f, top = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) ss += sums[i], top = max(top, tops[i]);
+  }
+}
+
+// The largest of the lanes' numbers, most of which are 0.
+template <int W>
+__device__ __forceinline__ double join(double m, double *tops) {
+  unsigned long long left = __ballot(m > 0.0);
+  const uint64_t b = __builtin_bit_cast(uint64_t, m);
+  m = 0.0;
+  while (left) {
+    const int l = __builtin_ctzll(left);
+    left &= left - 1;
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), l);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), l);
+    m = fmax(m, __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo));
+  }
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = tops[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) m = fmax(m, tops[i]);
+  }
+  return m;
+}
+
+// W waves a row; RUNS times 8 columns a lane in registers, or 0 for rows that
+// are read again.
+template <bool BF16, int W, int RUNS>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_rows_kernel(NormArgs a, int64_t first) {
+  __shared__ float sums[W];
+  __shared__ uint32_t tops[W];
+  __shared__ double tops64[W];
+  const int64_t m = first + (W == 1 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : int64_t(blockIdx.x));
+  if (m >= a.M) return;   // a whole wave; only where no wave waits for another
+  const int64_t K = a.K, row = m * K;
+  const int tid = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  constexpr int step = 64 * W * 8;
+
+  constexpr int N = RUNS ? RUNS : 1;
+  Run8<BF16> x[N], r[N];
+  float g[N][8];
+  auto load = [&](int i, int64_t c) {
+    fetch(x[i], a.x, row, c, K);
+    if (a.r) fetch(r[i], a.r, row, c, K);
+    else r[i].zero();
+    if (!a.g) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[i][j] = 1.0f;
+    } else if (a.g_bf16) {
+      Run8<true> t;
+      fetch(t, a.g, 0, c, K);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[i][j] = at(t, j);
+    } else {
+      Run8<false> t;
+      fetch(t, a.g, 0, c, K);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[i][j] = at(t, j);
+    }
+  };
+  // f over the lane's runs, loaded before where they stay in registers
+  auto each = [&](auto f) {
+    if constexpr (RUNS > 0) {
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i) f(i, int64_t(i) * step + tid * 8);
+    } else {
+      for (int64_t c = tid * 8; c < K; c += step) load(0, c), f(0, c);
+    }
+  };
+  auto product = [&](int i, int j) { return (at(x[i], j) + at(r[i], j)) * g[i][j]; };
+  auto product64 = [&](int i, int j) {
+    return (static_cast<double>(at(x[i], j)) + static_cast<double>(at(r[i], j))) * static_cast<double>(g[i][j]);
+  };
+  if constexpr (RUNS > 0) {
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) load(i, int64_t(i) * step + tid * 8);
+  }
+
+  float ss = 0.0f;
+  uint32_t top = 0;
+  each([&](int i, int64_t) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float h = at(x[i], j) + at(r[i], j);
+      ss = fmaf(h, h, ss);
+      top = max(top, magnitude(h * g[i][j]));
+    }
+  });
+  join<W>(ss, top, sums, tops);
+  const bool bad = top >= 0x7F800000u || !(ss < __builtin_inff());
+
+  // max|u| in f64, from the elements whose f32 product is within its roundings of the largest
+  double m64 = 0.0;
+  const uint32_t near_top = top > 8 ? top - 8 : 1;
+  each([&](int i, int64_t) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (magnitude(product(i, j)) >= near_top) m64 = fmax(m64, fabs(product64(i, j)));
+  });
+  m64 = join<W>(m64, tops64);
+  if (tid == 0)
+    a.sx[m] = bad ? __builtin_nanf("")
+                  : static_cast<float>(m64) * (1.0f / sqrtf(ss / static_cast<float>(K) + a.eps)) / 127.0f;
+
+  const float f = __uint_as_float(top);
+  const bool small = f < 0x1p-100f;   // subnormal products, or 127 / f past the range
+  const float k127 = small ? 0.0f : 127.0f / f;
+  each([&](int i, int64_t c) {
+    if (c >= K) return;
+    const int n = K - c < 8 ? static_cast<int>(K - c) : 8;
+    if (a.sum) {
+      float h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = at(x[i], j) + at(r[i], j);
+      if constexpr (BF16) {
+        uint16_t *p = static_cast<uint16_t *>(a.sum) + row + c;
+        const uint4 w = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]), pack_bf16(h[4], h[5]),
+                                   pack_bf16(h[6], h[7]));
+        if (n == 8) {
+          store_any(p, w);
+        } else {
+          const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 7; ++j)
+            if (j < n) p[j] = static_cast<uint16_t>(d[j / 2] >> (16 * (j & 1)));
+        }
+      } else {
+        float *p = static_cast<float *>(a.sum) + row + c;
+        if (n == 8) {
+          store_any(p, make_float4(h[0], h[1], h[2], h[3]));
+          store_any(p + 4, make_float4(h[4], h[5], h[6], h[7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 7; ++j)
+            if (j < n) p[j] = h[j];
+        }
+      }
+    }
+    int code[8];
+    bool near = small;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = product(i, j) * k127, q = rintf(t);
+      near |= fabsf(t - q) > 0.4998f;
+      code[j] = static_cast<int>(q);
+    }
+    if (bad || top == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) code[j] = 0;
+    } else if (near) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) code[j] = static_cast<int>(rint(127.0 * product64(i, j) / m64));
+    }
+    uint32_t d[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j / 4] |= (static_cast<uint32_t>(code[j]) & 0xFFu) << (8 * (j & 3));
+    int8_t *p = a.xq + row + c;
+    if (n == 8) {
+      store_any(p, make_uint2(d[0], d[1]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (j < n) p[j] = static_cast<int8_t>(d[j / 4] >> (8 * (j & 3)));
+    }
+  });
+}
+
+template <bool BF16, int W, int RUNS>
+void go(const NormArgs &a, hipStream_t st) {
+  constexpr int threads = W == 1 ? 256 : 64 * W, rows = W == 1 ? 4 : 1;
+  const int64_t most = rows * max_groups(threads);
+  for (int64_t first = 0; first < a.M; first += most) {   // rows of a launch
+    const int64_t n = a.M - first < most ? a.M - first : most;
+    rmsnorm_rows_kernel<BF16, W, RUNS><<<static_cast<unsigned>((n + rows - 1) / rows), threads, 0, st>>>(a, first);
+  }
+}
+
+template <bool BF16>
+void pick(const NormArgs &a, hipStream_t st) {
+  const int64_t runs = (a.K + 7) / 8;
+  if (runs <= 64) go<BF16, 1, 1>(a, st);
+  else if (a.M >= 2048 && runs <= 128) go<BF16, 1, 2>(a, st);
+  else if (a.M >= 2048 && runs <= 256) go<BF16, 1, 4>(a, st);
+  else if (runs <= 256) go<BF16, 4, 1>(a, st);
+  else if (runs <= 512) go<BF16, 4, 2>(a, st);
+  else if (runs <= 1024) go<BF16, 4, 4>(a, st);
+  else go<BF16, 4, 0>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm_rows(const NormArgs &a, bool bf16, hipStream_t st) {
+  bf16 ? pick<true>(a, st) : pick<false>(a, st);
+  return hipGetLastError();
+}
+
+}  // namespace q4
