@@ -484,7 +484,8 @@ size_t q8_attention_workspace(int64_t T, int64_t sequences, int64_t Hq, int64_t 
  *     if that is 0); calls that may run at a time need one each.
  * Scores, softmax and sums are f32.  With bf16 queries and results the weights
  * are rounded to 11 bits before the product with the values; otherwise queries
- * and weights have 22 bits.  A row that sees no key is 0; one that sees a NaN,
+ * and weights have 22 bits.  (Weights times their values' scale that are below
+ * 2^-23 of the row's largest such product have fewer.)  A row that sees no key is 0; one that sees a NaN,
  * in itself, a key or a value, is NaN.  What a row does not see does not touch
  * it.  A row's result depends on the split of the keys, so on T, sequences and
  * max_len, to its rounding.

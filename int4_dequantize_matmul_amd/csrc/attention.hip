@@ -6,13 +6,12 @@
 // Products go through the f16 matrix instructions: int8 codes are halves
 // exactly; a query row is scaled by a power of two to a maximum between 2^14
 // and 2^15 and rounded to halves (11 bits, exact for bf16 down to 2^-25 of the
-// row's maximum), and so are the weights exp(s), to at most 2^15 (11 bits; what
-// is below 2^-39 of the largest weight is lost).  For f32 queries or results
-// both come as two halves, 22 bits, at twice the products.  A block's scales
-// are powers of two: the keys' goes into the factor of the scores, the values'
-// into the exponent of the weights.  Maximum, sum and results are f32; the
-// maximum that is subtracted may lag behind the true one by a power of two, so
-// that results are seldom rescaled.
+// row's maximum), and so are the weights exp(s), times the power of two that is
+// their values' scale (11 bits down to 2^-23 of the largest such product, half a
+// step of 2^-33 of it below).  For f32 queries or results both come as two
+// halves, 22 bits, at twice the products.  Maximum, sum and results are f32; what
+// is subtracted from the scores are whole powers of two that may lag behind the
+// maximum, so that results are seldom rescaled, and exactly.
 //
 // S^T = K Q^T and Y^T = V^T P^T on 32 x 32 x 16 instructions, a lane (c, h) for
 // query row c.  Row 8 a + 4 h + b of the first product's keys is key 16 h + 4 a
@@ -88,14 +87,16 @@ struct Query {
   }
 };
 
-// Running softmax of one query row a lane: m what is subtracted from the scores
-// (in powers of two), l the sum of this half's weights, y the results, which
-// count 2^(e - 127 - kOffset) each.
+// Running softmax of one query row a lane, which lanes c and c + 32 share.  Scores
+// are in powers of two; `a` and `b` are whole numbers: l is this half's sum of
+// weights 2^(s - a); y holds the results, sums of 2^(s + e - b + kOffset) times
+// codes, e the exponent of their values' scale.  So the weights that meet the
+// codes are rounded next to the largest product of a weight and its values'
+// scale, whatever the scales are.  b may be kLag, a 30 below what they follow.
 template <int ND, bool TWO>
 struct State {
   static constexpr int kLag = TWO ? 1 : 6, kOffset = TWO ? 14 : 9;
-  float m = -__builtin_inff(), l = 0.0f;
-  int e = -1;
+  float a = -__builtin_inff(), b = -__builtin_inff(), l = 0.0f;
   f32x16 y[ND];
   __device__ __forceinline__ State() {
 #pragma unroll
@@ -103,78 +104,78 @@ struct State {
 #pragma unroll
       for (int j = 0; j < 16; ++j) y[d][j] = 0.0f;
   }
-  __device__ __forceinline__ void scale_results(float f) {
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) y[d][j] *= f;
-  }
-  // values of scale bytes up to to follow (the same in all lanes)
-  __device__ __forceinline__ void raise(int to) {
-    if (to <= e) return;
-    if (e >= 0) scale_results(ldexpf(1.0f, e - to));
-    e = to;
-  }
-  // The weights of 16 scores x, times f, under the scale byte kb of their keys
-  // and vb of their values, as operands; hidden(j): whether the row does not see key j.
+  // The weights of 16 keys' products x with the row, times f, under the scale
+  // bytes kb and vb of their block, as operands; hidden(j): the row does not see key j.
   template <bool MASK, class F>
   __device__ __forceinline__ void weights(f32x16 x, float f, int kb, int vb, F hidden, uint4 (&p)[2], uint4 (&rest)[2]) {
     f *= kb == 255 ? __builtin_nanf("") : __uint_as_float(kb ? static_cast<uint32_t>(kb) << 23 : 0x400000u);
-    float top;
     if constexpr (MASK) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) x[j] = hidden(j) ? -__builtin_inff() : x[j] * f;
       f = 1.0f;
     }
-    top = x[0];
+    float top = x[0];
 #pragma unroll
     for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
-    top = max_xor32(top * f);
-    if (__any(top > m + static_cast<float>(kLag))) {
-      const float n = fmaxf(m, top);
-      const float g = m == n ? 1.0f : exp2_fast(m - n);   // from nothing (-inf): 0
-      m = n;
-      l *= g;
-      scale_results(g);
+    top *= f;
+    const float e = static_cast<float>(vb - 127), ta = max_xor32(top), tb = max_xor32(top + e);
+    if (__any(ta > a + 30.0f || tb > b + static_cast<float>(kLag))) {
+      const float na = fmaxf(a, ceilf(ta)), nb = fmaxf(b, ceilf(tb));
+      const float ga = a == na ? 1.0f : exp2_fast(a - na), gb = b == nb ? 1.0f : exp2_fast(b - nb);   // from -inf: 0
+      a = na, b = nb;
+      l *= ga;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[d][j] *= gb;
     }
-    // exponent of the weights: at least 2^-60 of what counts, so that their sum stays right
-    const int d = max(vb - e + kOffset, -60);
     // nothing seen so far: any finite number will do
-    const float add = vb == 255 ? __builtin_nanf("") : static_cast<float>(d) - (m == -__builtin_inff() ? 0.0f : m);
-    float sum = 0.0f;
-    float w[16];
+    const float fa = a == -__builtin_inff() ? 0.0f : a, fb = b == -__builtin_inff() ? 0.0f : b;
+    // weights of 2^-60 and less of what counts are 0 as halves; kept that large, their f32 sum stays right
+    const float shift = fmaxf(e + static_cast<float>(kOffset) - fb, -60.0f - fa);
+    const float add = vb == 255 ? __builtin_nanf("") : shift;
+    float w[16], sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      float t = fmaf(x[j], f, add);
-      if constexpr (MASK) t = x[j] == -__builtin_inff() ? x[j] : t;
-      w[j] = exp2_fast(t);
+      float s = fmaf(x[j], f, add);
+      if constexpr (MASK) s = x[j] == -__builtin_inff() ? x[j] : s;
+      w[j] = exp2_fast(s);
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) sum += w[j];
-    l = fmaf(sum, power2(vb == 255 ? 0 : -d), l);
+    l = fmaf(sum, exp2_fast(-(shift + fa)), l);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      uint32_t a[4], b[4];
+      uint32_t q[4], r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a[j] = pack_f16(w[8 * u + 2 * j], w[8 * u + 2 * j + 1]);
-        b[j] = pack_f16(rest_f16(w[8 * u + 2 * j]), rest_f16(w[8 * u + 2 * j + 1]));
+        q[j] = pack_f16(w[8 * u + 2 * j], w[8 * u + 2 * j + 1]);
+        r[j] = pack_f16(rest_f16(w[8 * u + 2 * j]), rest_f16(w[8 * u + 2 * j + 1]));
       }
-      p[u] = make_uint4(a[0], a[1], a[2], a[3]);
-      if constexpr (TWO) rest[u] = make_uint4(b[0], b[1], b[2], b[3]);
+      p[u] = make_uint4(q[0], q[1], q[2], q[3]);
+      if constexpr (TWO) rest[u] = make_uint4(r[0], r[1], r[2], r[3]);
     }
   }
 };
 
-// Where the results begin behind m and l of `splits` parts of `all` rows, on 16 bytes.
-__host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { return (2 * splits * all + 3) / 4 * 4; }
+// Where the results begin behind a, b and l of `splits` parts of `all` rows, on 16 bytes.
+__host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { return (3 * splits * all + 3) / 4 * 4; }
 
-// What sums and results under the maximum m count under the maximum `to`; l is
-// their sum: a part that saw nothing counts 0, one with NaN keys alone its NaN.
+// What sums or results relative to 2^m count relative to 2^to; l is their sum of
+// weights: a part that saw nothing counts 0, one with NaN alone its NaN.
 __device__ __forceinline__ float rescale(float m, float l, float to) {
   if (m == -__builtin_inff()) return l == 0.0f ? 0.0f : 1.0f;
   return exp2_fast(m - to);
 }
+
+// Results over their sum of weights; a row that sees nothing is 0.
+struct Quotient {
+  float n;
+  int e;
+  __device__ __forceinline__ Quotient(float a, float b, float l, int offset)
+      : n(l == 0.0f ? 0.0f : 1.0f / l), e(b == -__builtin_inff() ? 0 : static_cast<int>(b - a) - offset) {}
+  __device__ __forceinline__ float operator()(float y) const { return ldexpf(y * n, e); }
+};
 
 // Four results of one row from column d on.
 __device__ __forceinline__ void store4(void *y, bool bf16, int64_t i, float a, float b, float c, float d) {
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(kThreads, ND <= 4 && !TWO ? 2 : 1) void attention_r
                                                                                          int splits, float *parts,
                                                                                          int64_t first) {
   constexpr int kMeet = ND < 4 ? ND : 4;   // tiles of 32 columns that meet in LDS at a time
-  __shared__ float ms[kWaves][kRows], ls[kWaves][kRows];
+  __shared__ float as[kWaves][kRows], bs[kWaves][kRows], ls[kWaves][kRows];
   __shared__ __attribute__((aligned(16))) float meet[kWaves - 1][kRows][32 * kMeet + 4];
   const int64_t id = first + blockIdx.x;
   const int split = static_cast<int>(id % splits);
@@ -230,10 +231,6 @@ __global__ __launch_bounds__(kThreads, ND <= 4 && !TWO ? 2 : 1) void attention_r
       at = b < 0 ? 0 : static_cast<int>(b);
       bytes = b < 0 ? 0xFFFF : a.pool.ks[b] | a.pool.vs[b] << 8;
     }
-    int top = bytes >> 8 == 255 ? 0 : bytes >> 8;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = max(top, __shfl_xor(top, d));
-    st.raise(__builtin_amdgcn_readfirstlane(top));
 
     auto load = [&](Tile &x, int s) {
       const int b0 = __builtin_amdgcn_readlane(at, 2 * s), b1 = __builtin_amdgcn_readlane(at, 2 * s + 1);
@@ -298,26 +295,25 @@ __global__ __launch_bounds__(kThreads, ND <= 4 && !TWO ? 2 : 1) void attention_r
     }
   }
 
-  // the four waves' parts to one maximum, then their sums in order, by the first wave
+  // the four waves' parts relative to the same powers, then their sums in order, by the first wave
   st.l = add_xor32(st.l);
-  if (h == 0) ms[wave][c] = st.m, ls[wave][c] = st.l;
+  if (h == 0) as[wave][c] = st.a, bs[wave][c] = st.b, ls[wave][c] = st.l;
   __syncthreads();
-  float m = ms[0][c], l = 0.0f;
+  float ma = as[0][c], mb = bs[0][c], l = 0.0f;
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, ms[w][c]);
+  for (int w = 1; w < kWaves; ++w) ma = fmaxf(ma, as[w][c]), mb = fmaxf(mb, bs[w][c]);
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) l += ls[w][c] * rescale(ms[w][c], ls[w][c], m);
-  const float f = rescale(st.m, st.l, m);
-  const int e = st.e - 127 - State<ND, TWO>::kOffset;
+  for (int w = 0; w < kWaves; ++w) l += ls[w][c] * rescale(as[w][c], ls[w][c], ma);
+  const float f = rescale(st.b, st.l, mb);
+  const Quotient quotient(ma, mb, l, State<ND, TWO>::kOffset);
   const int64_t all = a.seqs.T * a.Hq, out = row * a.Hq + qh;
-  const float n = l == 0.0f ? 0.0f : 1.0f / l;   // a row that sees nothing is 0
 #pragma unroll
   for (int d0 = 0; d0 < ND; d0 += kMeet) {
     if (d0 > 0) __syncthreads();
 #pragma unroll
     for (int d = d0; d < ND && d < d0 + kMeet; ++d)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) st.y[d][j] = ldexpf(st.y[d][j] * f, e);
+      for (int j = 0; j < 16; ++j) st.y[d][j] *= f;
     if (wave > 0 && c < rows) {
 #pragma unroll
       for (int d = d0; d < ND && d < d0 + kMeet; ++d)
@@ -343,19 +339,20 @@ __global__ __launch_bounds__(kThreads, ND <= 4 && !TWO ? 2 : 1) void attention_r
           if (parts)
             *reinterpret_cast<float4 *>(parts + results_at(splits, all) + (split * all + out) * D + col) = sum;
           else
-            store4(a.y, types.out_bf16, out * D + col, sum.x * n, sum.y * n, sum.z * n, sum.w * n);
+            store4(a.y, types.out_bf16, out * D + col, quotient(sum.x), quotient(sum.y), quotient(sum.z), quotient(sum.w));
         }
     }
   }
   if (parts && wave == 0 && h == 0 && c < rows) {
-    parts[split * all + out] = m;
-    parts[(splits + split) * all + out] = l;
+    parts[split * all + out] = ma;
+    parts[(splits + split) * all + out] = mb;
+    parts[(2 * splits + split) * all + out] = l;
   }
 }
 
 // Joins the splits of a row in order.
-__global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types types, int splits, const float *parts,
-                                                           int64_t first) {
+__global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types types, int offset, int splits,
+                                                           const float *parts, int64_t first) {
   const int64_t all = a.seqs.T * a.Hq;
   const int D = static_cast<int>(a.pool.D), quads = D / 4;
   const int64_t u = first + blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
@@ -365,20 +362,20 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types typ
   const int64_t t = out / a.Hq;
   // rows in front of the first sequence or behind the last are left as they were
   if (t < Sequence::clamp(a.seqs.starts[0], a.seqs.T) || t >= Sequence::clamp(a.seqs.starts[a.seqs.N], a.seqs.T)) return;
-  float m = -__builtin_inff();
-  for (int s = 0; s < splits; ++s) m = fmaxf(m, parts[s * all + out]);
+  float ma = -__builtin_inff(), mb = ma;
+  for (int s = 0; s < splits; ++s) ma = fmaxf(ma, parts[s * all + out]), mb = fmaxf(mb, parts[(splits + s) * all + out]);
   float l = 0.0f;
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int s = 0; s < splits; ++s) {
-    const float ms = parts[s * all + out], ls = parts[(splits + s) * all + out];
+    const float ls = parts[(2 * splits + s) * all + out];
     if (ls == 0.0f) continue;             // saw nothing
-    const float f = rescale(ms, ls, m);
+    const float f = rescale(parts[(splits + s) * all + out], ls, mb);
     const float4 o = *reinterpret_cast<const float4 *>(parts + results_at(splits, all) + (s * all + out) * D + col);
-    l = fmaf(ls, f, l);
+    l = fmaf(ls, rescale(parts[s * all + out], ls, ma), l);
     sum.x = fmaf(o.x, f, sum.x), sum.y = fmaf(o.y, f, sum.y), sum.z = fmaf(o.z, f, sum.z), sum.w = fmaf(o.w, f, sum.w);
   }
-  const float n = l == 0.0f ? 0.0f : 1.0f / l;
-  store4(a.y, types.out_bf16, out * D + col, sum.x * n, sum.y * n, sum.z * n, sum.w * n);
+  const Quotient q(ma, mb, l, offset);
+  store4(a.y, types.out_bf16, out * D + col, q(sum.x), q(sum.y), q(sum.z), q(sum.w));
 }
 
 template <int ND, bool TWO>
@@ -392,7 +389,8 @@ void go_rows(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hi
   const int64_t quads = a.seqs.T * a.Hq * (a.pool.D / 4), per = most * kThreads;
   for (int64_t first = 0; first < quads; first += per) {
     const int64_t n = quads - first < per ? quads - first : per;
-    combine_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(a, t, p.splits, ws, first);
+    combine_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(
+        a, t, State<ND, TWO>::kOffset, p.splits, ws, first);
   }
 }
 
