@@ -24,164 +24,9 @@ namespace q4 {
 namespace {
 
 constexpr int kThreads = 256, kWaves = 4, kRows = 32;
-constexpr float kLog2e = 1.44269504088896340736f;
-
-struct Types {
-  bool in_bf16, out_bf16;
-};
-
-// A query row's 16 columns at a time, as operands: f[2 s], f[2 s + 1] are the
-// columns 32 s + 16 h .. + 15.
-template <int ND, bool TWO>
-struct Query {
-  uint4 hi[2 * ND], lo[TWO ? 2 * ND : 1];
-  float factor;   // what a product's result is multiplied with: scores in powers of two, without the key's scale
-  __device__ __forceinline__ void load(const AttnArgs &a, const Types &t, int64_t at, bool live, int h) {
-    const int D = static_cast<int>(a.pool.D);
-    float x[ND][16];
-    uint32_t top = 0;
-#pragma unroll
-    for (int s = 0; s < ND; ++s) {
-      const int c = 32 * s + 16 * h;
-      const bool in = live && c < D;
-#pragma unroll
-      for (int u = 0; u < 16; u += 8) {
-        if (t.in_bf16) {
-          Run8<true> r;
-          if (in) r.load(a.q, at + c + u);
-          else r.zero();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[s][u + j] = __uint_as_float(j & 1 ? r.v[j / 2] & 0xFFFF0000u : r.v[j / 2] << 16);
-        } else {
-          Run8<false> r;
-          if (in) r.load(a.q, at + c + u);
-          else r.zero();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[s][u + j] = r.v[j];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
-    }
-    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-    // exponent of the largest: top in [2^e, 2^(e + 1)); a NaN or an infinity makes the whole row NaN
-    const bool bad = top >= 0x7F800000u;
-    const int e = bad || top == 0 ? 0 : ilogbf(__uint_as_float(top));
-    factor = bad ? __builtin_nanf("") : ldexpf(fabsf(a.scale) * kLog2e, e - 14);
-#pragma unroll
-    for (int s = 0; s < ND; ++s)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t w[4], v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float n = a.scale < 0.0f ? -1.0f : 1.0f;
-          const float p = bad ? 0.0f : n * ldexpf(x[s][8 * u + 2 * j], 14 - e);
-          const float q = bad ? 0.0f : n * ldexpf(x[s][8 * u + 2 * j + 1], 14 - e);
-          w[j] = pack_f16(p, q);
-          v[j] = pack_f16(rest_f16(p), rest_f16(q));
-        }
-        hi[2 * s + u] = make_uint4(w[0], w[1], w[2], w[3]);
-        if constexpr (TWO) lo[2 * s + u] = make_uint4(v[0], v[1], v[2], v[3]);
-      }
-  }
-};
-
-// Running softmax of one query row a lane, which lanes c and c + 32 share.  Scores
-// are in powers of two; `a` and `b` are whole numbers: l is this half's sum of
-// weights 2^(s - a); y holds the results, sums of 2^(s + e - b + kOffset) times
-// codes, e the exponent of their values' scale.  So the weights that meet the
-// codes are rounded next to the largest product of a weight and its values'
-// scale, whatever the scales are.  b may be kLag, a 30 below what they follow.
-template <int ND, bool TWO>
-struct State {
-  static constexpr int kLag = TWO ? 1 : 6, kOffset = TWO ? 14 : 9;
-  float a = -__builtin_inff(), b = -__builtin_inff(), l = 0.0f;
-  f32x16 y[ND];
-  __device__ __forceinline__ State() {
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) y[d][j] = 0.0f;
-  }
-  // The weights of 16 keys' products x with the row, times f, under the scale
-  // bytes kb and vb of their block, as operands; hidden(j): the row does not see key j.
-  template <bool MASK, class F>
-  __device__ __forceinline__ void weights(f32x16 x, float f, int kb, int vb, F hidden, uint4 (&p)[2], uint4 (&rest)[2]) {
-    f *= kb == 255 ? __builtin_nanf("") : __uint_as_float(kb ? static_cast<uint32_t>(kb) << 23 : 0x400000u);
-    if constexpr (MASK) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = hidden(j) ? -__builtin_inff() : x[j] * f;
-      f = 1.0f;
-    }
-    float top = x[0];
-#pragma unroll
-    for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
-    top *= f;
-    const float e = static_cast<float>(vb - 127), ta = max_xor32(top), tb = max_xor32(top + e);
-    if (__any(ta > a + 30.0f || tb > b + static_cast<float>(kLag))) {
-      const float na = fmaxf(a, ceilf(ta)), nb = fmaxf(b, ceilf(tb));
-      const float ga = a == na ? 1.0f : exp2_fast(a - na), gb = b == nb ? 1.0f : exp2_fast(b - nb);   // from -inf: 0
-      a = na, b = nb;
-      l *= ga;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[d][j] *= gb;
-    }
-    // nothing seen so far: any finite number will do
-    const float fa = a == -__builtin_inff() ? 0.0f : a, fb = b == -__builtin_inff() ? 0.0f : b;
-    // weights of 2^-60 and less of what counts are 0 as halves; kept that large, their f32 sum stays right
-    const float shift = fmaxf(e + static_cast<float>(kOffset) - fb, -60.0f - fa);
-    const float add = vb == 255 ? __builtin_nanf("") : shift;
-    float w[16], sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float s = fmaf(x[j], f, add);
-      if constexpr (MASK) s = x[j] == -__builtin_inff() ? x[j] : s;
-      w[j] = exp2_fast(s);
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) sum += w[j];
-    l = fmaf(sum, exp2_fast(-(shift + fa)), l);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint32_t q[4], r[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[j] = pack_f16(w[8 * u + 2 * j], w[8 * u + 2 * j + 1]);
-        r[j] = pack_f16(rest_f16(w[8 * u + 2 * j]), rest_f16(w[8 * u + 2 * j + 1]));
-      }
-      p[u] = make_uint4(q[0], q[1], q[2], q[3]);
-      if constexpr (TWO) rest[u] = make_uint4(r[0], r[1], r[2], r[3]);
-    }
-  }
-};
 
 // Where the results begin behind a, b and l of `splits` parts of `all` rows, on 16 bytes.
 __host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { return (3 * splits * all + 3) / 4 * 4; }
-
-// What sums or results relative to 2^m count relative to 2^to; l is their sum of
-// weights: a part that saw nothing counts 0, one with NaN alone its NaN.
-__device__ __forceinline__ float rescale(float m, float l, float to) {
-  if (m == -__builtin_inff()) return l == 0.0f ? 0.0f : 1.0f;
-  return exp2_fast(m - to);
-}
-
-// Results over their sum of weights; a row that sees nothing is 0.
-struct Quotient {
-  float n;
-  int e;
-  __device__ __forceinline__ Quotient(float a, float b, float l, int offset)
-      : n(l == 0.0f ? 0.0f : 1.0f / l), e(b == -__builtin_inff() ? 0 : static_cast<int>(b - a) - offset) {}
-  __device__ __forceinline__ float operator()(float y) const { return ldexpf(y * n, e); }
-};
-
-// Four results of one row from column d on.
-__device__ __forceinline__ void store4(void *y, bool bf16, int64_t i, float a, float b, float c, float d) {
-  if (bf16) store_any(static_cast<uint16_t *>(y) + i, make_uint2(pack_bf16(a, b), pack_bf16(c, d)));
-  else store_any(static_cast<float *>(y) + i, make_float4(a, b, c, d));
-}
 
 // Few rows a sequence: a workgroup has 32 rows of one key head and a share of
 // their keys; its four waves share those out again, 32 keys a step straight from
@@ -198,8 +43,10 @@ __global__ __launch_bounds__(kThreads, ND <= 4 && !TWO ? 2 : 1) void attention_r
   const int split = static_cast<int>(id % splits);
   const int64_t head = id / splits % a.pool.Hk, slot = id / splits / a.pool.Hk;
   const int64_t G = a.Hq / a.pool.Hk;
-  const RowTile tile(a.seqs, slot, G, kRows);
+  RowTile tile(a.seqs, slot, G, kRows);
   if (tile.i < 0) return;
+  tile.i = uniform(tile.i), tile.r0 = uniform(tile.r0), tile.rows = uniform(tile.rows);
+  tile.s.row = uniform(tile.s.row), tile.s.first = uniform(tile.s.first);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
   const int D = static_cast<int>(a.pool.D);
   const int rows = tile.rows - tile.r0 < kRows ? static_cast<int>(tile.rows - tile.r0) : kRows;
@@ -411,8 +258,12 @@ void go(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hipStre
 }  // namespace
 
 AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len, int64_t window,
-                        int64_t sinks, int) {
+                        int64_t sinks, int path) {
   AttnPlan p = {};
+  p.splits = 1;
+  // rows of one key head a sequence, on average
+  p.tiled = path == kPathTiled || (path == kPathAuto && T * (Hq / Hk) / N >= 64);
+  if (p.tiled) return p;
   const int64_t G = Hq / Hk, groups = tile_slots(T, N, G, kRows) * Hk;
   int64_t keys = max_len;
   if (window > 0 && window + sinks + 32 < keys) keys = window + sinks + 32;
@@ -426,6 +277,7 @@ AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D,
 
 hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, bool bf16, bool out_bf16, void *ws, hipStream_t st) {
   const Types t = {bf16, out_bf16};
+  if (p.tiled) return launch_attention_tiled(a, t, st);
   if (bf16 && out_bf16) go<false>(a, t, p, static_cast<float *>(ws), st);
   else go<true>(a, t, p, static_cast<float *>(ws), st);
   return hipGetLastError();

@@ -37,8 +37,12 @@ __device__ __forceinline__ float rest_f16(float v) { return v - static_cast<floa
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// 2^n as a float, n in -126 .. 127.
-__device__ __forceinline__ float power2(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
+// What all lanes have the same of, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v)), hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
 
 // Rows of a tile: row r of a sequence and key head is query head g = r mod G of
 // that key head's G, of the sequence's row r / G, so that all rows of a tile
@@ -77,5 +81,174 @@ struct KeyBlocks {
   }
   __device__ __forceinline__ int block(int v) const { return v < sink_blocks ? v : v + skip; }
 };
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Types {
+  bool in_bf16, out_bf16;
+};
+
+// A query row's 16 columns at a time, as operands: f[2 s], f[2 s + 1] are the
+// columns 32 s + 16 h .. + 15.
+template <int ND, bool TWO>
+struct Query {
+  uint4 hi[2 * ND], lo[TWO ? 2 * ND : 1];
+  float factor;   // what a product's result is multiplied with: scores in powers of two, without the key's scale
+  __device__ __forceinline__ void load(const AttnArgs &a, const Types &t, int64_t at, bool live, int h) {
+    const int D = static_cast<int>(a.pool.D);
+    float x[ND][16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int s = 0; s < ND; ++s) {
+      const int c = 32 * s + 16 * h;
+      const bool in = live && c < D;
+#pragma unroll
+      for (int u = 0; u < 16; u += 8) {
+        if (t.in_bf16) {
+          Run8<true> r;
+          if (in) r.load(a.q, at + c + u);
+          else r.zero();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[s][u + j] = __uint_as_float(j & 1 ? r.v[j / 2] & 0xFFFF0000u : r.v[j / 2] << 16);
+        } else {
+          Run8<false> r;
+          if (in) r.load(a.q, at + c + u);
+          else r.zero();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[s][u + j] = r.v[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
+    }
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+    // exponent of the largest: top in [2^e, 2^(e + 1)); a NaN or an infinity makes the whole row NaN
+    const bool bad = top >= 0x7F800000u;
+    const int e = bad || top == 0 ? 0 : ilogbf(__uint_as_float(top));
+    factor = bad ? __builtin_nanf("") : ldexpf(fabsf(a.scale) * kLog2e, e - 14);
+#pragma unroll
+    for (int s = 0; s < ND; ++s)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t w[4], v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float n = a.scale < 0.0f ? -1.0f : 1.0f;
+          const float p = bad ? 0.0f : n * ldexpf(x[s][8 * u + 2 * j], 14 - e);
+          const float q = bad ? 0.0f : n * ldexpf(x[s][8 * u + 2 * j + 1], 14 - e);
+          w[j] = pack_f16(p, q);
+          v[j] = pack_f16(rest_f16(p), rest_f16(q));
+        }
+        hi[2 * s + u] = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (TWO) lo[2 * s + u] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+  }
+};
+
+// Running softmax of one query row a lane, which lanes c and c + 32 share.  Scores
+// are in powers of two; `a` and `b` are whole numbers: l is this half's sum of
+// weights 2^(s - a); y holds the results, sums of 2^(s + e - b + kOffset) times
+// codes, e the exponent of their values' scale.  So the weights that meet the
+// codes are rounded next to the largest product of a weight and its values'
+// scale, whatever the scales are.  No maximum is taken as long as the weights
+// stay halves: their sum, which is needed anyway, tells.
+template <int ND, bool TWO>
+struct State {
+  static constexpr int kOffset = TWO ? 10 : 9;
+  float a = -__builtin_inff(), b = -__builtin_inff(), l = 0.0f;
+  f32x16 y[ND];
+  __device__ __forceinline__ State() {
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[d][j] = 0.0f;
+  }
+  // The weights of 16 keys' products x with the row, times f, under the scale
+  // bytes kb and vb of their block, as operands; hidden(j): the row does not see key j.
+  template <bool MASK, class F>
+  __device__ __forceinline__ void weights(f32x16 x, float f, int kb, int vb, F hidden, uint4 (&p)[2], uint4 (&rest)[2]) {
+    f *= kb == 255 ? __builtin_nanf("") : __uint_as_float(kb ? static_cast<uint32_t>(kb) << 23 : 0x400000u);
+    if constexpr (MASK) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = hidden(j) ? -__builtin_inff() : x[j] * f;
+      f = 1.0f;
+    }
+    const float e = static_cast<float>(vb - 127);
+    float w[16], sum, shift, fa;
+    auto weigh = [&] {
+      // nothing seen so far: any finite number will do
+      fa = a == -__builtin_inff() ? 0.0f : a;
+      // weights of 2^-60 and less of what counts are 0 as halves; kept that large, their f32 sum stays right
+      shift = fmaxf(e + static_cast<float>(kOffset) - (b == -__builtin_inff() ? 0.0f : b), -60.0f - fa);
+      const float add = vb == 255 ? __builtin_nanf("") : shift;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float s = fmaf(x[j], f, add);
+        if constexpr (MASK) s = x[j] == -__builtin_inff() ? x[j] : s;
+        w[j] = exp2_fast(s);
+      }
+      float t[8];   // sums in pairs
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = w[2 * j] + w[2 * j + 1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[j] = t[2 * j] + t[2 * j + 1];
+      sum = (t[0] + t[1]) + (t[2] + t[3]);
+    };
+    weigh();
+    if (__any(b == -__builtin_inff() || sum > 32768.0f || shift <= -60.0f - fa)) {
+      float top = x[0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
+      top *= f;
+      const float na = fmaxf(a, ceilf(max_xor32(top))), nb = fmaxf(b, ceilf(max_xor32(top + e)));
+      const float ga = a == na ? 1.0f : exp2_fast(a - na), gb = b == nb ? 1.0f : exp2_fast(b - nb);   // from -inf: 0
+      a = na, b = nb;
+      l *= ga;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[d][j] *= gb;
+      weigh();
+    }
+    l = fmaf(sum, exp2_fast(-(shift + fa)), l);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t q[4], r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        q[j] = pack_f16(w[8 * u + 2 * j], w[8 * u + 2 * j + 1]);
+        r[j] = pack_f16(rest_f16(w[8 * u + 2 * j]), rest_f16(w[8 * u + 2 * j + 1]));
+      }
+      p[u] = make_uint4(q[0], q[1], q[2], q[3]);
+      if constexpr (TWO) rest[u] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+  }
+};
+
+// What sums or results relative to 2^m count relative to 2^to; l is their sum of
+// weights: a part that saw nothing counts 0, one with NaN alone its NaN.
+__device__ __forceinline__ float rescale(float m, float l, float to) {
+  if (m == -__builtin_inff()) return l == 0.0f ? 0.0f : 1.0f;
+  return exp2_fast(m - to);
+}
+
+// Results over their sum of weights; a row that sees nothing is 0.
+struct Quotient {
+  float n;
+  int e;
+  __device__ __forceinline__ Quotient(float a, float b, float l, int offset)
+      : n(l == 0.0f ? 0.0f : 1.0f / l), e(b == -__builtin_inff() ? 0 : static_cast<int>(b - a) - offset) {}
+  __device__ __forceinline__ float operator()(float y) const { return ldexpf(y * n, e); }
+};
+
+// Four results of one row from column d on.
+__device__ __forceinline__ void store4(void *y, bool bf16, int64_t i, float a, float b, float c, float d) {
+  if (bf16) store_any(static_cast<uint16_t *>(y) + i, make_uint2(pack_bf16(a, b), pack_bf16(c, d)));
+  else store_any(static_cast<float *>(y) + i, make_float4(a, b, c, d));
+}
+
+
+// Many rows a sequence (attention_tiled.hip); launch_attention chooses.
+hipError_t launch_attention_tiled(const AttnArgs &a, const Types &t, hipStream_t st);
 
 }  // namespace q4

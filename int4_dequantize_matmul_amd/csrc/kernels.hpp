@@ -221,6 +221,8 @@ struct AttnArgs {
   float scale;
   int64_t window, sinks;        // window 0: none
 };
+// The routes that attention_plan knows (values of q4_path); any other means few rows.
+constexpr int kPathAuto = 0, kPathTiled = 3;
 // How a call is shared out; from sizes alone, so that the workspace is known before.
 struct AttnPlan {
   bool tiled;      // LDS-tiled kernel for many rows a sequence, else waves that share out the keys

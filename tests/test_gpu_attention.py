@@ -9,7 +9,7 @@ largest (f32: two halves) or exact to 2^-25 of it (bf16).  Weights have half a
 step of 2^-11 (bf16 in and out) or 2^-22, the exponential two steps of f32; n
 keys are summed in chains of n / 16 and some joints.  Halves end at steps of
 2^-24, so a weight times its values' scale is off by half of that where the
-largest such product is 2^8 or more (2^13 with two halves): n times 2^-33 (2^-38)
+largest such product is 2^8 or more (2^9 with two halves): n times 2^-33 (2^-34)
 of `peak`, the largest, in all.  bf16 results are rounded once more, 2^-8 of
 themselves.
 """
@@ -53,7 +53,7 @@ def check(y, q, pool, pages, starts, lengths, scale, window=0, sinks=0, what="")
     h = 2.0 ** -24
     score = (D + 12) * h * terms + (2.0 ** -22 if q.dtype == torch.float32 else 2.0 ** -25) * flat
     weight = score + (2.0 ** -11 if coarse else 2.0 ** -22) + 4 * h
-    tol = (2 * weight + (n / 8 + 64) * h)[..., None] * size + (n * (2.0 ** -33 if coarse else 2.0 ** -38) * peak)[..., None]
+    tol = (2 * weight + (n / 8 + 64) * h)[..., None] * size + (n * (2.0 ** -33 if coarse else 2.0 ** -34) * peak)[..., None]
     if y.dtype == torch.bfloat16:
         tol = tol + 2.0 ** -8 * np.abs(ref)
     got = f64(y)
@@ -168,7 +168,7 @@ def test_values_of_extreme_scales(path):
         y = q4.q8_attention(q, on_gpu(pool), dev(pages), i32([0, 40]), i32([1100]))
         ref = S.attention(f64(q), pool, pages, [0, 40], [1100], np.float32(32 ** -0.5))
         tol = (2 * (2.0 ** -24 * 44 * ref[2] + 2.0 ** -22 * ref[3] + 2.0 ** -21) + 202 * 2.0 ** -24)[..., None] * ref[1]
-        tol = tol + (1100 * 2.0 ** -38 * ref[4])[..., None]
+        tol = tol + (1100 * 2.0 ** -34 * ref[4])[..., None]
         assert np.all(np.abs(f64(y) - ref[0]) <= tol + 2.0 ** -148), (low, high)
     # blocks of zeros under scale 0 in front of and between others
     pool = random_pool(rng, P, 1, 16, 32)
