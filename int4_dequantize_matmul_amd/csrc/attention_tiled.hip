@@ -43,9 +43,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   const int pos = static_cast<int>(at_pos + t);
   const int64_t p0 = at_pos + wr / G, p1 = at_pos + (active ? wr + rows - 1 : wr) / G;
 
-  Query<ND, TWO> q;
+  Query<ND, 2, TWO> q;
   q.load(a, types, active ? row * a.q_t + qh * a.q_h : 0, active, h);
-  State<ND, TWO> st;
+  State<f32x16, ND, 2, TWO> st;
 
   // blocks of 64 keys' worth a lane, two rounds ahead: pages, then scales
   struct Info {
@@ -123,11 +123,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
       }
       const int by = h ? m1.x : m0.x, key = h ? k1 : k0;
       auto whole = [&](int b) { return b + 15 <= p0 && (b > p1 - window || b + 15 < a.sinks); };
+      float x[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = acc[j];
       uint4 p[2], rest[2];
       if (whole(k0) && whole(k1)) {
-        st.template weights<false>(acc, q.factor, by & 255, by >> 8, [](int) { return false; }, p, rest);
+        st.template weights<false>(x, q.factor, by & 255, by >> 8, [](int) { return false; }, p, rest);
       } else {
-        st.template weights<true>(acc, q.factor, by & 255, by >> 8,
+        st.template weights<true>(x, q.factor, by & 255, by >> 8,
                                   [&](int j) {
                                     const int k = key + j;
                                     return k > pos || (k <= pos - window && k >= a.sinks);
@@ -159,7 +162,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
     lds_barrier();
   }
 
-  const Quotient quotient(st.a, st.b, add_xor32(st.l), State<ND, TWO>::kOffset);
+  const Quotient quotient(st.a, st.b, add_xor32(st.l), decltype(st)::kOffset);
   if (c >= rows) return;
   const int64_t out = (row * a.Hq + qh) * D;
 #pragma unroll

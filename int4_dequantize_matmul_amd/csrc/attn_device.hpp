@@ -14,6 +14,12 @@ __device__ __forceinline__ f32x16 mfma_f16_32x32x16(uint4 a, uint4 b, f32x16 c) 
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// acc += A B over 32 columns of 16 rows: lane (r, q) has 8 columns of row r; result register i of lane (c, q) is the
+// element of A's row 4 q + i and B's row c.
+__device__ __forceinline__ f32x4 mfma_f16_16x16x32(uint4 a, uint4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
 // Four int8 codes -> four halves, exactly: with the sign bit turned, a byte b
 // under the exponent 0x64 is the half 1024 + b, b = code + 128.
 __device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
@@ -88,19 +94,19 @@ struct Types {
   bool in_bf16, out_bf16;
 };
 
-// A query row's 16 columns at a time, as operands: f[2 s], f[2 s + 1] are the
-// columns 32 s + 16 h .. + 15.
-template <int ND, bool TWO>
+// A query row as operands, S lanes a row (2 or 4), lane h of them with the columns 16 (S s + h) .. + 15 in f[2 s] and
+// f[2 s + 1].
+template <int N, int S, bool TWO>
 struct Query {
-  uint4 hi[2 * ND], lo[TWO ? 2 * ND : 1];
+  uint4 hi[2 * N], lo[TWO ? 2 * N : 1];
   float factor;   // what a product's result is multiplied with: scores in powers of two, without the key's scale
   __device__ __forceinline__ void load(const AttnArgs &a, const Types &t, int64_t at, bool live, int h) {
     const int D = static_cast<int>(a.pool.D);
-    float x[ND][16];
+    float x[N][16];
     uint32_t top = 0;
 #pragma unroll
-    for (int s = 0; s < ND; ++s) {
-      const int c = 32 * s + 16 * h;
+    for (int s = 0; s < N; ++s) {
+      const int c = 16 * (S * s + h);
       const bool in = live && c < D;
 #pragma unroll
       for (int u = 0; u < 16; u += 8) {
@@ -121,21 +127,22 @@ struct Query {
 #pragma unroll
       for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[s][j]) & 0x7FFFFFFFu);
     }
+    if constexpr (S == 4) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
     top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
     // exponent of the largest: top in [2^e, 2^(e + 1)); a NaN or an infinity makes the whole row NaN
     const bool bad = top >= 0x7F800000u;
     const int e = bad || top == 0 ? 0 : ilogbf(__uint_as_float(top));
     factor = bad ? __builtin_nanf("") : ldexpf(fabsf(a.scale) * kLog2e, e - 14);
+    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
-    for (int s = 0; s < ND; ++s)
+    for (int s = 0; s < N; ++s)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t w[4], v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float n = a.scale < 0.0f ? -1.0f : 1.0f;
-          const float p = bad ? 0.0f : n * ldexpf(x[s][8 * u + 2 * j], 14 - e);
-          const float q = bad ? 0.0f : n * ldexpf(x[s][8 * u + 2 * j + 1], 14 - e);
+          const float p = bad ? 0.0f : sign * ldexpf(x[s][8 * u + 2 * j], 14 - e);
+          const float q = bad ? 0.0f : sign * ldexpf(x[s][8 * u + 2 * j + 1], 14 - e);
           w[j] = pack_f16(p, q);
           v[j] = pack_f16(rest_f16(p), rest_f16(q));
         }
@@ -145,28 +152,42 @@ struct Query {
   }
 };
 
-// Running softmax of one query row a lane, which lanes c and c + 32 share.  Scores
-// are in powers of two; `a` and `b` are whole numbers: l is this half's sum of
+// The largest of the S lanes' values, and their sum.
+template <int S>
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (S == 4) v = max_xor16(v);
+  return max_xor32(v);
+}
+template <int S>
+__device__ __forceinline__ float row_sum(float v) {
+  if constexpr (S == 4) v = add_xor16(v);
+  return add_xor32(v);
+}
+
+// Running softmax of one query row a lane, which S lanes share (2 or 4), each with
+// the scores of one block of 16 keys a step.  Scores
+// are in powers of two; `a` and `b` are whole numbers: l is this lane's sum of
 // weights 2^(s - a); y holds the results, sums of 2^(s + e - b + kOffset) times
 // codes, e the exponent of their values' scale.  So the weights that meet the
 // codes are rounded next to the largest product of a weight and its values'
 // scale, whatever the scales are.  No maximum is taken as long as the weights
 // stay halves: their sum, which is needed anyway, tells.
-template <int ND, bool TWO>
+template <class V, int N, int S, bool TWO>   // N vectors of results
 struct State {
   static constexpr int kOffset = TWO ? 10 : 9;
   float a = -__builtin_inff(), b = -__builtin_inff(), l = 0.0f;
-  f32x16 y[ND];
+  V y[N];
+  static constexpr int kWidth = sizeof(V) / sizeof(float);
   __device__ __forceinline__ State() {
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < N; ++d)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) y[d][j] = 0.0f;
+      for (int j = 0; j < kWidth; ++j) y[d][j] = 0.0f;
   }
   // The weights of 16 keys' products x with the row, times f, under the scale
   // bytes kb and vb of their block, as operands; hidden(j): the row does not see key j.
   template <bool MASK, class F>
-  __device__ __forceinline__ void weights(f32x16 x, float f, int kb, int vb, F hidden, uint4 (&p)[2], uint4 (&rest)[2]) {
+  __device__ __forceinline__ void weights(float (&x)[16], float f, int kb, int vb, F hidden, uint4 (&p)[2], uint4 (&rest)[2]) {
     f *= kb == 255 ? __builtin_nanf("") : __uint_as_float(kb ? static_cast<uint32_t>(kb) << 23 : 0x400000u);
     if constexpr (MASK) {
 #pragma unroll
@@ -200,14 +221,14 @@ struct State {
 #pragma unroll
       for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
       top *= f;
-      const float na = fmaxf(a, ceilf(max_xor32(top))), nb = fmaxf(b, ceilf(max_xor32(top + e)));
+      const float na = fmaxf(a, ceilf(row_max<S>(top))), nb = fmaxf(b, ceilf(row_max<S>(top + e)));
       const float ga = a == na ? 1.0f : exp2_fast(a - na), gb = b == nb ? 1.0f : exp2_fast(b - nb);   // from -inf: 0
       a = na, b = nb;
       l *= ga;
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+      for (int d = 0; d < N; ++d)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[d][j] *= gb;
+        for (int j = 0; j < kWidth; ++j) y[d][j] *= gb;
       weigh();
     }
     l = fmaf(sum, exp2_fast(-(shift + fa)), l);
