@@ -37,6 +37,11 @@ HIP_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-result", f"-I{INCLUDE}",
 ]
+# Results of 16 or 32 rows live in vectors of up to 16 registers over a kernel's
+# loop; taken apart at the loop's head, each step copied them (64 moves of a
+# wave's about 250 other vector instructions).
+WHOLE_VECTORS = ["-mllvm", "-amdgpu-codegenprepare-break-large-phis=false"]
+FILE_FLAGS = {"attention.hip": WHOLE_VECTORS, "attention_tiled.hip": WHOLE_VECTORS}
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-Wextra", f"-I{INCLUDE}"]
 
 
@@ -71,7 +76,7 @@ def build(verbose: bool = False) -> str:
     jobs = []
     for src in sorted(glob.glob(os.path.join(CSRC, "*.hip"))):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        jobs.append([HIPCC, *HIP_FLAGS, "-c", src, "-o", obj])
+        jobs.append([HIPCC, *HIP_FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj])
     for src in sorted(glob.glob(os.path.join(CSRC, "*.cpp"))):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         jobs.append(["g++", *CXX_FLAGS, "-c", src, "-o", obj])

@@ -55,10 +55,11 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
   const int rows = n - r0 < kRows ? static_cast<int>(n - r0) : kRows;
   const int64_t r = r0 + (c < rows ? c : rows - 1), t = r / G;
   const int64_t row = at_row + t, qh = head * G + (r - t * G);
-  const int64_t p0 = at_pos + r0 / G, p1 = at_pos + (r0 + rows - 1) / G;
-  const int pos = static_cast<int>(at_pos + t);   // int32 lengths
+  // lengths are int32, and so positions
+  const int p0 = static_cast<int>(at_pos + r0 / G), p1 = static_cast<int>(at_pos + (r0 + rows - 1) / G);
+  const int pos = static_cast<int>(at_pos + t);
   const KeyBlocks keys(p0, p1, a.window, a.sinks);
-  const int64_t window = a.window > 0 ? a.window : INT64_C(1) << 40;
+  const Sight sight(a.window, a.sinks);
 
   const int steps = (keys.count + 3) / 4;
   const int w0 = static_cast<int>(static_cast<int64_t>(steps) * (split * kWaves + wave) / (splits * kWaves));
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
     for (int s = w0; s < w1; ++s) {
       const int l = (s - w0) & 15;
       const int bytes = __shfl(cur.bytes, 4 * l + q4), k0 = __shfl(cur.blk, 4 * l + q4) * kKvBlock;
-      float x[16];
+      f32x16 x;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         f32x4 acc = {};
@@ -142,28 +143,21 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
       if (l == 15) cur = next;
       if (s + 1 < w1) load_keys((l + 1) & 15);
       __builtin_amdgcn_sched_barrier(0);
-      // whether all rows see all of this lane's block
-      const bool all = k0 + 15 <= p0 && (k0 > p1 - window || k0 + 15 < a.sinks);
-      uint4 p[2], rest[2];
-      if (__all(all)) {
-        st.template weights<false>(x, q.factor, bytes & 255, bytes >> 8, [](int) { return false; }, p, rest);
-      } else {
-        st.template weights<true>(x, q.factor, bytes & 255, bytes >> 8,
-                                  [&](int j) {
-                                    const int key = k0 + j;
-                                    return key > pos || (key <= pos - window && key >= a.sinks);
-                                  },
-                                  p, rest);
-      }
+      typename decltype(st)::Keys w[1];
+      if (__all(sight.whole(p0, p1, k0)))
+        w[0].template scores<false>(x, q.factor, bytes & 255, bytes >> 8, [](int) { return false; });
+      else
+        w[0].template scores<true>(x, q.factor, bytes & 255, bytes >> 8, [&](int j) { return sight.hides(pos, k0 + j); });
+      st.weights(w);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int d = 0; d < NV; ++d) {
         const uint4 lo = codes_to_f16(v[d].x, v[d].y), hi = codes_to_f16(v[d].z, v[d].w);
-        st.y[d] = mfma_f16_16x16x32(lo, p[0], st.y[d]);
-        st.y[d] = mfma_f16_16x16x32(hi, p[1], st.y[d]);
+        st.y[d] = mfma_f16_16x16x32(lo, w[0].p[0], st.y[d]);
+        st.y[d] = mfma_f16_16x16x32(hi, w[0].p[1], st.y[d]);
         if constexpr (TWO) {
-          st.y[d] = mfma_f16_16x16x32(lo, rest[0], st.y[d]);
-          st.y[d] = mfma_f16_16x16x32(hi, rest[1], st.y[d]);
+          st.y[d] = mfma_f16_16x16x32(lo, w[0].rest[0], st.y[d]);
+          st.y[d] = mfma_f16_16x16x32(hi, w[0].rest[1], st.y[d]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);

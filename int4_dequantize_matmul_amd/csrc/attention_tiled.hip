@@ -5,8 +5,10 @@
 // side by side.  Keys and values of a step (64 keys, 32 past 128 columns) become
 // halves once, on their way to LDS, where they lie as the matrix instructions'
 // operands, 16 bytes a lane, 1 KB an instruction, so that neither writes nor
-// reads conflict.  Two buffers; a step's codes are loaded while the step before
-// the last is multiplied, one barrier a step that waits for LDS alone.
+// reads conflict.  Operands come to registers four at a time, those of the next
+// four instructions before these four.  Two buffers of LDS; a step's codes are
+// loaded while the step before the last is multiplied; one barrier a step, which
+// waits for LDS alone.
 #include "attn_device.hpp"
 
 namespace q4 {
@@ -19,7 +21,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   constexpr int kRows = 32 * WAVES, kOps = 2 * ND;             // operands of 1 KB of one product and 32 keys
   constexpr int kLoads = (TILES * 2 * ND + WAVES - 1) / WAVES; // 16-byte loads of a lane a step
   constexpr int kSteps = 32 / TILES;                           // steps whose blocks the 64 lanes hold
-  __shared__ uint4 ops[2][TILES][2][kOps][64];
+  __shared__ uint4 key_ops[2][TILES][kOps][64], value_ops[2][TILES][kOps][64];
   __shared__ int2 blocks[2][2 * TILES];                        // scale bytes and first key of a step's blocks
   const int64_t id = first + blockIdx.x;
   // heads next to each other go to different XCDs, each with its keys in an L2 of its own; long rows first
@@ -32,16 +34,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   const int64_t r0 = uniform(tile.r0), n = uniform(tile.rows), at_row = uniform(tile.s.row), at_pos = uniform(tile.s.first);
   const int64_t last = r0 + kRows < n ? r0 + kRows - 1 : n - 1;
   const KeyBlocks keys(at_pos + r0 / G, at_pos + last / G, a.window, a.sinks);
-  const int64_t window = a.window > 0 ? a.window : INT64_C(1) << 40;
-
   // this wave's rows
   const int64_t wr = r0 + 32 * wave;
   const bool active = wr <= last;
   const int rows = !active ? 0 : last - wr < 31 ? static_cast<int>(last - wr) + 1 : 32;
   const int64_t r = wr + (c < rows ? c : rows - 1), t = r / G;
   const int64_t row = at_row + t, qh = head * G + (r - t * G);
+  // lengths are int32, and so positions
   const int pos = static_cast<int>(at_pos + t);
-  const int64_t p0 = at_pos + wr / G, p1 = at_pos + (active ? wr + rows - 1 : wr) / G;
+  const int p0 = static_cast<int>(at_pos + wr / G), p1 = static_cast<int>(at_pos + (active ? wr + rows - 1 : wr) / G);
+  const Sight sight(a.window, a.sinks);
 
   Query<ND, 2, TWO> q;
   q.load(a, types, active ? row * a.q_t + qh * a.q_h : 0, active, h);
@@ -69,7 +71,29 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   Info cur = info_of(0, page_of(0)), next = info_of(1, page_of(1));
   int page = page_of(2);
 
+  // This wave's loads of a step: load u is of keys or values, of 32 columns of one
+  // tile, which of two blocks by lane.  Columns past D, which the query has as 0 or
+  // no result asks for, are the last ones again.
   uint4 raw[kLoads];
+  int from[kLoads], to[kLoads];        // bytes from the block on; 16 bytes of LDS
+  bool second[kLoads];
+  const int8_t *base[kLoads];
+  const int unit = kKvBlock * D;
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int x = wave + WAVES * u, tl = x / (2 * ND), d = x / 2 % ND;
+    to[u] = (tl * kOps + 2 * d) * 64 + lane;
+    if (x & 1) {
+      base[u] = a.pool.v;
+      from[u] = min(32 * d + c, D - 1) * 16;
+      second[u] = h;
+    } else {
+      // row c of the first product is key 16 (c / 4 mod 2) + 4 (c / 8) + c mod 4
+      base[u] = a.pool.k;
+      from[u] = min(2 * d + h, D / 16 - 1) * 256 + (4 * (c >> 3) + (c & 3)) * 16;
+      second[u] = c & 4;
+    }
+  }
   auto load = [&](int s) {
     const int l = s % kSteps;
     if (l == 0 && s > 0) {
@@ -79,72 +103,90 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
     }
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      const int x = wave + WAVES * u, tl = x / (2 * ND), d = x / 2 % ND;
-      raw[u] = make_uint4(0, 0, 0, 0);
+      const int x = wave + WAVES * u, tl = x / (2 * ND);
       if (x >= TILES * 2 * ND) continue;
       const int b0 = __builtin_amdgcn_readlane(cur.at, 2 * TILES * l + 2 * tl);
       const int b1 = __builtin_amdgcn_readlane(cur.at, 2 * TILES * l + 2 * tl + 1);
-      if (x & 1) {
-        const int8_t *p = a.pool.v + static_cast<int64_t>(h ? b1 : b0) * (kKvBlock * D);
-        if (32 * d + c < D) raw[u] = load16(p + (32 * d + c) * 16);
-      } else {
-        // row c of the first product is key 16 (c / 4 mod 2) + 4 (c / 8) + c mod 4
-        const int8_t *p = a.pool.k + static_cast<int64_t>(c & 4 ? b1 : b0) * (kKvBlock * D);
-        if (32 * d + 16 * h < D) raw[u] = load16(p + (2 * d + h) * 256 + (4 * (c >> 3) + (c & 3)) * 16);
-      }
+      raw[u] = load16(base[u] + (static_cast<int64_t>(second[u] ? b1 : b0) * unit + from[u]));
     }
   };
   // the codes that load(s) brought; called before load(s + 1)
   auto store = [&](int s) {
-    const int buf = s & 1;
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      const int x = wave + WAVES * u, tl = x / (2 * ND), d = x / 2 % ND;
+      const int x = wave + WAVES * u;
       if (x >= TILES * 2 * ND) continue;
-      ops[buf][tl][x & 1][2 * d][lane] = codes_to_f16(raw[u].x, raw[u].y);
-      ops[buf][tl][x & 1][2 * d + 1][lane] = codes_to_f16(raw[u].z, raw[u].w);
+      uint4 *p = (x & 1 ? &value_ops[s & 1][0][0][0] : &key_ops[s & 1][0][0][0]) + to[u];
+      p[0] = codes_to_f16(raw[u].x, raw[u].y);
+      p[64] = codes_to_f16(raw[u].z, raw[u].w);
     }
     if (wave == 0 && lane / (2 * TILES) == s % kSteps)
-      blocks[buf][lane % (2 * TILES)] = make_int2(cur.bytes, cur.blk * kKvBlock);
+      blocks[s & 1][lane % (2 * TILES)] = make_int2(cur.bytes, cur.blk * kKvBlock);
   };
-  auto compute = [&](int buf) {
+  constexpr int kAll = TILES * kOps, kGroup = 4, kGroups = (kAll + kGroup - 1) / kGroup;
+  auto fetch_ops = [&](uint4 (&to)[kGroup], const uint4 (&ops)[TILES][kOps][64], int g) {
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j)
+      if (kGroup * g + j < kAll) to[j] = ops[(kGroup * g + j) / kOps][(kGroup * g + j) % kOps][lane];
+  };
+  auto compute = [&](int s) {
+    int by[TILES], key[TILES];
+    bool none = true, whole = true;    // of the step's keys that a row, or every row, sees
 #pragma unroll
     for (int tl = 0; tl < TILES; ++tl) {
-      const int2 m0 = blocks[buf][2 * tl], m1 = blocks[buf][2 * tl + 1];
-      const int k0 = __builtin_amdgcn_readfirstlane(m0.y), k1 = __builtin_amdgcn_readfirstlane(m1.y);
-      auto none = [&](int b) { return b > p1 || (b + 15 <= p0 - window && b >= a.sinks); };
-      if (none(k0) && none(k1)) continue;
-      f32x16 acc = {};
-#pragma unroll
-      for (int d = 0; d < kOps; ++d) {
-        const uint4 k = ops[buf][tl][0][d][lane];
-        acc = mfma_f16_32x32x16(k, q.hi[d], acc);
-        if constexpr (TWO) acc = mfma_f16_32x32x16(k, q.lo[d], acc);
+      const int2 m0 = blocks[s & 1][2 * tl], m1 = blocks[s & 1][2 * tl + 1];
+      const int k0 = uniform(m0.y), k1 = uniform(m1.y);
+      for (const int k : {k0, k1}) {
+        none &= sight.none(p0, p1, k);
+        whole &= sight.whole(p0, p1, k);
       }
-      const int by = h ? m1.x : m0.x, key = h ? k1 : k0;
-      auto whole = [&](int b) { return b + 15 <= p0 && (b > p1 - window || b + 15 < a.sinks); };
-      float x[16];
+      by[tl] = h ? m1.x : m0.x, key[tl] = h ? k1 : k0;
+    }
+    if (none) return;
+    uint4 op[2][kGroup];
+    f32x16 acc[TILES];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = acc[j];
-      uint4 p[2], rest[2];
-      if (whole(k0) && whole(k1)) {
-        st.template weights<false>(x, q.factor, by & 255, by >> 8, [](int) { return false; }, p, rest);
-      } else {
-        st.template weights<true>(x, q.factor, by & 255, by >> 8,
-                                  [&](int j) {
-                                    const int k = key + j;
-                                    return k > pos || (k <= pos - window && k >= a.sinks);
-                                  },
-                                  p, rest);
+    for (int tl = 0; tl < TILES; ++tl) acc[tl] = f32x16{};
+    fetch_ops(op[0], key_ops[s & 1], 0);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      if (g + 1 < kGroups) fetch_ops(op[(g + 1) & 1], key_ops[s & 1], g + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        const int o = kGroup * g + j, tl = o / kOps, d = o % kOps;
+        if (o >= kAll) break;
+        acc[tl] = mfma_f16_32x32x16(op[g & 1][j], q.hi[d], acc[tl]);
+        if constexpr (TWO) acc[tl] = mfma_f16_32x32x16(op[g & 1][j], q.lo[d], acc[tl]);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    fetch_ops(op[0], value_ops[s & 1], 0);
+    typename decltype(st)::Keys w[TILES];
+    if (whole) {
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+      for (int tl = 0; tl < TILES; ++tl)
+        w[tl].template scores<false>(acc[tl], q.factor, by[tl] & 255, by[tl] >> 8, [](int) { return false; });
+    } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint4 v = ops[buf][tl][1][2 * d + u][lane];
-          st.y[d] = mfma_f16_32x32x16(v, p[u], st.y[d]);
-          if constexpr (TWO) st.y[d] = mfma_f16_32x32x16(v, rest[u], st.y[d]);
-        }
+      for (int tl = 0; tl < TILES; ++tl)
+        w[tl].template scores<true>(acc[tl], q.factor, by[tl] & 255, by[tl] >> 8, [&](int j) {
+          return sight.hides(pos, key[tl] + j);
+        });
+    }
+    st.weights(w);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      if (g + 1 < kGroups) fetch_ops(op[(g + 1) & 1], value_ops[s & 1], g + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        const int o = kGroup * g + j, tl = o / kOps, d = o % kOps / 2, u = o % 2;
+        if (o >= kAll) break;
+        st.y[d] = mfma_f16_32x32x16(op[g & 1][j], w[tl].p[u], st.y[d]);
+        if constexpr (TWO) st.y[d] = mfma_f16_32x32x16(op[g & 1][j], w[tl].rest[u], st.y[d]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -158,10 +200,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   for (int s = 0; s < steps; ++s) {
     if (s + 1 < steps) store(s + 1);
     if (s + 2 < steps) load(s + 2);
-    if (active) compute(s & 1);
+    if (active) compute(s);
     lds_barrier();
   }
-
   const Quotient quotient(st.a, st.b, add_xor32(st.l), decltype(st)::kOffset);
   if (c >= rows) return;
   const int64_t out = (row * a.Hq + qh) * D;

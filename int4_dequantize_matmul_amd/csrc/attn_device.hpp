@@ -72,6 +72,26 @@ struct RowTile {
 };
 inline int64_t tile_slots(int64_t T, int64_t N, int64_t G, int ROWS) { return T * G / ROWS + N; }
 
+// Which keys a row sees, in 32 bits (positions are; a larger window or number of
+// sinks is like the largest position).
+struct Sight {
+  int window, sinks;   // window 0 on the outside: all
+  __device__ __forceinline__ Sight(int64_t w, int64_t s)
+      : window(w > 0 && w < INT32_MAX ? static_cast<int>(w) : INT32_MAX),
+        sinks(s < INT32_MAX ? static_cast<int>(s) : INT32_MAX) {}
+  // The row at pos does not see key k; pos - k only wraps where k > pos.
+  __device__ __forceinline__ bool hides(int pos, int k) const {
+    return k > pos || (static_cast<int>(static_cast<uint32_t>(pos) - static_cast<uint32_t>(k)) >= window && k >= sinks);
+  }
+  // No row, or every row, at positions p0 .. p1 sees the 16 keys from k on.
+  __device__ __forceinline__ bool none(int p0, int p1, int k) const {
+    return k > p1 || (max(p0, -1) - (k + 15) >= window && k >= sinks);
+  }
+  __device__ __forceinline__ bool whole(int p0, int p1, int k) const {
+    return k + 15 <= p0 && (p1 - k < window || k + 15 < sinks);
+  }
+};
+
 // The keys that rows at positions p0 .. p1 see together, as blocks of 16 in a
 // row: sinks' blocks, then those from the window's first key to the last row's own.
 struct KeyBlocks {
@@ -177,72 +197,91 @@ struct State {
   static constexpr int kOffset = TWO ? 10 : 9;
   float a = -__builtin_inff(), b = -__builtin_inff(), l = 0.0f;
   V y[N];
-  static constexpr int kWidth = sizeof(V) / sizeof(float);
   __device__ __forceinline__ State() {
 #pragma unroll
-    for (int d = 0; d < N; ++d)
-#pragma unroll
-      for (int j = 0; j < kWidth; ++j) y[d][j] = 0.0f;
+    for (int d = 0; d < N; ++d) y[d] = V{};
   }
-  // The weights of 16 keys' products x with the row, times f, under the scale
-  // bytes kb and vb of their block, as operands; hidden(j): the row does not see key j.
-  template <bool MASK, class F>
-  __device__ __forceinline__ void weights(float (&x)[16], float f, int kb, int vb, F hidden, uint4 (&p)[2], uint4 (&rest)[2]) {
-    f *= kb == 255 ? __builtin_nanf("") : __uint_as_float(kb ? static_cast<uint32_t>(kb) << 23 : 0x400000u);
-    if constexpr (MASK) {
+  // 16 keys of one block: scores x times f, then weights as operands.
+  struct Keys {
+    f32x16 x;
+    float f, e, sum, shift;
+    uint4 p[2], rest[2];
+    // Products x of the row with the keys, factor f; kb and vb: the scale bytes of
+    // the block's keys and values; hidden(j): the row does not see key j.
+    template <bool MASK, class F>
+    __device__ __forceinline__ void scores(f32x16 products, float factor, int kb, int vb, F hidden) {
+      f = factor * __uint_as_float(kb ? static_cast<uint32_t>(kb) << 23 : 0x400000u);
+      if (kb == 255 || vb == 255) f = __builtin_nanf("");
+      e = static_cast<float>(vb - 127);
+      x = products;
+      if constexpr (MASK) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = hidden(j) ? -__builtin_inff() : x[j] * f;
-      f = 1.0f;
-    }
-    const float e = static_cast<float>(vb - 127);
-    float w[16], sum, shift, fa;
-    auto weigh = [&] {
-      // nothing seen so far: any finite number will do
-      fa = a == -__builtin_inff() ? 0.0f : a;
-      // weights of 2^-60 and less of what counts are 0 as halves; kept that large, their f32 sum stays right
-      shift = fmaxf(e + static_cast<float>(kOffset) - (b == -__builtin_inff() ? 0.0f : b), -60.0f - fa);
-      const float add = vb == 255 ? __builtin_nanf("") : shift;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float s = fmaf(x[j], f, add);
-        if constexpr (MASK) s = x[j] == -__builtin_inff() ? x[j] : s;
-        w[j] = exp2_fast(s);
+        for (int j = 0; j < 16; ++j) x[j] = hidden(j) ? -__builtin_inff() : x[j] * f;
+        f = 1.0f;
       }
-      float t[8];   // sums in pairs
+    }
+    // Under the powers a and b.
+    __device__ __forceinline__ void weigh(float a, float b) {
+      // nothing seen so far: any finite number will do
+      const float fa = a == -__builtin_inff() ? 0.0f : a, fb = b == -__builtin_inff() ? 0.0f : b;
+      // weights of 2^-60 and less of what counts are 0 as halves; kept that large, their f32 sum stays right
+      shift = fmaxf(e + static_cast<float>(kOffset) - fb, -60.0f - fa);
+      float w[16];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = w[2 * j] + w[2 * j + 1];
+      for (int j = 0; j < 16; ++j) w[j] = exp2_fast(fmaf(x[j], f, shift));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) t[j] = t[2 * j] + t[2 * j + 1];
-      sum = (t[0] + t[1]) + (t[2] + t[3]);
-    };
-    weigh();
-    if (__any(b == -__builtin_inff() || sum > 32768.0f || shift <= -60.0f - fa)) {
-      float top = x[0];
+      for (int u = 0; u < 2; ++u) {
+        uint32_t q[4], r[4];
 #pragma unroll
-      for (int j = 1; j < 16; ++j) top = fmaxf(top, x[j]);
-      top *= f;
-      const float na = fmaxf(a, ceilf(row_max<S>(top))), nb = fmaxf(b, ceilf(row_max<S>(top + e)));
+        for (int j = 0; j < 4; ++j) {
+          q[j] = pack_f16(w[8 * u + 2 * j], w[8 * u + 2 * j + 1]);
+          r[j] = pack_f16(rest_f16(w[8 * u + 2 * j]), rest_f16(w[8 * u + 2 * j + 1]));
+        }
+        p[u] = make_uint4(q[0], q[1], q[2], q[3]);
+        if constexpr (TWO) rest[u] = make_uint4(r[0], r[1], r[2], r[3]);
+      }
+#pragma unroll
+      for (int n = 8; n > 0; n /= 2)
+#pragma unroll
+        for (int j = 0; j < n; ++j) w[j] = w[j] + w[j + n];
+      sum = w[0];
+    }
+    __device__ __forceinline__ float top() const {
+      float v = x[0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) v = fmaxf(v, x[j]);
+      return v * f;
+    }
+  };
+  // The weights of the T blocks that this lane has; x: their scores.
+  template <int T>
+  __device__ __forceinline__ void weights(Keys (&x)[T]) {
+    bool again = b == -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      x[i].weigh(a, b);
+      // too large for halves, or kept larger than they are; sums are that of T blocks at most
+      again |= x[i].sum > 32768.0f || x[i].shift <= -60.0f - a;
+    }
+    if (__any(again)) {
+      float ta = -__builtin_inff(), tb = ta;
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        const float v = x[i].top();
+        ta = fmaxf(ta, v), tb = fmaxf(tb, v + x[i].e);
+      }
+      const float na = fmaxf(a, ceilf(row_max<S>(ta))), nb = fmaxf(b, ceilf(row_max<S>(tb)));
       const float ga = a == na ? 1.0f : exp2_fast(a - na), gb = b == nb ? 1.0f : exp2_fast(b - nb);   // from -inf: 0
       a = na, b = nb;
       l *= ga;
 #pragma unroll
-      for (int d = 0; d < N; ++d)
+      for (int d = 0; d < N; ++d) y[d] *= gb;
 #pragma unroll
-        for (int j = 0; j < kWidth; ++j) y[d][j] *= gb;
-      weigh();
+      for (int i = 0; i < T; ++i) x[i].weigh(a, b);
     }
-    l = fmaf(sum, exp2_fast(-(shift + fa)), l);
+    const float fa = a == -__builtin_inff() ? 0.0f : a;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint32_t q[4], r[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[j] = pack_f16(w[8 * u + 2 * j], w[8 * u + 2 * j + 1]);
-        r[j] = pack_f16(rest_f16(w[8 * u + 2 * j]), rest_f16(w[8 * u + 2 * j + 1]));
-      }
-      p[u] = make_uint4(q[0], q[1], q[2], q[3]);
-      if constexpr (TWO) rest[u] = make_uint4(r[0], r[1], r[2], r[3]);
-    }
+    for (int i = 0; i < T; ++i) l = fmaf(x[i].sum, exp2_fast(-(x[i].shift + fa)), l);
   }
 };
 
