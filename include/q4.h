@@ -398,7 +398,7 @@ q4_status q8_rmsnorm_rows(const void *x, const void *residual, q4_dtype xt, cons
 /* A paged cache of keys and values in 8 bits (device pointers; the struct
  * itself is the host's, read before a call returns).
  * A page holds `page` tokens (a power of two from 16 to 65536) of each of
- * `heads` key heads, cut into blocks of 16 tokens; a block of a head has one
+ * `heads` key heads (up to 65536), cut into blocks of 16 tokens; a block of a head has one
  * scale byte b for its keys and one for its values, which stand for 2^(b - 127)
  * (255: the whole block is NaN).  D, the numbers of a head, is a multiple of 16
  * up to Q8_KV_MAX_D.
@@ -420,7 +420,8 @@ q4_status q8_rmsnorm_rows(const void *x, const void *residual, q4_dtype xt, cons
  * checked on the host: what they and the table say is kept within the buffers.
  * Tokens on a page that is not in the table or not in the pool read as NaN and
  * are dropped when written.  ESHAPE: the sizes above, heads, n_pages or table
- * < 1, T or sequences beyond 2^31 - 1. */
+ * < 1, T or sequences beyond 2^31 - 1, or more work than 2^32 - 1 workgroups
+ * (writing and reading: two for each of T / 16 + 2 sequences and head). */
 typedef struct {
   int8_t *k, *v;
   uint8_t *k_scale, *v_scale;

@@ -39,27 +39,24 @@ __host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { 
 // and results of splits x rows for combine_kernel, or null with one split.
 template <int NV, bool TWO>   // 16 NV columns
 __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Types types, int splits,
-                                                                                 float *parts, int64_t first) {
+                                                                                 float *parts, uint32_t first) {
   constexpr int NS = (NV + 3) / 4, D = 16 * NV;
   __shared__ float as[kWaves][kRows], bs[kWaves][kRows], ls[kWaves][kRows];
   __shared__ __attribute__((aligned(16))) float meet[kWaves - 1][kRows][D + 4];
-  const int64_t id = first + blockIdx.x;
-  const int split = static_cast<int>(id % splits);
-  const int64_t head = id / splits % a.pool.Hk, slot = id / splits / a.pool.Hk;
-  const int64_t G = a.Hq / a.pool.Hk;
-  const RowTile tile(a.seqs, slot, G, kRows);
-  if (tile.i < 0) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, q4 = lane >> 4;
-  const int i = uniform(tile.i);
-  const int64_t r0 = uniform(tile.r0), n = uniform(tile.rows), at_row = uniform(tile.s.row), at_pos = uniform(tile.s.first);
-  const int rows = n - r0 < kRows ? static_cast<int>(n - r0) : kRows;
-  const int64_t r = r0 + (c < rows ? c : rows - 1), t = r / G;
-  const int64_t row = at_row + t, qh = head * G + (r - t * G);
+  const uint32_t Hk = static_cast<uint32_t>(a.pool.Hk), G = static_cast<uint32_t>(a.G);
+  const int split = static_cast<int>(blockIdx.x % splits);
+  const int head = static_cast<int>(blockIdx.x / splits % Hk);
+  const RowTile<kRows> tile(a.seqs, first + blockIdx.x / splits / Hk, G);
+  if (tile.s.i < 0) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15, q4 = lane >> 4;
+  const int rows = min(tile.rows - tile.r0, kRows);
+  const int r = tile.r0 + (c < rows ? c : rows - 1), t = static_cast<int>(static_cast<uint32_t>(r) / G);
+  const int64_t row = tile.s.row + t, qh = head * static_cast<int>(G) + (r - t * static_cast<int>(G));
   // lengths are int32, and so positions
-  const int p0 = static_cast<int>(at_pos + r0 / G), p1 = static_cast<int>(at_pos + (r0 + rows - 1) / G);
-  const int pos = static_cast<int>(at_pos + t);
-  const KeyBlocks keys(p0, p1, a.window, a.sinks);
+  const int p0 = uniform(tile.s.first + tile.r0 / static_cast<int>(G));
+  const int p1 = uniform(tile.s.first + (tile.r0 + rows - 1) / static_cast<int>(G)), pos = tile.s.first + t;
   const Sight sight(a.window, a.sinks);
+  const KeyBlocks keys(p0, p1, sight);
 
   const int steps = (keys.count + 3) / 4;
   const int w0 = static_cast<int>(static_cast<int64_t>(steps) * (split * kWaves + wave) / (splits * kWaves));
@@ -69,17 +66,18 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
   struct Info {
     int at, bytes, blk;
   };
+  const int32_t *pages = a.pool.pages + tile.s.i * a.pool.width;
+  const int page_mask = (1 << a.pool.page_blocks_log2) - 1;
   auto page_of = [&](int round) {
     const int v = 4 * w0 + 64 * round + lane;
     const int64_t p = v < keys.count ? keys.block(v) >> a.pool.page_blocks_log2 : a.pool.width;
-    return p < a.pool.width ? a.pool.pages[i * a.pool.width + p] : -1;
+    return p < a.pool.width ? pages[p] : -1;
   };
   auto info_of = [&](int round, int page) {
     const int v = 4 * w0 + 64 * round + lane;
     Info f = {0, 0xFFFF, keys.block(v)};     // a page that is not there: NaN
     if (v < keys.count && page >= 0 && page < a.pool.n_pages) {
-      const int mask = (1 << a.pool.page_blocks_log2) - 1;
-      f.at = static_cast<int>(((page * a.pool.Hk + head) << a.pool.page_blocks_log2) + (f.blk & mask));
+      f.at = ((page * static_cast<int>(Hk) + head) << a.pool.page_blocks_log2) + (f.blk & page_mask);
       f.bytes = a.pool.ks[f.at] | a.pool.vs[f.at] << 8;
     }
     return f;
@@ -242,11 +240,13 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types typ
 
 template <int NV, bool TWO>
 void go_rows(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hipStream_t st) {
-  const int64_t G = a.Hq / a.pool.Hk, all = tile_slots(a.seqs.T, a.seqs.N, G, kRows) * a.pool.Hk * p.splits;
+  const int64_t slots = tile_slots(a.seqs.T, a.seqs.N, a.G, kRows), each = a.pool.Hk * p.splits;
   const int64_t most = max_groups(kThreads);
-  for (int64_t first = 0; first < all; first += most)
-    attention_rows_kernel<NV, TWO><<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, 0, st>>>(
-        a, t, p.splits, p.splits > 1 ? ws : nullptr, first);
+  for (int64_t first = 0; first < slots; first += most / each) {   // slots of a launch
+    const int64_t n = slots - first < most / each ? slots - first : most / each;
+    attention_rows_kernel<NV, TWO><<<static_cast<unsigned>(n * each), kThreads, 0, st>>>(
+        a, t, p.splits, p.splits > 1 ? ws : nullptr, static_cast<uint32_t>(first));
+  }
   if (p.splits == 1) return;
   const int64_t rows = a.seqs.T * a.Hq;
   for (int64_t first = 0; first < rows; first += most)

@@ -5,10 +5,12 @@
 // side by side.  Keys and values of a step (64 keys, 32 past 128 columns) become
 // halves once, on their way to LDS, where they lie as the matrix instructions'
 // operands, 16 bytes a lane, 1 KB an instruction, so that neither writes nor
-// reads conflict.  Operands come to registers four at a time, those of the next
-// four instructions before these four.  Two buffers of LDS; a step's codes are
-// loaded while the step before the last is multiplied; one barrier a step, which
-// waits for LDS alone.
+// reads conflict.  An operand is on its way to registers seven instructions before
+// the one that takes it.  One barrier a step, which waits for LDS alone; the second
+// wave of a SIMD has it in the middle of its step, so that one wave has the
+// exponentials of its scores while the other has the matrix instructions.  Two
+// buffers each of keys and values, values a step behind; codes are loaded a step
+// before they become halves, 1 KB of one block an instruction.
 #include "attn_device.hpp"
 
 namespace q4 {
@@ -16,85 +18,86 @@ namespace {
 
 // WAVES waves, TILES times 32 keys a step.
 template <int ND, bool TWO, int WAVES, int TILES>
-__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(AttnArgs a, Types types, int64_t slots,
-                                                                                int64_t first) {
-  constexpr int kRows = 32 * WAVES, kOps = 2 * ND;             // operands of 1 KB of one product and 32 keys
-  constexpr int kLoads = (TILES * 2 * ND + WAVES - 1) / WAVES; // 16-byte loads of a lane a step
-  constexpr int kSteps = 32 / TILES;                           // steps whose blocks the 64 lanes hold
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(AttnArgs a, Types types, uint32_t last_slot) {
+  constexpr int kRows = 32 * WAVES, kOps = 2 * ND, kAll = TILES * kOps;   // operands of 1 KB of a product
+  constexpr int kBlocks = 2 * TILES, kSteps = 64 / kBlocks;               // blocks a step; steps whose blocks 64 lanes hold
+  constexpr int kUnits = kBlocks * ((ND + 1) / 2), kLoads = (kUnits + WAVES - 1) / WAVES;   // loads of a step, of a wave
   __shared__ uint4 key_ops[2][TILES][kOps][64], value_ops[2][TILES][kOps][64];
-  __shared__ int2 blocks[2][2 * TILES];                        // scale bytes and first key of a step's blocks
-  const int64_t id = first + blockIdx.x;
+  __shared__ int2 blocks[2][kBlocks];                                     // scale bytes and first key of a step's blocks
   // heads next to each other go to different XCDs, each with its keys in an L2 of its own; long rows first
-  const int64_t head = id % a.pool.Hk, slot = slots - 1 - id / a.pool.Hk;
-  const int64_t G = a.Hq / a.pool.Hk;
-  const RowTile tile(a.seqs, slot, G, kRows);
-  if (tile.i < 0) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
-  const int D = static_cast<int>(a.pool.D), i = uniform(tile.i);
-  const int64_t r0 = uniform(tile.r0), n = uniform(tile.rows), at_row = uniform(tile.s.row), at_pos = uniform(tile.s.first);
-  const int64_t last = r0 + kRows < n ? r0 + kRows - 1 : n - 1;
-  const KeyBlocks keys(at_pos + r0 / G, at_pos + last / G, a.window, a.sinks);
-  // this wave's rows
-  const int64_t wr = r0 + 32 * wave;
-  const bool active = wr <= last;
-  const int rows = !active ? 0 : last - wr < 31 ? static_cast<int>(last - wr) + 1 : 32;
-  const int64_t r = wr + (c < rows ? c : rows - 1), t = r / G;
-  const int64_t row = at_row + t, qh = head * G + (r - t * G);
-  // lengths are int32, and so positions
-  const int pos = static_cast<int>(at_pos + t);
-  const int p0 = static_cast<int>(at_pos + wr / G), p1 = static_cast<int>(at_pos + (active ? wr + rows - 1 : wr) / G);
+  const uint32_t Hk = static_cast<uint32_t>(a.pool.Hk), slot = last_slot - blockIdx.x / Hk;
+  const int head = static_cast<int>(blockIdx.x % Hk);
+  const uint32_t G = static_cast<uint32_t>(a.G);
+  const RowTile<kRows> tile(a.seqs, slot, G);
+  if (tile.s.i < 0) return;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 31, h = lane >> 5;
+  const int D = static_cast<int>(a.pool.D);
+  const int last = (tile.rows - tile.r0 > kRows ? tile.r0 + kRows : tile.rows) - 1;
   const Sight sight(a.window, a.sinks);
+  const KeyBlocks keys(tile.s.first + tile.r0 / static_cast<int>(G), tile.s.first + last / static_cast<int>(G), sight);
+  const int steps = (keys.count + kBlocks - 1) / kBlocks;
 
-  Query<ND, 2, TWO> q;
-  q.load(a, types, active ? row * a.q_t + qh * a.q_h : 0, active, h);
-  State<f32x16, ND, 2, TWO> st;
-
-  // blocks of 64 keys' worth a lane, two rounds ahead: pages, then scales
+  // blocks of a round of kSteps steps, one a lane, two rounds ahead: pages, then scales
+  const int32_t *pages = a.pool.pages + tile.s.i * a.pool.width;
+  const int page_mask = (1 << a.pool.page_blocks_log2) - 1;
   struct Info {
     int at, bytes, blk;
   };
   auto page_of = [&](int round) {
     const int v = 64 * round + lane;
     const int64_t p = v < keys.count ? keys.block(v) >> a.pool.page_blocks_log2 : a.pool.width;
-    return p < a.pool.width ? a.pool.pages[i * a.pool.width + p] : -1;
+    return p < a.pool.width ? pages[p] : -1;
   };
   auto info_of = [&](int round, int page) {
     const int v = 64 * round + lane;
     Info f = {0, 0xFFFF, keys.block(v)};     // a page that is not there: NaN
     if (v < keys.count && page >= 0 && page < a.pool.n_pages) {
-      const int mask = (1 << a.pool.page_blocks_log2) - 1;
-      f.at = static_cast<int>(((page * a.pool.Hk + head) << a.pool.page_blocks_log2) + (f.blk & mask));
+      f.at = ((page * static_cast<int>(Hk) + head) << a.pool.page_blocks_log2) + (f.blk & page_mask);
       f.bytes = a.pool.ks[f.at] | a.pool.vs[f.at] << 8;
     }
     return f;
   };
-  Info cur = info_of(0, page_of(0)), next = info_of(1, page_of(1));
+  const int page0 = page_of(0), page1 = page_of(1);
   int page = page_of(2);
 
-  // This wave's loads of a step: load u is of keys or values, of 32 columns of one
-  // tile, which of two blocks by lane.  Columns past D, which the query has as 0 or
-  // no result asks for, are the last ones again.
-  uint4 raw[kLoads];
-  int from[kLoads], to[kLoads];        // bytes from the block on; 16 bytes of LDS
-  bool second[kLoads];
-  const int8_t *base[kLoads];
-  const int unit = kKvBlock * D;
+  // this wave's rows; lengths are int32, and so positions
+  const int wr = tile.r0 + 32 * wave;
+  const bool active = wr <= last;
+  const int rows = !active ? 0 : min(last - wr + 1, 32);
+  const int r = wr + (c < rows ? c : max(rows - 1, 0)), t = static_cast<int>(static_cast<uint32_t>(r) / G);
+  const int64_t row = tile.s.row + t, qh = head * static_cast<int>(G) + (r - t * static_cast<int>(G));
+  const int pos = tile.s.first + t;
+  const int p0 = uniform(tile.s.first + wr / static_cast<int>(G));
+  const int p1 = uniform(tile.s.first + (active ? wr + rows - 1 : wr) / static_cast<int>(G));
+  Query<ND, 2, TWO> q;
+  q.load(a, types, active ? row * a.q_t + qh * a.q_h : 0, active, h);
+  Info cur = info_of(0, page0), next = info_of(1, page1);
+
+  // This wave's loads of a step: load u is 64 columns of one block.  Lane l has 16
+  // columns of token l mod 16 of the keys, column l of the values.  Columns past D,
+  // which the query has as 0 or no result asks for, are the last ones again.
+  uint4 raw_k[kLoads], raw_v[kLoads];
+  int from_k[kLoads], from_v[kLoads], to_k[kLoads], to_v[kLoads];   // bytes in the block; 16 bytes of LDS
+  int of[kLoads];                                                   // the blocks of the values to load next
+  const int64_t unit = kKvBlock * D;
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
-    const int x = wave + WAVES * u, tl = x / (2 * ND), d = x / 2 % ND;
-    to[u] = (tl * kOps + 2 * d) * 64 + lane;
-    if (x & 1) {
-      base[u] = a.pool.v;
-      from[u] = min(32 * d + c, D - 1) * 16;
-      second[u] = h;
-    } else {
-      // row c of the first product is key 16 (c / 4 mod 2) + 4 (c / 8) + c mod 4
-      base[u] = a.pool.k;
-      from[u] = min(2 * d + h, D / 16 - 1) * 256 + (4 * (c >> 3) + (c & 3)) * 16;
-      second[u] = c & 4;
-    }
+    const int x = wave + WAVES * u, b = x % kBlocks, g = x / kBlocks, tl = b / 2, half = b % 2;
+    // token 4 i + j of block h is row 8 i + 4 h + j of the first product
+    const int token = lane & 15, chunk = 4 * g + (lane >> 4), col = 64 * g + lane;
+    from_k[u] = min(chunk, D / 16 - 1) * 256 + token * 16;
+    from_v[u] = min(col, D - 1) * 16;
+    to_k[u] = (tl * kOps + chunk / 2 * 2) * 64 + 8 * (token >> 2) + 4 * half + (token & 3) + 32 * (chunk & 1);
+    to_v[u] = (tl * kOps + col / 32 * 2) * 64 + (col & 31) + 32 * half;
+    if (ND % 2 && chunk >= kOps) to_k[u] = -1;   // past the last 32 columns
+    if (ND % 2 && col >= 32 * ND) to_v[u] = -1;
   }
-  auto load = [&](int s) {
+  auto load_values = [&] {   // of the step whose keys were loaded last
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      if (wave + WAVES * u < kUnits) raw_v[u] = load16(a.pool.v + of[u] * unit + from_v[u]);
+  };
+  auto load_keys = [&](int s) {
     const int l = s % kSteps;
     if (l == 0 && s > 0) {
       cur = next;
@@ -103,67 +106,85 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
     }
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      const int x = wave + WAVES * u, tl = x / (2 * ND);
-      if (x >= TILES * 2 * ND) continue;
-      const int b0 = __builtin_amdgcn_readlane(cur.at, 2 * TILES * l + 2 * tl);
-      const int b1 = __builtin_amdgcn_readlane(cur.at, 2 * TILES * l + 2 * tl + 1);
-      raw[u] = load16(base[u] + (static_cast<int64_t>(second[u] ? b1 : b0) * unit + from[u]));
+      if (wave + WAVES * u >= kUnits) continue;
+      of[u] = __builtin_amdgcn_readlane(cur.at, kBlocks * l + (wave + WAVES * u) % kBlocks);
+      raw_k[u] = load16(a.pool.k + of[u] * unit + from_k[u]);
     }
   };
-  // the codes that load(s) brought; called before load(s + 1)
-  auto store = [&](int s) {
+  auto store = [&](uint4 *ops, const int (&to)[kLoads], const uint4 (&raw)[kLoads]) {
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      const int x = wave + WAVES * u;
-      if (x >= TILES * 2 * ND) continue;
-      uint4 *p = (x & 1 ? &value_ops[s & 1][0][0][0] : &key_ops[s & 1][0][0][0]) + to[u];
-      p[0] = codes_to_f16(raw[u].x, raw[u].y);
-      p[64] = codes_to_f16(raw[u].z, raw[u].w);
+      if (wave + WAVES * u >= kUnits || to[u] < 0) continue;
+      ops[to[u]] = codes_to_f16(raw[u].x, raw[u].y);
+      ops[to[u] + 64] = codes_to_f16(raw[u].z, raw[u].w);
     }
-    if (wave == 0 && lane / (2 * TILES) == s % kSteps)
-      blocks[s & 1][lane % (2 * TILES)] = make_int2(cur.bytes, cur.blk * kKvBlock);
   };
-  constexpr int kAll = TILES * kOps, kGroup = 4, kGroups = (kAll + kGroup - 1) / kGroup;
-  auto fetch_ops = [&](uint4 (&to)[kGroup], const uint4 (&ops)[TILES][kOps][64], int g) {
+  // the keys that load_keys(s) brought; called before load_keys(s + 1)
+  auto store_keys = [&](int s) {
+    store(&key_ops[s & 1][0][0][0], to_k, raw_k);
+    if (wave == 0 && lane / kBlocks == s % kSteps)
+      blocks[s & 1][lane % kBlocks] = make_int2(cur.bytes, cur.blk * kKvBlock);
+  };
+  // In step s, when no wave reads them any more: the keys of s + 1 and the values of s.
+  auto stage = [&](int s) {
+    if (s + 1 < steps) store_keys(s + 1);
+    if (s < steps) store(&value_ops[s & 1][0][0][0], to_v, raw_v);
+    if (s + 1 < steps) load_values();
+    if (s + 2 < steps) load_keys(s + 2);
+  };
+
+  // This wave's rows all see all of the keys of steps [inner, outer), of blocks from
+  // the last row's window's first whole one to the first row's last, and nothing
+  // from `end` on; in the other steps, sinks among them, each score is looked at.
+  int inner = 0, outer = 0, end = -1;
+  if (active) {
+    if (p1 >= sight.window) inner = (static_cast<int>((static_cast<uint32_t>(p1 - sight.window) + 16) / kKvBlock) - keys.skip + kBlocks - 1) / kBlocks;
+    if (p0 >= 0) outer = (static_cast<int>((static_cast<uint32_t>(p0) + 1) / kKvBlock) - keys.skip) / kBlocks;
+    end = p1 < 0 ? 0 : (p1 / kKvBlock + 1 - keys.skip + kBlocks - 1) / kBlocks;
+  }
+
+  State<f32x16, ND, 2, TWO> st;
+  constexpr int kRing = 8;
+  uint4 ring[kRing];
+  f32x16 acc[TILES];
+  typename decltype(st)::Keys w[TILES];
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j)
-      if (kGroup * g + j < kAll) to[j] = ops[(kGroup * g + j) / kOps][(kGroup * g + j) % kOps][lane];
-  };
-  auto compute = [&](int s) {
-    int by[TILES], key[TILES];
-    bool none = true, whole = true;    // of the step's keys that a row, or every row, sees
+  for (int tl = 0; tl < TILES; ++tl)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) w[tl].p[u] = w[tl].rest[u] = make_uint4(0, 0, 0, 0);
+  int by[TILES], key[TILES];
+  // The products of step s - 1 with its values, of step s with its keys.  The first
+  // step has weights and values of 0 in front of it, and behind the last one scores
+  // that nobody reads: one form of this loop, whose results stay where they are.
+  auto multiply = [&](int s) {
+    const uint4 *vo = &value_ops[(s - 1) & 1][0][0][lane], *ko = &key_ops[s & 1][0][0][lane];
 #pragma unroll
     for (int tl = 0; tl < TILES; ++tl) {
-      const int2 m0 = blocks[s & 1][2 * tl], m1 = blocks[s & 1][2 * tl + 1];
-      const int k0 = uniform(m0.y), k1 = uniform(m1.y);
-      for (const int k : {k0, k1}) {
-        none &= sight.none(p0, p1, k);
-        whole &= sight.whole(p0, p1, k);
-      }
-      by[tl] = h ? m1.x : m0.x, key[tl] = h ? k1 : k0;
+      const int2 m = blocks[s & 1][2 * tl + h];
+      by[tl] = m.x, key[tl] = m.y;
+      acc[tl] = f32x16{};
     }
-    if (none) return;
-    uint4 op[2][kGroup];
-    f32x16 acc[TILES];
+    auto operand = [&](int o) { return o < kAll ? vo[64 * o] : ko[64 * (o - kAll)]; };
 #pragma unroll
-    for (int tl = 0; tl < TILES; ++tl) acc[tl] = f32x16{};
-    fetch_ops(op[0], key_ops[s & 1], 0);
+    for (int o = 0; o < kRing - 1 && o < 2 * kAll; ++o) ring[o] = operand(o);
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (g + 1 < kGroups) fetch_ops(op[(g + 1) & 1], key_ops[s & 1], g + 1);
+    for (int o = 0; o < 2 * kAll; ++o) {
+      if (o + kRing - 1 < 2 * kAll) ring[(o + kRing - 1) % kRing] = operand(o + kRing - 1);
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        const int o = kGroup * g + j, tl = o / kOps, d = o % kOps;
-        if (o >= kAll) break;
-        acc[tl] = mfma_f16_32x32x16(op[g & 1][j], q.hi[d], acc[tl]);
-        if constexpr (TWO) acc[tl] = mfma_f16_32x32x16(op[g & 1][j], q.lo[d], acc[tl]);
+      const uint4 x = ring[o % kRing];
+      const int tl = o % kAll / kOps, d = o % kOps;
+      if (o < kAll) {
+        st.y[d / 2] = mfma_f16_32x32x16(x, w[tl].p[d % 2], st.y[d / 2]);
+        if constexpr (TWO) st.y[d / 2] = mfma_f16_32x32x16(x, w[tl].rest[d % 2], st.y[d / 2]);
+      } else {
+        acc[tl] = mfma_f16_32x32x16(x, q.hi[d], acc[tl]);
+        if constexpr (TWO) acc[tl] = mfma_f16_32x32x16(x, q.lo[d], acc[tl]);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-    fetch_ops(op[0], value_ops[s & 1], 0);
-    typename decltype(st)::Keys w[TILES];
-    if (whole) {
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto weigh = [&](int s) {
+    if (s >= inner && s < outer) {
 #pragma unroll
       for (int tl = 0; tl < TILES; ++tl)
         w[tl].template scores<false>(acc[tl], q.factor, by[tl] & 255, by[tl] >> 8, [](int) { return false; });
@@ -175,34 +196,26 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
         });
     }
     st.weights(w);
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (g + 1 < kGroups) fetch_ops(op[(g + 1) & 1], value_ops[s & 1], g + 1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        const int o = kGroup * g + j, tl = o / kOps, d = o % kOps / 2, u = o % 2;
-        if (o >= kAll) break;
-        st.y[d] = mfma_f16_32x32x16(op[g & 1][j], w[tl].p[u], st.y[d]);
-        if constexpr (TWO) st.y[d] = mfma_f16_32x32x16(op[g & 1][j], w[tl].rest[u], st.y[d]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
   };
 
-  const int steps = (keys.count + 2 * TILES - 1) / (2 * TILES);
   if (steps > 0) {
-    load(0);
-    store(0);
-    if (steps > 1) load(1);
-    lds_barrier();
+    load_keys(0);
+    load_values();
+    store_keys(0);
+    if (steps > 1) load_keys(1);
   }
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) store(s + 1);
-    if (s + 2 < steps) load(s + 2);
-    if (active) compute(s);
-    lds_barrier();
+  for (int x = threadIdx.x; x < kAll * 64; x += 64 * WAVES) (&value_ops[1][0][0][0])[x] = make_uint4(0, 0, 0, 0);
+  lds_barrier();
+  // Between two barriers, step s: K(s) and V(s - 1) are read, K(s + 1) and V(s) written.
+  const bool second = WAVES == 8 && wave >= 4;
+  for (int s = 0; s <= steps; ++s) {
+    if (s <= end) multiply(s);
+    stage(s);
+    if (second) lds_barrier();
+    if (s < end) weigh(s);
+    if (!second) lds_barrier();
   }
+
   const Quotient quotient(st.a, st.b, add_xor32(st.l), decltype(st)::kOffset);
   if (c >= rows) return;
   const int64_t out = (row * a.Hq + qh) * D;
@@ -221,11 +234,11 @@ template <int ND, bool TWO>
 void go(const AttnArgs &a, const Types &t, hipStream_t st) {
   // 64 keys of more than 128 columns would be more than 64 KB in two buffers, and eight waves' registers too few
   constexpr int WAVES = ND <= 4 ? 8 : 4, TILES = ND <= 4 ? 2 : 1;
-  const int64_t slots = tile_slots(a.seqs.T, a.seqs.N, a.Hq / a.pool.Hk, 32 * WAVES), all = slots * a.pool.Hk;
-  const int64_t most = max_groups(64 * WAVES);
-  for (int64_t first = 0; first < all; first += most)
+  const int64_t slots = tile_slots(a.seqs.T, a.seqs.N, a.G, 32 * WAVES), most = max_groups(64 * WAVES) / a.pool.Hk;
+  for (int64_t left = slots; left > 0; left -= most)   // slots of a launch
     attention_tiled_kernel<ND, TWO, WAVES, TILES>
-        <<<static_cast<unsigned>(all - first < most ? all - first : most), 64 * WAVES, 0, st>>>(a, t, slots, first);
+        <<<static_cast<unsigned>((left < most ? left : most) * a.pool.Hk), 64 * WAVES, 0, st>>>(
+            a, t, static_cast<uint32_t>(left - 1));
 }
 
 template <bool TWO>

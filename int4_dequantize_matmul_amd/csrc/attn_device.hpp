@@ -43,31 +43,24 @@ __device__ __forceinline__ float rest_f16(float v) { return v - static_cast<floa
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// What all lanes have the same of, in a scalar register.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v)), hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
-  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
-}
-
 // Rows of a tile: row r of a sequence and key head is query head g = r mod G of
 // that key head's G, of the sequence's row r / G, so that all rows of a tile
 // share their keys.
+template <int ROWS>
 struct RowTile {
-  int i;                  // sequence, or -1: nothing to do
-  int64_t r0, rows;       // first row, rows of the sequence in all
-  Sequence s;
-  // ROWS a tile; sequence i has the slots from floor(starts[i] G / ROWS) + i on
-  __device__ __forceinline__ RowTile(const KvSeqs &q, int64_t slot, int64_t G, int ROWS)
-      : i(search_last<64>(static_cast<int>(q.N), slot, [&](int j) { return start(q, j, G, ROWS); })),
-        s(q, i < 0 ? 0 : i) {
-    if (i < 0) return;
-    r0 = (slot - start(q, i, G, ROWS)) * ROWS;
-    rows = s.n * G;
-    if (r0 >= rows) i = -1;
-  }
-  static __device__ __forceinline__ int64_t start(const KvSeqs &q, int j, int64_t G, int ROWS) {
-    return Sequence::clamp(q.starts[j], q.T) * G / ROWS + j;
+  Sequence s;             // i = -1: nothing to do
+  int r0, rows;           // first row, rows of the sequence in all
+  // sequence i has the slots from floor(starts[i] G / ROWS) + i on
+  __device__ __forceinline__ RowTile(const KvSeqs &q, uint32_t slot, uint32_t G) {
+    const auto f = [&](uint32_t start, int j) { return start * G / ROWS + static_cast<uint32_t>(j); };
+    s = find_sequence<64>(q, slot, f);
+    if (s.i < 0) return;
+    const uint32_t at = (slot - f(static_cast<uint32_t>(s.row), s.i)) * static_cast<uint64_t>(ROWS) > INT32_MAX
+                            ? INT32_MAX
+                            : (slot - f(static_cast<uint32_t>(s.row), s.i)) * ROWS;
+    r0 = static_cast<int>(at);
+    rows = s.n * static_cast<int>(G);
+    if (r0 >= rows) s.i = -1;
   }
 };
 inline int64_t tile_slots(int64_t T, int64_t N, int64_t G, int ROWS) { return T * G / ROWS + N; }
@@ -83,10 +76,7 @@ struct Sight {
   __device__ __forceinline__ bool hides(int pos, int k) const {
     return k > pos || (static_cast<int>(static_cast<uint32_t>(pos) - static_cast<uint32_t>(k)) >= window && k >= sinks);
   }
-  // No row, or every row, at positions p0 .. p1 sees the 16 keys from k on.
-  __device__ __forceinline__ bool none(int p0, int p1, int k) const {
-    return k > p1 || (max(p0, -1) - (k + 15) >= window && k >= sinks);
-  }
+  // Every row at positions p0 .. p1 sees the 16 keys from k on.
   __device__ __forceinline__ bool whole(int p0, int p1, int k) const {
     return k + 15 <= p0 && (p1 - k < window || k + 15 < sinks);
   }
@@ -96,12 +86,10 @@ struct Sight {
 // row: sinks' blocks, then those from the window's first key to the last row's own.
 struct KeyBlocks {
   int sink_blocks, skip, count;   // block v is v, or v + skip from sink_blocks on
-  __device__ __forceinline__ KeyBlocks(int64_t p0, int64_t p1, int64_t window, int64_t sinks) {
-    const int end = p1 < 0 ? 0 : static_cast<int>(p1 / kKvBlock) + 1;
-    const int64_t w0 = window > 0 && p0 - window + 1 > 0 ? p0 - window + 1 : 0;
-    const int first = static_cast<int>(w0 / kKvBlock);
-    const int64_t sb = (sinks + kKvBlock - 1) / kKvBlock;
-    sink_blocks = sb < first ? static_cast<int>(sb) : first;
+  __device__ __forceinline__ KeyBlocks(int p0, int p1, const Sight &s) {
+    const int end = p1 < 0 ? 0 : p1 / kKvBlock + 1;
+    const int first = p0 >= s.window ? (p0 - s.window + 1) / kKvBlock : 0;
+    sink_blocks = min((s.sinks >> 4) + ((s.sinks & 15) != 0), first);
     skip = first - sink_blocks;
     count = end - skip;
   }
@@ -149,11 +137,11 @@ struct Query {
     }
     if constexpr (S == 4) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
     top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-    // exponent of the largest: top in [2^e, 2^(e + 1)); a NaN or an infinity makes the whole row NaN
-    const bool bad = top >= 0x7F800000u;
-    const int e = bad || top == 0 ? 0 : ilogbf(__uint_as_float(top));
-    factor = bad ? __builtin_nanf("") : ldexpf(fabsf(a.scale) * kLog2e, e - 14);
-    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+    // exponent of the largest: top in [2^e, 2^(e + 1)), but for rows below 2^-100, which are scaled as if they reached
+    // it; a NaN or an infinity makes the whole row NaN
+    const int e = max(static_cast<int>(top >> 23) - 127, -100);
+    factor = top >= 0x7F800000u ? __builtin_nanf("") : ldexpf(fabsf(a.scale) * kLog2e, e - 14);
+    const float to = __uint_as_float(static_cast<uint32_t>(14 - min(e, 127) + 127) << 23) * (a.scale < 0.0f ? -1.0f : 1.0f);
 #pragma unroll
     for (int s = 0; s < N; ++s)
 #pragma unroll
@@ -161,8 +149,7 @@ struct Query {
         uint32_t w[4], v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float p = bad ? 0.0f : sign * ldexpf(x[s][8 * u + 2 * j], 14 - e);
-          const float q = bad ? 0.0f : sign * ldexpf(x[s][8 * u + 2 * j + 1], 14 - e);
+          const float p = x[s][8 * u + 2 * j] * to, q = x[s][8 * u + 2 * j + 1] * to;
           w[j] = pack_f16(p, q);
           v[j] = pack_f16(rest_f16(p), rest_f16(q));
         }

@@ -217,7 +217,7 @@ struct AttnArgs {
   const void *q;
   int64_t q_t, q_h;
   void *y;
-  int64_t Hq;
+  int64_t Hq, G;                // query heads, and of a key head
   float scale;
   int64_t window, sinks;        // window 0: none
 };

@@ -158,25 +158,20 @@ __device__ __forceinline__ uint32_t coarser(uint32_t w, int shift) {
 
 // Workgroups of a launch: slots x heads x {keys, values}, then 16 query rows each.
 template <bool BF16, bool OB>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, int64_t blocks, int64_t first) {
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, uint32_t blocks, uint32_t first) {
   extern __shared__ double lds[];
   __shared__ double tops[kThreads / 64];
-  const int64_t id = first + blockIdx.x;
+  const uint32_t id = first + blockIdx.x;
   const int lane = threadIdx.x & 15, slot16 = threadIdx.x >> 4;
   const int D = static_cast<int>(a.pool.D);
 
   if (id >= blocks) {   // queries
-    const int64_t r = (id - blocks) * 16 + slot16, t = r / a.Hq, h = r - t * a.Hq;
+    const uint32_t r = (id - blocks) * 16 + slot16, Hq = static_cast<uint32_t>(a.Hq);
+    const int64_t t = r / Hq, h = r % Hq;
     const bool in = t < a.seqs.T;
-    const int i = search_last<16>(static_cast<int>(a.seqs.N), in ? t : 0,
-                                  [&](int j) { return Sequence::clamp(a.seqs.starts[j], a.seqs.T); });
-    int64_t pos = -1;
-    bool live = false;
-    if (in && i >= 0) {
-      const Sequence s(a.seqs, i);
-      live = t - s.row < s.n;            // not behind the last sequence
-      pos = s.first + (t - s.row);
-    }
+    const Sequence s = find_sequence<16>(a.seqs, in ? static_cast<uint32_t>(t) : 0, [&](uint32_t start, int) { return start; });
+    const bool live = in && s.i >= 0 && t - s.row < s.n;   // not behind the last sequence
+    const int64_t pos = live ? s.first + (t - s.row) : -1;
     float y[2][8];
     head_row<float, BF16>(a, a.q, t * a.q_t + h * a.q_h, a.gq, pos, live, y, reinterpret_cast<float *>(lds) + slot16 * D);
     if (!live) return;
@@ -189,20 +184,18 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, int64
   }
 
   const bool values = id & 1;
-  const int64_t slot = (id >> 1) / a.pool.Hk, h = (id >> 1) - slot * a.pool.Hk;
-  const BlockOf w(a.seqs, slot);
-  if (w.i < 0) return;
-  const Sequence s(a.seqs, w.i);
-  const int64_t at = block_at(a.pool, w.i, w.b, h);
+  const uint32_t Hk = static_cast<uint32_t>(a.pool.Hk), h = (id >> 1) % Hk;
+  const BlockOf w(a.seqs, (id >> 1) / Hk);
+  const Sequence &s = w.s;
+  if (s.i < 0) return;
+  const int64_t at = block_at(a.pool, s.i, w.b, h);
   if (at < 0) return;                    // no such page: the tokens are dropped
-  const int64_t begin = w.b * kKvBlock, lo = s.first > 0 ? s.first : 0;
-  const int had = lo > begin ? static_cast<int>(lo - begin) : 0;
-  const int have = s.len - begin < kKvBlock ? static_cast<int>(s.len - begin) : kKvBlock;
+  const int begin = w.b * kKvBlock, had = max(max(s.first, 0) - begin, 0), have = min(s.len - begin, kKvBlock);
   int8_t *codes = (values ? a.pool.v : a.pool.k) + at * kKvBlock * D;
   uint8_t *scale = (values ? a.pool.vs : a.pool.ks) + at;
 
   const bool live = slot16 >= had && slot16 < have;
-  const int64_t row = s.row + begin + slot16 - s.first;
+  const int64_t row = static_cast<int64_t>(s.row) + begin + slot16 - s.first;
   double y[2][8];
   if (values) {
 #pragma unroll
@@ -297,21 +290,21 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, int64
 
 // A block of one head, keys or values, as bf16 or f32 rows.
 template <bool OB>
-__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvPool pool, KvSeqs seqs, void *ko, void *vo, int64_t first) {
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvPool pool, KvSeqs seqs, void *ko, void *vo, uint32_t first) {
   __shared__ uint8_t turn[256 * 16];
-  const int64_t id = first + blockIdx.x;
+  const uint32_t id = first + blockIdx.x;
   const bool values = id & 1;
-  const int64_t slot = (id >> 1) / pool.Hk, h = (id >> 1) - slot * pool.Hk;
-  const BlockOf w(seqs, slot);
-  if (w.i < 0) return;
-  const Sequence s(seqs, w.i);
+  const uint32_t Hk = static_cast<uint32_t>(pool.Hk), h = (id >> 1) % Hk;
+  const BlockOf w(seqs, (id >> 1) / Hk);
+  const Sequence &s = w.s;
+  if (s.i < 0) return;
   const int lane = threadIdx.x & 15, slot16 = threadIdx.x >> 4, D = static_cast<int>(pool.D);
-  const int64_t at = block_at(pool, w.i, w.b, h), pos = w.b * kKvBlock + slot16;
+  const int64_t at = block_at(pool, s.i, w.b, h), pos = static_cast<int64_t>(w.b) * kKvBlock + slot16;
   const bool known = at >= 0;            // no such page: NaN
   const int8_t *codes = (values ? pool.v : pool.k) + (known ? at : 0) * kKvBlock * D;
   const int byte = known ? (values ? pool.vs : pool.ks)[at] : 255;
   const bool live = pos >= s.first && pos < s.len;
-  const int64_t row = s.row + pos - s.first;
+  const int64_t row = s.row + (pos - s.first);
   if (values) {
     const int c = threadIdx.x;
     if (c < D && known) *reinterpret_cast<uint4 *>(turn + c * 16) = load16(codes + c * 16);
@@ -343,7 +336,8 @@ hipError_t launch_kv_append(const AppendArgs &a, bool bf16, bool out_bf16, hipSt
   const auto kernel = bf16 ? (out_bf16 ? kv_append_kernel<true, true> : kv_append_kernel<true, false>)
                            : (out_bf16 ? kv_append_kernel<false, true> : kv_append_kernel<false, false>);
   for (int64_t first = 0; first < all; first += most)
-    kernel<<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, lds, st>>>(a, blocks, first);
+    kernel<<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, lds, st>>>(
+        a, static_cast<uint32_t>(blocks), static_cast<uint32_t>(first));
   return hipGetLastError();
 }
 
@@ -351,7 +345,8 @@ hipError_t launch_kv_read(const KvPool &pool, const KvSeqs &seqs, void *ko, void
   const int64_t all = block_slots(seqs.T, seqs.N) * pool.Hk * 2, most = max_groups(kThreads);
   const auto kernel = out_bf16 ? kv_read_kernel<true> : kv_read_kernel<false>;
   for (int64_t first = 0; first < all; first += most)
-    kernel<<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, 0, st>>>(pool, seqs, ko, vo, first);
+    kernel<<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, 0, st>>>(
+        pool, seqs, ko, vo, static_cast<uint32_t>(first));
   return hipGetLastError();
 }
 

@@ -16,39 +16,60 @@ namespace q4 {
 
 constexpr int kKvBlock = 16;
 
-// The last i in 0 .. n - 1 with f(i) <= x, f not decreasing; -1 if there is
-// none.  G lanes (a power of two, 16 or 64) search together, all of them active.
+// What all lanes have the same of, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A sequence's rows of this call (its last tokens) and where they stand; 32 bits,
+// as starts and lengths have.
+struct Sequence {
+  int i;            // its number, or -1: none
+  int row, n;       // first row, rows
+  int len, first;   // tokens with them; position of the first row (below 0: more rows than tokens)
+  __device__ __forceinline__ void set(int a, int b, int l) {
+    row = a;
+    n = b > a ? b - a : 0;
+    len = l > 0 ? l : 0;
+    first = len - n;
+  }
+  static __device__ __forceinline__ int clamp(int v, int64_t T) { return v < 0 ? 0 : v > T ? static_cast<int>(T) : v; }
+};
+
+// The last sequence i with f(starts[i], i) <= x, f not decreasing.  G lanes (16 or
+// 64) search together, all of them active; what they find is the same in each.
+// Fewer than 64 sequences take one round of loads.
 template <int G, class F>
-__device__ __forceinline__ int search_last(int n, int64_t x, F f) {
-  const int lane = threadIdx.x & (G - 1), base = threadIdx.x & 63 & ~(G - 1);
-  int lo = 0;
-  while (n > 0) {
-    const int step = (n + G - 1) / G, i = lane * step;
-    const bool yes = i < n && f(lo + i) <= x;
+__device__ __forceinline__ Sequence find_sequence(const KvSeqs &s, uint32_t x, F f) {
+  Sequence q;
+  const int N = static_cast<int>(s.N), lane = threadIdx.x & 63;
+  if (G == 64 && N < 64) {
+    const int start = Sequence::clamp(s.starts[min(lane, N)], s.T), length = s.lengths[min(lane, N - 1)];
+    q.i = __popcll(__ballot(lane < N && f(static_cast<uint32_t>(start), lane) <= x)) - 1;
+    if (q.i >= 0)
+      q.set(__builtin_amdgcn_readlane(start, q.i), __builtin_amdgcn_readlane(start, q.i + 1),
+            __builtin_amdgcn_readlane(length, q.i));
+    return q;
+  }
+  const int sub = lane & (G - 1), base = lane & ~(G - 1);
+  int lo = 0, n = N;
+  q.i = -1;
+  while (true) {
+    const int step = (n + G - 1) / G, i = sub * step;
+    const bool yes = i < n && f(static_cast<uint32_t>(Sequence::clamp(s.starts[lo + (i < n ? i : 0)], s.T)), lo + i) <= x;
     unsigned long long b = __ballot(yes) >> base;
     if constexpr (G < 64) b &= (1ull << G) - 1;
     const int c = __popcll(b);
-    if (c == 0) return -1;             // only in the first turn
+    if (c == 0) return q;               // only in the first turn
     lo += (c - 1) * step;
     if (step == 1) break;
     n = n - (c - 1) * step < step ? n - (c - 1) * step : step;
   }
-  return lo;
-}
-
-// A sequence's rows of this call (its last tokens) and where they stand.
-struct Sequence {
-  int64_t row, n;      // first row, rows
-  int64_t len, first;  // tokens with them; position of the first row (below 0: more rows than tokens)
-  __device__ __forceinline__ Sequence(const KvSeqs &s, int i) {
-    const int64_t a = clamp(s.starts[i], s.T), b = clamp(s.starts[i + 1], s.T);
-    row = a;
-    n = b > a ? b - a : 0;
-    len = s.lengths[i] > 0 ? s.lengths[i] : 0;
-    first = len - n;
+  q.i = lo;
+  q.set(Sequence::clamp(s.starts[lo], s.T), Sequence::clamp(s.starts[lo + 1], s.T), s.lengths[lo]);
+  if constexpr (G == 64) {
+    q.i = uniform(q.i), q.row = uniform(q.row), q.n = uniform(q.n), q.len = uniform(q.len), q.first = uniform(q.first);
   }
-  static __device__ __forceinline__ int64_t clamp(int64_t v, int64_t T) { return v < 0 ? 0 : v > T ? T : v; }
-};
+  return q;
+}
 
 // The number in the pool of block b of a head of sequence i, or -1 where its
 // page is not in the table or not in the pool.
@@ -66,16 +87,16 @@ __device__ __forceinline__ int64_t block_at(const KvPool &c, int i, int64_t b, i
 inline int64_t block_slots(int64_t T, int64_t N) { return T / kKvBlock + 2 * N; }
 
 struct BlockOf {
-  int i;             // the sequence, or -1: nothing to do
-  int64_t b;         // its block
-  __device__ __forceinline__ BlockOf(const KvSeqs &s, int64_t slot) {
-    const auto f = [&](int j) { return Sequence::clamp(s.starts[j], s.T) / kKvBlock + 2 * int64_t(j); };
-    i = search_last<64>(static_cast<int>(s.N), slot, f);
-    if (i < 0) return;
-    const Sequence q(s, i);
-    const int64_t lo = q.first > 0 ? q.first : 0;
-    b = lo / kKvBlock + (slot - f(i));
-    if (q.n == 0 || b * kKvBlock >= q.len) i = -1;
+  Sequence s;        // i = -1: nothing to do
+  int b;             // its block
+  __device__ __forceinline__ BlockOf(const KvSeqs &seqs, uint32_t slot) {
+    const auto f = [&](uint32_t start, int j) { return start / kKvBlock + 2 * static_cast<uint32_t>(j); };
+    s = find_sequence<64>(seqs, slot, f);
+    if (s.i < 0) return;
+    const uint32_t ahead = slot - f(static_cast<uint32_t>(s.row), s.i);
+    b = max(s.first, 0) / kKvBlock + static_cast<int>(ahead);
+    // (a number of blocks past any sequence's)
+    if (s.n == 0 || ahead > (1u << 28) || b * static_cast<int64_t>(kKvBlock) >= s.len) s.i = -1;
   }
 };
 

@@ -870,10 +870,15 @@ q4_status cache_bad(const q8_kv_cache *c, const int32_t *starts, const int32_t *
   if (misaligned(c->k, 16) || misaligned(c->v, 16)) return Q4_EINVAL;
   if (c->D % 16 != 0 || c->D < 16 || c->D > Q8_KV_MAX_D) return Q4_ESHAPE;
   if (c->page < 16 || c->page > 65536 || (c->page & (c->page - 1)) != 0) return Q4_ESHAPE;
-  if (c->heads < 1 || c->n_pages < 1 || c->table < 1) return Q4_ESHAPE;
-  if (c->heads > kMaxRows || c->n_pages > kMaxRows || c->n_pages * c->heads > kMaxRows / (c->page / 16)) return Q4_ESHAPE;
+  if (c->heads < 1 || c->heads > 65536 || c->n_pages < 1 || c->table < 1) return Q4_ESHAPE;
+  if (c->n_pages > kMaxRows || c->n_pages * c->heads > kMaxRows / (c->page / 16)) return Q4_ESHAPE;
   if (T > kMaxRows || c->sequences > kMaxRows || c->table > kMaxRows) return Q4_ESHAPE;
   return Q4_OK;
+}
+
+// Workgroups of the append and read kernels: two a block slot and head, one for 16 query rows.
+bool too_many_groups(const q8_kv_cache &c, int64_t T, int64_t Hq) {
+  return (u(T) / 16 + 2 * u(c.sequences)) * u(c.heads) * 2 + u(T) * u(Hq) / 16 + 1 > UINT32_MAX;
 }
 
 uint64_t pool_blocks(const q8_kv_cache &c) { return u(c.n_pages) * u(c.heads) * u(c.page / 16); }
@@ -913,7 +918,7 @@ extern "C" q4_status q8_kv_append(const q8_kv_cache *cache, const int32_t *start
   const q8_kv_cache &c = *cache;
   if (cos_sin && (R % 2 != 0 || R < 2 || R > c.D || P < 1 || P > kMaxNK)) return Q4_ESHAPE;
   if (!cos_sin) P = R = 0;
-  if (Hq > kMaxRows || (T > 0 && Hq > kMaxRows / T)) return Q4_ESHAPE;
+  if (Hq > kMaxRows || (T > 0 && Hq > kMaxRows / T) || too_many_groups(c, T, Hq)) return Q4_ESHAPE;
   if (Hq == 0) q = q_out = nullptr, q_token = q_head = 0;
   if (!norm) k_gain = q_gain = nullptr;
   uint64_t qb, kb, vb;
@@ -943,7 +948,7 @@ extern "C" q4_status q8_kv_read(const q8_kv_cache *cache, const int32_t *starts,
   const q8_kv_cache &c = *cache;
   const CacheBufs b(c, starts, lengths);
   uint64_t out;
-  if (!span(T, c.heads, c.D, c.heads * c.D, c.D, size_of(yt), &out)) return Q4_ESHAPE;
+  if (!span(T, c.heads, c.D, c.heads * c.D, c.D, size_of(yt), &out) || too_many_groups(c, T, 0)) return Q4_ESHAPE;
   if (any_overlap({{k_out, out}, {v_out, out}}, {b.k, b.v, b.ks, b.vs, b.pages, b.starts, b.lengths})) return Q4_EINVAL;
   if (T == 0 || c.sequences == 0) return Q4_OK;
   if (!device_ok()) return Q4_EDEVICE;
@@ -956,7 +961,7 @@ namespace {
 
 // Sizes that attention takes beside those of the cache.
 bool attention_shape_bad(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
-  if (D % 16 != 0 || D < 16 || D > Q8_KV_MAX_D || Hk < 1 || Hq < 1 || Hq % Hk != 0) return true;
+  if (D % 16 != 0 || D < 16 || D > Q8_KV_MAX_D || Hk < 1 || Hk > 65536 || Hq < 1 || Hq % Hk != 0) return true;
   return T > kMaxRows || N > kMaxRows || Hq > kMaxRows || (T > 0 && Hq > kMaxRows / T) || max_len > kMaxRows;
 }
 
@@ -992,7 +997,8 @@ extern "C" q4_status q8_attention(const void *q, int64_t q_token, int64_t q_head
                   {{q, qb}, b.k, b.v, b.ks, b.vs, b.pages, b.starts, b.lengths}))
     return Q4_EINVAL;
   if (!device_ok()) return Q4_EDEVICE;
-  const q4::AttnArgs a = {pool_of(c), {starts, lengths, c.sequences, T}, q, q_token, q_head, y, Hq, scale, window, sinks};
+  const q4::AttnArgs a = {pool_of(c), {starts, lengths, c.sequences, T}, q, q_token, q_head, y, Hq,
+                          Hq / c.heads, scale, window, sinks};
   return finish(q4::launch_attention(a, p, xt == Q4_DT_BF16, yt == Q4_DT_BF16, ws, S(stream)),
                 p.tiled ? Q4_PATH_TILED : Q4_PATH_GEMV);
 }
