@@ -11,10 +11,15 @@
 // scaling by a power of two is exact.  Query rows, rounded to 24 or 8 bits, go
 // in f32.
 //
-// Bound: memory.  A block has one owner, a workgroup of 16 tokens by 16 lanes
-// (8 columns a lane, twice past 128), so nothing is shared between workgroups
-// and a block's scale is written by who writes its codes; keys and values are
-// two workgroups.  Values are turned in LDS to their layout, 16 tokens a column.
+// Bound: memory.  A block of a head has one owner, so nothing is shared between
+// workgroups, and a block's scale is written by who writes its codes; keys, values
+// and queries are workgroups of their own.  A row of a query or key head belongs to
+// D / 16 lanes (rounded up to a power of two) of 16 columns, two runs of 8 that are
+// rotated with each other where the halves' distance allows it; they keep their
+// angles and gains over the heads that their workgroup has.  Four value columns of
+// a block belong to a lane, which turns them in registers, 16 tokens a column.
+#include <type_traits>
+
 #include "kv_device.hpp"
 
 namespace q4 {
@@ -52,87 +57,123 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// One head's row by 16 lanes: lane j has the columns 8 j .. and 8 (j + 16) ...
-// Norm and rotation; turn: D numbers of LDS of the row's own.  All lanes of the
-// wave come here; rows that are not live read nothing.
-template <class real, bool BF16>
-__device__ __forceinline__ void head_row(const AppendArgs &a, const void *x, int64_t xi, const void *gain, int64_t pos,
-                                         bool live, real (&y)[2][8], real *turn) {
-  const int lane = threadIdx.x & 15, D = static_cast<int>(a.pool.D), R = static_cast<int>(a.R);
-  real ss = 0;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int c = 8 * (lane + 16 * u);
-    float t[8] = {};
-    if (live && c < D) load8<BF16>(x, xi + c, t);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      y[u][j] = t[j];
-      ss += y[u][j] * y[u][j];
-    }
-  }
-  if (a.norm) {
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) ss += __shfl_xor(ss, d);
-    const real rms = 1 / sqrt(ss / D + static_cast<real>(a.eps));
+// How a row's rotation meets its lanes.
+enum Rotation : int {
+  kPlain = 0,        // none
+  kNeighbours = 1,   // columns 2 i and 2 i + 1: in one run
+  kHalves = 2,       // i and i + R / 2, R a multiple of 16: in the two runs of one lane
+  kHalvesLds = 3     // any other R: through LDS
+};
+
+// The 16 columns of one lane of a head's row, and what is the same for all heads of
+// its token: gains and angles.
+template <class real, int MODE>
+struct Lane {
+  int c[2];          // first columns of the two runs
+  bool in;           // D / 16 lanes have columns
+  bool rotated;      // kHalves: these runs are
+  float g[2][8];
+  float co[2][8], si[2][8];   // kNeighbours: of pairs 0 .. 3 of each run; kHalves: of run 0's columns; kHalvesLds: of each column
+  // p: which of the row's lanes
+  __device__ __forceinline__ Lane(const AppendArgs &a, const void *gain, int p, int64_t pos) {
+    const int D = static_cast<int>(a.pool.D), R = static_cast<int>(a.R);
+    in = p < D / 16;
+    rotated = MODE == kHalves && p < R / 16;
+    c[0] = rotated ? 8 * p : 16 * p;
+    c[1] = rotated ? 8 * p + R / 2 : 16 * p + 8;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int c = 8 * (lane + 16 * u);
-      if (c >= D) break;
-      float g[8];
-      if (!gain) {
+      if (!a.norm || !gain || !in) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+        for (int j = 0; j < 8; ++j) g[u][j] = 1.0f;
       } else if (a.g_bf16) {
-        load8<true>(gain, c, g);
+        load8<true>(gain, c[u], g[u]);
       } else {
-        load8<false>(gain, c, g);
+        load8<false>(gain, c[u], g[u]);
       }
+    }
+    if (MODE == kPlain || !in) return;
+    const bool known = pos >= 0 && pos < a.P;   // an unknown position gives NaN, not a wild read
+    const float *cs = a.table + (known ? pos : 0) * R, *sn = cs + R / 2;
+    if constexpr (MODE == kHalves) {
+      if (rotated) load8<false>(cs, c[0], co[0]), load8<false>(sn, c[0], si[0]);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[u][j] = y[u][j] * rms * static_cast<real>(g[j]);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < (MODE == kNeighbours ? 4 : 8); ++j) {
+          const int col = c[u] + (MODE == kNeighbours ? 2 * j : j);
+          if (col >= R) break;
+          const int i = MODE == kNeighbours ? col / 2 : col < R / 2 ? col : col - R / 2;
+          co[u][j] = cs[i], si[u][j] = sn[i];
+        }
+    }
+    if (!known) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) co[u][j] = __builtin_nanf("");
     }
   }
-  if (!a.table) return;
-  const bool known = pos >= 0 && pos < a.P;   // an unknown position gives NaN, not a wild read
-  const float *cs = a.table + (known ? pos : 0) * R, *sn = cs + R / 2;
-  if (a.neighbours) {
+  // The row's norm, over L lanes, and rotation.  turn: D numbers of LDS of the row's own (kHalvesLds).
+  __device__ __forceinline__ void finish(const AppendArgs &a, int L, real (&y)[2][8], real *turn) const {
+    const int D = static_cast<int>(a.pool.D), R = static_cast<int>(a.R);
+    if (a.norm) {
+      real ss = 0;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = 8 * (lane + 16 * u);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        if (c + j >= R) break;
-        const real co = known ? cs[(c + j) / 2] : __builtin_nanf(""), si = sn[(c + j) / 2];
-        const real p = y[u][j], q = y[u][j + 1];
-        y[u][j] = p * co - q * si;
-        y[u][j + 1] = q * co + p * si;
-      }
+        for (int j = 0; j < 8; ++j) ss += y[u][j] * y[u][j];
+      for (int d = 1; d < L; d <<= 1) ss += __shfl_xor(ss, d);
+      const real rms = 1 / sqrt(ss / D + static_cast<real>(a.eps));
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[u][j] = y[u][j] * rms * static_cast<real>(g[u][j]);
     }
-  } else {
+    if constexpr (MODE == kNeighbours) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = 8 * (lane + 16 * u);
-      if (c < D) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) turn[c + j] = y[u][j];
+        for (int j = 0; j < 8; j += 2) {
+          if (c[u] + j >= R) break;
+          const real p = y[u][j], q = y[u][j + 1], cj = co[u][j / 2], sj = si[u][j / 2];
+          y[u][j] = p * cj - q * sj;
+          y[u][j + 1] = q * cj + p * sj;
+        }
+    } else if constexpr (MODE == kHalves) {
+      if (rotated) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const real p = y[0][j], q = y[1][j], cj = co[0][j], sj = si[0][j];
+          y[0][j] = p * cj - q * sj;
+          y[1][j] = q * cj + p * sj;
+        }
       }
-    }
-    wave_sync();
+    } else if constexpr (MODE == kHalvesLds) {
+      if (in) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = 8 * (lane + 16 * u) + j;
-        if (c >= R) break;
-        const bool low = c < R / 2;
-        const int p = low ? c : c - R / 2;
-        const real co = known ? cs[p] : __builtin_nanf(""), si = sn[p];
-        const real other = turn[low ? c + R / 2 : p];
-        y[u][j] = low ? y[u][j] * co - other * si : y[u][j] * co + other * si;
+          for (int j = 0; j < 8; ++j) turn[c[u] + j] = y[u][j];
       }
+      wave_sync();
+      if (in) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int col = c[u] + j;
+            if (col >= R) break;
+            const bool low = col < R / 2;
+            const real other = turn[low ? col + R / 2 : col - R / 2], cj = co[u][j], sj = si[u][j];
+            y[u][j] = low ? y[u][j] * cj - other * sj : y[u][j] * cj + other * sj;
+          }
+      }
+      wave_sync();   // the next head's row comes to the same place
     }
   }
-}
+};
 
 // The scale byte of a block whose largest magnitude is t, finite: the smallest
 // e + 127 >= 0 with t <= 127 2^e.  127 is 1.984375 2^6.
@@ -156,197 +197,338 @@ __device__ __forceinline__ uint32_t coarser(uint32_t w, int shift) {
   return o;
 }
 
-// Workgroups of a launch: slots x heads x {keys, values}, then 16 query rows each.
-template <bool BF16, bool OB>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, uint32_t blocks, uint32_t first) {
-  extern __shared__ double lds[];
-  __shared__ double tops[kThreads / 64];
-  const uint32_t id = first + blockIdx.x;
-  const int lane = threadIdx.x & 15, slot16 = threadIdx.x >> 4;
-  const int D = static_cast<int>(a.pool.D);
+// Bytes 0 .. 3 of four words, one a column -> four words, one a byte place.
+__device__ __forceinline__ void turn4(const uint32_t (&w)[4], uint32_t (&o)[4]) {
+  const uint32_t a = perm_b32(w[1], w[0], 0x05010400u), b = perm_b32(w[3], w[2], 0x05010400u);
+  const uint32_t c = perm_b32(w[1], w[0], 0x07030602u), d = perm_b32(w[3], w[2], 0x07030602u);
+  o[0] = perm_b32(b, a, 0x05040100u), o[1] = perm_b32(b, a, 0x07060302u);
+  o[2] = perm_b32(d, c, 0x05040100u), o[3] = perm_b32(d, c, 0x07060302u);
+}
 
-  if (id >= blocks) {   // queries
-    const uint32_t r = (id - blocks) * 16 + slot16, Hq = static_cast<uint32_t>(a.Hq);
-    const int64_t t = r / Hq, h = r % Hq;
-    const bool in = t < a.seqs.T;
-    const Sequence s = find_sequence<16>(a.seqs, in ? static_cast<uint32_t>(t) : 0, [&](uint32_t start, int) { return start; });
-    const bool live = in && s.i >= 0 && t - s.row < s.n;   // not behind the last sequence
-    const int64_t pos = live ? s.first + (t - s.row) : -1;
-    float y[2][8];
-    head_row<float, BF16>(a, a.q, t * a.q_t + h * a.q_h, a.gq, pos, live, y, reinterpret_cast<float *>(lds) + slot16 * D);
-    if (!live) return;
+// What a call touches of a block, and its scale.
+struct Open {
+  int had, have;      // tokens 0 .. had - 1 were there, had .. have - 1 are new
+  int old, byte;      // the scale bytes before and now
+  __device__ __forceinline__ void set(int need) { byte = had ? max(old, need) : need; }
+  // powers of two that the codes of what was there lose
+  __device__ __forceinline__ int shift() const { return had && byte != 255 ? byte - old : 0; }
+};
+
+// Workgroups of a launch: for each slot of a block the keys, key_groups times `heads`
+// heads, and the values, value_groups times as many heads as 256 lanes have; then
+// query rows, 256 / L tokens and `per` heads each.
+struct AppendPlan {
+  uint32_t key_groups, value_groups, blocks, query_groups;
+  int log2_L, heads, per;
+};
+
+template <bool BF16, bool OB, int MODE>
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, AppendPlan p, uint32_t first) {
+  extern __shared__ double lds[];
+  __shared__ unsigned long long tops[16];
+  __shared__ uint32_t value_tops[kThreads / 4];
+  const uint32_t id = first + blockIdx.x;
+  const int D = static_cast<int>(a.pool.D), L = 1 << p.log2_L, lane = threadIdx.x & (L - 1), row_of = threadIdx.x >> p.log2_L;
+  const int Hk = static_cast<int>(a.pool.Hk);
+
+  if (id >= p.blocks) {   // queries
+    const uint32_t tile = (id - p.blocks) / p.query_groups, group = (id - p.blocks) % p.query_groups;
+    const int64_t t = static_cast<int64_t>(tile) * (kThreads >> p.log2_L) + row_of;
+    const bool in_rows = t < a.seqs.T;
+    const Sequence s = find_sequence<1>(a.seqs, in_rows ? static_cast<uint32_t>(t) : 0, [&](uint32_t start, int) { return start; });
+    const bool live = in_rows && s.i >= 0 && t - s.row < s.n;   // not behind the last sequence
+    const Lane<float, MODE> ln(a, a.gq, lane, live ? s.first + (t - s.row) : -1);
+    const int h0 = static_cast<int>(group) * p.per, h1 = min(h0 + p.per, static_cast<int>(a.Hq));
+    const bool mine = live && ln.in;
+    float x[2][8] = {}, y[2][8];
+    auto fetch = [&](int h) {
+      if (mine)
+        for (int u = 0; u < 2; ++u) load8<BF16>(a.q, t * a.q_t + h * a.q_h + ln.c[u], x[u]);
+    };
+    fetch(h0);
+    for (int h = h0; h < h1; ++h) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = 8 * (lane + 16 * u);
-      if (c < D) store8<OB>(a.qo, (t * a.Hq + h) * D + c, y[u]);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[u][j] = x[u][j];
+      if (h + 1 < h1) fetch(h + 1);
+      ln.finish(a, L, y, reinterpret_cast<float *>(lds) + row_of * D);
+      if (mine)
+        for (int u = 0; u < 2; ++u) store8<OB>(a.qo, (t * a.Hq + h) * D + ln.c[u], y[u]);
     }
     return;
   }
 
-  const bool values = id & 1;
-  const uint32_t Hk = static_cast<uint32_t>(a.pool.Hk), h = (id >> 1) % Hk;
-  const BlockOf w(a.seqs, (id >> 1) / Hk);
+  const uint32_t groups = p.key_groups + p.value_groups, group = id % groups;
+  const BlockOf w(a.seqs, id / groups);
   const Sequence &s = w.s;
   if (s.i < 0) return;
-  const int64_t at = block_at(a.pool, s.i, w.b, h);
-  if (at < 0) return;                    // no such page: the tokens are dropped
-  const int begin = w.b * kKvBlock, had = max(max(s.first, 0) - begin, 0), have = min(s.len - begin, kKvBlock);
-  int8_t *codes = (values ? a.pool.v : a.pool.k) + at * kKvBlock * D;
-  uint8_t *scale = (values ? a.pool.vs : a.pool.ks) + at;
+  const int begin = w.b * kKvBlock;
+  Open open = {max(max(s.first, 0) - begin, 0), min(s.len - begin, kKvBlock), 0, 0};
+  const int64_t row0 = static_cast<int64_t>(s.row) + begin - s.first;   // of the block's token 0
+  const int64_t block0 = block_at(a.pool, s.i, w.b, 0);
+  if (block0 < 0) return;                    // no such page: the tokens are dropped
+  const int64_t unit = kKvBlock * D;
 
-  const bool live = slot16 >= had && slot16 < have;
-  const int64_t row = static_cast<int64_t>(s.row) + begin + slot16 - s.first;
-  double y[2][8];
-  if (values) {
+  if (group >= p.key_groups) {   // values: four columns of a head a lane
+    const int quads = D / 4, each = kThreads / quads, hh = threadIdx.x / quads, c = 4 * (threadIdx.x - hh * quads);
+    const int h = static_cast<int>(group - p.key_groups) * each + hh;
+    const bool mine = hh < each && h < Hk;
+    const int64_t at = block0 + (static_cast<int64_t>(mine ? h : 0) << a.pool.page_blocks_log2);
+    if (threadIdx.x < kThreads / 4) value_tops[threadIdx.x] = 0;
+    uint4 codes[4] = {};
+    if (open.had) {
+      open.old = a.pool.vs[at];
+      if (mine)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = 8 * (lane + 16 * u);
-      float t[8] = {};
-      if (live && c < D) load8<BF16>(a.v, row * a.v_t + h * a.v_h + c, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[u][j] = t[j];
+        for (int i = 0; i < 4; ++i) codes[i] = load16(a.pool.v + at * unit + (c + i) * 16);
     }
-  } else {
-    head_row<double, BF16>(a, a.k, row * a.k_t + h * a.k_h, a.gk, begin + slot16, live, y, lds + slot16 * D);
-  }
-
-  const int old = had ? *scale : 0;       // before the barrier: the first thread writes it behind that
-  double top = 0.0;
+    float x[kKvBlock][4];
+    uint32_t top = 0;
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+    for (int k = 0; k < kKvBlock; ++k) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double v = live ? fabs(y[u][j]) : 0.0;
-      top = v <= top ? top : v;          // NaN goes on as NaN: it is not <= anything ...
-      if (!(v < __builtin_inf())) top = __builtin_inf();   // ... and counts as infinity
-    }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = fmax(top, __shfl_xor(top, d));
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) top = fmax(top, tops[i]);
-  const int need = top < __builtin_inf() ? scale_byte(top) : 255;
-  const int byte = had ? max(old, need) : need;
-  const int shift = byte == 255 ? 0 : byte - old;   // of the codes that the block has
-
-  // codes of this lane's columns, 8 bytes a run
-  uint2 c8[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    uint32_t d[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = byte == 255 ? 0 : static_cast<int>(rint(ldexp(y[u][j], 127 - byte)));
-      d[j / 4] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (j & 3));
-    }
-    c8[u] = make_uint2(d[0], d[1]);
-  }
-  if (!values) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = 8 * (lane + 16 * u);
-      if (c >= D) break;
-      uint2 *p = reinterpret_cast<uint2 *>(codes + (c / 16) * 256 + slot16 * 16 + (c & 8));
-      if (live) *p = c8[u];
-      else if (slot16 < had && shift > 0) {
-        const uint2 t = *p;
-        *p = make_uint2(coarser(t.x, shift), coarser(t.y, shift));
+      for (int i = 0; i < 4; ++i) x[k][i] = 0.0f;
+      if (k < open.had || k >= open.have || !mine) continue;
+      const int64_t i0 = (row0 + k) * a.v_t + h * a.v_h + c;
+      if constexpr (BF16) {
+        const uint2 r = load_any<uint2>(static_cast<const uint16_t *>(a.v) + i0);
+        x[k][0] = __uint_as_float(r.x << 16), x[k][1] = __uint_as_float(r.x & 0xFFFF0000u);
+        x[k][2] = __uint_as_float(r.y << 16), x[k][3] = __uint_as_float(r.y & 0xFFFF0000u);
+      } else {
+        const float4 r = load_any<float4>(static_cast<const float *>(a.v) + i0);
+        x[k][0] = r.x, x[k][1] = r.y, x[k][2] = r.z, x[k][3] = r.w;
       }
     }
-  } else {
-    // columns side by side per token -> tokens side by side per column
-    uint8_t *turn = reinterpret_cast<uint8_t *>(lds);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int c = 8 * (lane + 16 * u);
-      if (c >= D) break;
+    for (int k = 0; k < kKvBlock; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        turn[(c + j) * 16 + slot16] = static_cast<uint8_t>((j < 4 ? c8[u].x : c8[u].y) >> (8 * (j & 3)));
-    }
+      for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[k][i]) & 0x7FFFFFFFu);   // NaN and infinity come last
     __syncthreads();
-    const int c = threadIdx.x;
-    if (c < D) {
-      uint4 v = *reinterpret_cast<const uint4 *>(turn + c * 16);
-      uint4 *p = reinterpret_cast<uint4 *>(codes + c * 16);
-      if (had) {
-        const uint4 t = *p;
-        const uint32_t o[4] = {t.x, t.y, t.z, t.w};
-        uint32_t n[4] = {v.x, v.y, v.z, v.w};
+    if (mine) atomicMax(&value_tops[hh], top);
+    __syncthreads();
+    if (!mine) return;
+    top = value_tops[hh];
+    open.set(top >= 0x7F800000u ? 255 : scale_byte(static_cast<double>(__uint_as_float(top))));
+    // x / 2^e in two exact factors, since one could pass the range
+    const int n = 127 - open.byte;
+    const float f0 = ldexpf(1.0f, n / 2), f1 = open.byte == 255 ? 0.0f : ldexpf(1.0f, n - n / 2);
+    const int shift = open.shift();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = had - 4 * j;     // bytes of this word that the block has
-          const uint32_t mask = k <= 0 ? 0u : k >= 4 ? ~0u : (1u << (8 * k)) - 1;
-          n[j] = (n[j] & ~mask) | ((shift > 0 ? coarser(o[j], shift) : o[j]) & mask);
+    for (int k = 0; k < kKvBlock; k += 4) {
+      uint32_t words[4], columns[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {       // a token's four columns
+        words[m] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int q = open.byte == 255 ? 0 : static_cast<int>(rintf(x[k + m][i] * f0 * f1));
+          words[m] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * i);
         }
-        v = make_uint4(n[0], n[1], n[2], n[3]);
       }
-      *p = v;
+      turn4(words, columns);
+      const int had = min(max(open.had - k, 0), 4);   // bytes of these words that the block has
+      const uint32_t mask = had == 4 ? ~0u : (1u << (8 * had)) - 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t &o = k == 0 ? codes[i].x : k == 4 ? codes[i].y : k == 8 ? codes[i].z : codes[i].w;
+        o = (columns[i] & ~mask) | ((shift > 0 ? coarser(o, shift) : o) & mask);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(a.pool.v + at * unit + (c + i) * 16) = codes[i];
+    if (c == 0) a.pool.vs[at] = static_cast<uint8_t>(open.byte);
+    return;
   }
-  if (threadIdx.x == 0) *scale = static_cast<uint8_t>(byte);
+
+  // keys: 16 tokens of 16 / L heads at a time
+  const int tok = row_of & 15, hh = row_of >> 4, at_once = 16 >> p.log2_L;
+  const bool live = tok >= open.had && tok < open.have;
+  const Lane<double, MODE> ln(a, a.gk, lane, begin + tok);
+  const int h0 = static_cast<int>(group) * p.heads, h1 = min(h0 + p.heads, Hk);
+  for (int hb = h0; hb < h1; hb += at_once) {
+    const int h = hb + hh;
+    const bool mine = h < h1;
+    const int64_t at = block0 + (static_cast<int64_t>(mine ? h : h0) << a.pool.page_blocks_log2);
+    if (threadIdx.x < 16) tops[threadIdx.x] = 0;
+    open.old = open.had ? a.pool.ks[at] : 0;   // before the barrier behind which it is written
+    uint2 *place[2];
+    uint2 before[2] = {};
+    double y[2][8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      place[u] = reinterpret_cast<uint2 *>(a.pool.k + at * unit + (ln.c[u] / 16) * 256 + tok * 16 + (ln.c[u] & 8));
+      if (mine && ln.in && tok < open.had) before[u] = *place[u];
+      float x[8] = {};
+      if (mine && live && ln.in) load8<BF16>(a.k, (row0 + tok) * a.k_t + h * a.k_h + ln.c[u], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[u][j] = x[j];
+    }
+    ln.finish(a, L, y, lds + row_of * D);
+    double top = 0.0;
+    bool finite = true;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double v = fabs(y[u][j]);
+        finite &= v < __builtin_inf();     // NaN is not either
+        top = fmax(top, v);
+      }
+    if (!finite) top = __builtin_inf();
+    if (!(mine && live && ln.in)) top = 0.0;
+    for (int d = 1; d < min(16 * L, 64); d <<= 1) top = fmax(top, __shfl_xor(top, d));
+    __syncthreads();
+    if ((threadIdx.x & (min(16 * L, 64) - 1)) == 0) atomicMax(&tops[hh], __builtin_bit_cast(unsigned long long, top));
+    __syncthreads();
+    top = __builtin_bit_cast(double, tops[hh]);
+    open.set(top < __builtin_inf() ? scale_byte(top) : 255);
+    const int shift = open.shift();
+    if (mine && ln.in) {
+      // times 2^(127 - byte), which f64 has
+      const double f = ldexp(1.0, 127 - open.byte);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (live) {
+          uint32_t d[2] = {0, 0};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int q = open.byte == 255 ? 0 : static_cast<int>(rint(y[u][j] * f));
+            d[j / 4] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (j & 3));
+          }
+          *place[u] = make_uint2(d[0], d[1]);
+        } else if (tok < open.had && shift > 0) {
+          *place[u] = make_uint2(coarser(before[u].x, shift), coarser(before[u].y, shift));
+        }
+      }
+      if (tok == 0 && lane == 0) a.pool.ks[at] = static_cast<uint8_t>(open.byte);
+    }
+    __syncthreads();   // before the next heads' maxima
+  }
 }
 
-// A block of one head, keys or values, as bf16 or f32 rows.
+// Blocks as bf16 or f32 rows: keys 16 columns of a token a lane, values four columns
+// of 16 tokens.
 template <bool OB>
-__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvPool pool, KvSeqs seqs, void *ko, void *vo, uint32_t first) {
-  __shared__ uint8_t turn[256 * 16];
-  const uint32_t id = first + blockIdx.x;
-  const bool values = id & 1;
-  const uint32_t Hk = static_cast<uint32_t>(pool.Hk), h = (id >> 1) % Hk;
-  const BlockOf w(seqs, (id >> 1) / Hk);
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvPool pool, KvSeqs seqs, AppendPlan p, void *ko, void *vo,
+                                                           uint32_t first) {
+  const uint32_t id = first + blockIdx.x, groups = p.key_groups + p.value_groups, group = id % groups;
+  const BlockOf w(seqs, id / groups);
   const Sequence &s = w.s;
   if (s.i < 0) return;
-  const int lane = threadIdx.x & 15, slot16 = threadIdx.x >> 4, D = static_cast<int>(pool.D);
-  const int64_t at = block_at(pool, s.i, w.b, h), pos = static_cast<int64_t>(w.b) * kKvBlock + slot16;
-  const bool known = at >= 0;            // no such page: NaN
-  const int8_t *codes = (values ? pool.v : pool.k) + (known ? at : 0) * kKvBlock * D;
-  const int byte = known ? (values ? pool.vs : pool.ks)[at] : 255;
-  const bool live = pos >= s.first && pos < s.len;
-  const int64_t row = s.row + (pos - s.first);
-  if (values) {
-    const int c = threadIdx.x;
-    if (c < D && known) *reinterpret_cast<uint4 *>(turn + c * 16) = load16(codes + c * 16);
-    __syncthreads();
-  }
+  const int D = static_cast<int>(pool.D), Hk = static_cast<int>(pool.Hk), begin = w.b * kKvBlock;
+  const int lo = max(s.first - begin, 0), hi = min(s.len - begin, kKvBlock);   // tokens that are asked for
+  const int64_t row0 = static_cast<int64_t>(s.row) + begin - s.first, unit = kKvBlock * D;
+  const int64_t block0 = block_at(pool, s.i, w.b, 0);
+  const bool known = block0 >= 0;            // no such page: NaN
+  // a code's value under scale byte b: 2^(b - 127) in f32, subnormal for b = 0
+  auto step = [](int b) {
+    return b == 255 ? __builtin_nanf("") : __uint_as_float(b ? static_cast<uint32_t>(b) << 23 : 0x400000u);
+  };
+  auto at_head = [&](int h) { return (known ? block0 : 0) + (static_cast<int64_t>(h) << pool.page_blocks_log2); };
+  if (group >= p.key_groups) {
+    const int quads = D / 4, each = kThreads / quads, hh = threadIdx.x / quads, c = 4 * (threadIdx.x - hh * quads);
+    const int h = static_cast<int>(group - p.key_groups) * each + hh;
+    if (hh >= each || h >= Hk) return;
+    uint4 codes[4] = {};
+    if (known)
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int c = 8 * (lane + 16 * u);
-    if (c >= D || !live) break;
-    float y[8];
-    uint2 t = make_uint2(0, 0);
-    if (!values && known) t = *reinterpret_cast<const uint2 *>(codes + (c / 16) * 256 + slot16 * 16 + (c & 8));
+      for (int i = 0; i < 4; ++i) codes[i] = load16(pool.v + at_head(h) * unit + (c + i) * 16);
+    const float f = step(known ? pool.vs[at_head(h)] : 255);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int8_t q = values ? static_cast<int8_t>(turn[(c + j) * 16 + slot16])
-                              : static_cast<int8_t>((j < 4 ? t.x : t.y) >> (8 * (j & 3)));
-      y[j] = byte == 255 ? __builtin_nanf("") : ldexpf(static_cast<float>(q), byte - 127);
+    for (int k = 0; k < kKvBlock; k += 4) {
+      uint32_t columns[4], words[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) columns[i] = k == 0 ? codes[i].x : k == 4 ? codes[i].y : k == 8 ? codes[i].z : codes[i].w;
+      turn4(columns, words);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (k + m < lo || k + m >= hi) continue;
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = static_cast<float>(static_cast<int8_t>(words[m] >> (8 * i))) * f;
+        const int64_t o = ((row0 + k + m) * Hk + h) * D + c;
+        if constexpr (OB) store_any(static_cast<uint16_t *>(vo) + o, make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])));
+        else store_any(static_cast<float *>(vo) + o, make_float4(y[0], y[1], y[2], y[3]));
+      }
     }
-    store8<OB>(values ? vo : ko, (row * pool.Hk + h) * D + c, y);
+    return;
   }
+  const int L = 1 << p.log2_L, lane = threadIdx.x & (L - 1), row_of = threadIdx.x >> p.log2_L;
+  const int tok = row_of & 15, at_once = 16 >> p.log2_L, h0 = static_cast<int>(group) * p.heads, h1 = min(h0 + p.heads, Hk);
+  if (tok < lo || tok >= hi || lane >= D / 16) return;
+  for (int h = h0 + (row_of >> 4); h < h1; h += at_once) {
+    uint4 codes = make_uint4(0, 0, 0, 0);
+    if (known) codes = load16(pool.k + at_head(h) * unit + lane * 256 + tok * 16);
+    const float f = step(known ? pool.ks[at_head(h)] : 255);
+    const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = static_cast<float>(static_cast<int8_t>(words[2 * u + j / 4] >> (8 * (j & 3)))) * f;
+      store8<OB>(ko, ((row0 + tok) * Hk + h) * D + 16 * lane + 8 * u, y);
+    }
+  }
+}
+
+// Shares for D columns, Hk heads and T rows: a workgroup has more than one set of
+// heads only where there are enough workgroups without.
+AppendPlan plan(const KvPool &pool, const KvSeqs &seqs, int64_t Hq) {
+  AppendPlan p = {};
+  while ((16 << p.log2_L) < pool.D) ++p.log2_L;
+  const int at_once = 16 >> p.log2_L;
+  const int64_t slots = block_slots(seqs.T, seqs.N), sets = (pool.Hk + at_once - 1) / at_once;
+  auto share = [](int64_t all, int64_t most) {
+    const int64_t n = all / 2048;
+    return n < 1 ? 1 : n < most ? n : most;
+  };
+  p.heads = static_cast<int>(share(slots * sets, sets < 8 ? sets : 8) * at_once);
+  p.key_groups = static_cast<uint32_t>((pool.Hk + p.heads - 1) / p.heads);
+  const int64_t each = kThreads / (pool.D / 4);
+  p.value_groups = static_cast<uint32_t>((pool.Hk + each - 1) / each);
+  p.blocks = static_cast<uint32_t>(slots * (p.key_groups + p.value_groups));
+  const int64_t tiles = (seqs.T + (kThreads >> p.log2_L) - 1) / (kThreads >> p.log2_L);
+  p.per = static_cast<int>(share(tiles * Hq, Hq < 8 ? (Hq < 1 ? 1 : Hq) : 8));
+  p.query_groups = static_cast<uint32_t>((Hq + p.per - 1) / p.per);
+  return p;
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const AppendArgs &a, bool bf16, bool out_bf16, hipStream_t st) {
-  const int64_t blocks = block_slots(a.seqs.T, a.seqs.N) * a.pool.Hk * 2;
-  const int64_t all = blocks + (a.q ? (a.seqs.T * a.Hq + 15) / 16 : 0), most = max_groups(kThreads);
-  const size_t lds = 16 * a.pool.D * sizeof(double);
-  const auto kernel = bf16 ? (out_bf16 ? kv_append_kernel<true, true> : kv_append_kernel<true, false>)
-                           : (out_bf16 ? kv_append_kernel<false, true> : kv_append_kernel<false, false>);
-  for (int64_t first = 0; first < all; first += most)
-    kernel<<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, lds, st>>>(
-        a, static_cast<uint32_t>(blocks), static_cast<uint32_t>(first));
+  const AppendPlan p = plan(a.pool, a.seqs, a.Hq);
+  const int64_t tiles = (a.seqs.T + (kThreads >> p.log2_L) - 1) / (kThreads >> p.log2_L);
+  const int64_t all = p.blocks + (a.q ? tiles * p.query_groups : 0), most = max_groups(kThreads);
+  const int mode = !a.table ? kPlain : a.neighbours ? kNeighbours : a.R % 16 == 0 ? kHalves : kHalvesLds;
+  const size_t lds = mode == kHalvesLds ? (kThreads >> p.log2_L) * a.pool.D * sizeof(double) : 0;
+  auto go = [&](auto kernel) {
+    for (int64_t first = 0; first < all; first += most)
+      kernel<<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, lds, st>>>(a, p, static_cast<uint32_t>(first));
+  };
+  auto pick = [&](auto in, auto out) {
+    constexpr bool I = decltype(in)::value, O = decltype(out)::value;
+    switch (mode) {
+      case kPlain: return go(kv_append_kernel<I, O, kPlain>);
+      case kNeighbours: return go(kv_append_kernel<I, O, kNeighbours>);
+      case kHalves: return go(kv_append_kernel<I, O, kHalves>);
+      default: return go(kv_append_kernel<I, O, kHalvesLds>);
+    }
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
+  if (bf16) out_bf16 ? pick(yes, yes) : pick(yes, no);
+  else out_bf16 ? pick(no, yes) : pick(no, no);
   return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvPool &pool, const KvSeqs &seqs, void *ko, void *vo, bool out_bf16, hipStream_t st) {
-  const int64_t all = block_slots(seqs.T, seqs.N) * pool.Hk * 2, most = max_groups(kThreads);
+  const AppendPlan p = plan(pool, seqs, 0);
+  const int64_t all = p.blocks, most = max_groups(kThreads);
   const auto kernel = out_bf16 ? kv_read_kernel<true> : kv_read_kernel<false>;
   for (int64_t first = 0; first < all; first += most)
     kernel<<<static_cast<unsigned>(all - first < most ? all - first : most), kThreads, 0, st>>>(
-        pool, seqs, ko, vo, static_cast<uint32_t>(first));
+        pool, seqs, p, ko, vo, static_cast<uint32_t>(first));
   return hipGetLastError();
 }
 

@@ -34,9 +34,9 @@ struct Sequence {
   static __device__ __forceinline__ int clamp(int v, int64_t T) { return v < 0 ? 0 : v > T ? static_cast<int>(T) : v; }
 };
 
-// The last sequence i with f(starts[i], i) <= x, f not decreasing.  G lanes (16 or
-// 64) search together, all of them active; what they find is the same in each.
-// Fewer than 64 sequences take one round of loads.
+// The last sequence i with f(starts[i], i) <= x, f not decreasing.  G lanes (1, or
+// 64 with the same x) search together, all of them active; what they find is the
+// same in each.  Fewer than 64 sequences take one round of loads.
 template <int G, class F>
 __device__ __forceinline__ Sequence find_sequence(const KvSeqs &s, uint32_t x, F f) {
   Sequence q;
@@ -49,25 +49,36 @@ __device__ __forceinline__ Sequence find_sequence(const KvSeqs &s, uint32_t x, F
             __builtin_amdgcn_readlane(length, q.i));
     return q;
   }
-  const int sub = lane & (G - 1), base = lane & ~(G - 1);
   int lo = 0, n = N;
   q.i = -1;
+  if constexpr (G == 1) {
+    const bool few = N < 64;               // then every lane has one's start
+    const int start = few ? Sequence::clamp(s.starts[min(lane, N)], s.T) : 0;
+    auto at = [&](int i) { return few ? __shfl(start, i) : Sequence::clamp(s.starts[i], s.T); };
+    int hi = N;                            // f(lo) <= x < f(hi), taken that way at the ends
+    for (int m = N; m > 0; m >>= 1) {      // the same turns in every lane
+      const int mid = (lo + hi) >> 1;
+      const bool yes = f(static_cast<uint32_t>(at(mid)), mid) <= x;
+      if (yes) lo = mid;
+      else hi = mid > lo ? mid : hi;
+    }
+    const int from = at(lo), to = at(lo + 1);   // by all lanes
+    q.i = f(static_cast<uint32_t>(from), lo) <= x ? lo : -1;
+    q.set(from, to, s.lengths[lo]);
+    return q;
+  }
   while (true) {
-    const int step = (n + G - 1) / G, i = sub * step;
+    const int step = (n + 63) / 64, i = lane * step;
     const bool yes = i < n && f(static_cast<uint32_t>(Sequence::clamp(s.starts[lo + (i < n ? i : 0)], s.T)), lo + i) <= x;
-    unsigned long long b = __ballot(yes) >> base;
-    if constexpr (G < 64) b &= (1ull << G) - 1;
-    const int c = __popcll(b);
-    if (c == 0) return q;               // only in the first turn
+    const int c = __popcll(__ballot(yes));
+    if (c == 0) return q;                  // only in the first turn
     lo += (c - 1) * step;
     if (step == 1) break;
     n = n - (c - 1) * step < step ? n - (c - 1) * step : step;
   }
   q.i = lo;
   q.set(Sequence::clamp(s.starts[lo], s.T), Sequence::clamp(s.starts[lo + 1], s.T), s.lengths[lo]);
-  if constexpr (G == 64) {
-    q.i = uniform(q.i), q.row = uniform(q.row), q.n = uniform(q.n), q.len = uniform(q.len), q.first = uniform(q.first);
-  }
+  q.i = uniform(q.i), q.row = uniform(q.row), q.n = uniform(q.n), q.len = uniform(q.len), q.first = uniform(q.first);
   return q;
 }
 
