@@ -28,14 +28,17 @@ namespace {
 constexpr int kThreads = 256;
 
 template <bool BF16>
+__device__ __forceinline__ float element(const Run8<BF16> &r, int j) {
+  if constexpr (BF16) return __uint_as_float(j & 1 ? r.v[j / 2] & 0xFFFF0000u : r.v[j / 2] << 16);
+  else return r.v[j];
+}
+
+template <bool BF16>
 __device__ __forceinline__ void load8(const void *p, int64_t i, float (&o)[8]) {
   Run8<BF16> t;
   t.load(p, i);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (BF16) o[j] = __uint_as_float(j & 1 ? t.v[j / 2] & 0xFFFF0000u : t.v[j / 2] << 16);
-    else o[j] = t.v[j];
-  }
+  for (int j = 0; j < 8; ++j) o[j] = element(t, j);
 }
 
 template <bool BF16>
@@ -223,7 +226,7 @@ struct AppendPlan {
 };
 
 template <bool BF16, bool OB, int MODE>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, AppendPlan p, uint32_t first) {
+__global__ __launch_bounds__(kThreads, MODE == kHalvesLds ? 2 : 3) void kv_append_kernel(AppendArgs a, AppendPlan p, uint32_t first) {
   extern __shared__ double lds[];
   __shared__ unsigned long long tops[16];
   __shared__ uint32_t value_tops[kThreads / 4];
@@ -240,17 +243,19 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, Appen
     const Lane<float, MODE> ln(a, a.gq, lane, live ? s.first + (t - s.row) : -1);
     const int h0 = static_cast<int>(group) * p.per, h1 = min(h0 + p.per, static_cast<int>(a.Hq));
     const bool mine = live && ln.in;
-    float x[2][8] = {}, y[2][8];
+    Run8<BF16> x[2];
+    x[0].zero(), x[1].zero();
+    float y[2][8];
     auto fetch = [&](int h) {
       if (mine)
-        for (int u = 0; u < 2; ++u) load8<BF16>(a.q, t * a.q_t + h * a.q_h + ln.c[u], x[u]);
+        for (int u = 0; u < 2; ++u) x[u].load(a.q, t * a.q_t + h * a.q_h + ln.c[u]);
     };
     fetch(h0);
     for (int h = h0; h < h1; ++h) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[u][j] = x[u][j];
+        for (int j = 0; j < 8; ++j) y[u][j] = element(x[u], j);
       if (h + 1 < h1) fetch(h + 1);
       ln.finish(a, L, y, reinterpret_cast<float *>(lds) + row_of * D);
       if (mine)
@@ -266,23 +271,15 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, Appen
   const int begin = w.b * kKvBlock;
   Open open = {max(max(s.first, 0) - begin, 0), min(s.len - begin, kKvBlock), 0, 0};
   const int64_t row0 = static_cast<int64_t>(s.row) + begin - s.first;   // of the block's token 0
+  // The page is looked up while the rows are on their way; no such page: the tokens are dropped.
   const int64_t block0 = block_at(a.pool, s.i, w.b, 0);
-  if (block0 < 0) return;                    // no such page: the tokens are dropped
   const int64_t unit = kKvBlock * D;
 
   if (group >= p.key_groups) {   // values: four columns of a head a lane
     const int quads = D / 4, each = kThreads / quads, hh = threadIdx.x / quads, c = 4 * (threadIdx.x - hh * quads);
     const int h = static_cast<int>(group - p.key_groups) * each + hh;
     const bool mine = hh < each && h < Hk;
-    const int64_t at = block0 + (static_cast<int64_t>(mine ? h : 0) << a.pool.page_blocks_log2);
     if (threadIdx.x < kThreads / 4) value_tops[threadIdx.x] = 0;
-    uint4 codes[4] = {};
-    if (open.had) {
-      open.old = a.pool.vs[at];
-      if (mine)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) codes[i] = load16(a.pool.v + at * unit + (c + i) * 16);
-    }
     float x[kKvBlock][4];
     uint32_t top = 0;
 #pragma unroll
@@ -299,6 +296,15 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, Appen
         const float4 r = load_any<float4>(static_cast<const float *>(a.v) + i0);
         x[k][0] = r.x, x[k][1] = r.y, x[k][2] = r.z, x[k][3] = r.w;
       }
+    }
+    if (block0 < 0) return;
+    const int64_t at = block0 + (static_cast<int64_t>(mine ? h : 0) << a.pool.page_blocks_log2);
+    uint4 codes[4] = {};
+    if (open.had) {
+      open.old = a.pool.vs[at];
+      if (mine)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) codes[i] = load16(a.pool.v + at * unit + (c + i) * 16);
     }
 #pragma unroll
     for (int k = 0; k < kKvBlock; ++k)
@@ -346,24 +352,26 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, Appen
   const bool live = tok >= open.had && tok < open.have;
   const Lane<double, MODE> ln(a, a.gk, lane, begin + tok);
   const int h0 = static_cast<int>(group) * p.heads, h1 = min(h0 + p.heads, Hk);
+  Run8<BF16> x[2];
+  x[0].zero(), x[1].zero();
+  auto fetch = [&](int h) {
+    if (h < h1 && live && ln.in)
+      for (int u = 0; u < 2; ++u) x[u].load(a.k, (row0 + tok) * a.k_t + h * a.k_h + ln.c[u]);
+  };
+  fetch(h0 + hh);
+  if (block0 < 0) return;
   for (int hb = h0; hb < h1; hb += at_once) {
     const int h = hb + hh;
     const bool mine = h < h1;
     const int64_t at = block0 + (static_cast<int64_t>(mine ? h : h0) << a.pool.page_blocks_log2);
     if (threadIdx.x < 16) tops[threadIdx.x] = 0;
     open.old = open.had ? a.pool.ks[at] : 0;   // before the barrier behind which it is written
-    uint2 *place[2];
-    uint2 before[2] = {};
     double y[2][8];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      place[u] = reinterpret_cast<uint2 *>(a.pool.k + at * unit + (ln.c[u] / 16) * 256 + tok * 16 + (ln.c[u] & 8));
-      if (mine && ln.in && tok < open.had) before[u] = *place[u];
-      float x[8] = {};
-      if (mine && live && ln.in) load8<BF16>(a.k, (row0 + tok) * a.k_t + h * a.k_h + ln.c[u], x);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[u][j] = x[j];
-    }
+      for (int j = 0; j < 8; ++j) y[u][j] = element(x[u], j);
+    fetch(h + at_once);
     ln.finish(a, L, y, lds + row_of * D);
     double top = 0.0;
     bool finite = true;
@@ -389,6 +397,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, Appen
       const double f = ldexp(1.0, 127 - open.byte);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        uint2 *place = reinterpret_cast<uint2 *>(a.pool.k + at * unit + (ln.c[u] / 16) * 256 + tok * 16 + (ln.c[u] & 8));
         if (live) {
           uint32_t d[2] = {0, 0};
 #pragma unroll
@@ -396,9 +405,10 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a, Appen
             const int q = open.byte == 255 ? 0 : static_cast<int>(rint(y[u][j] * f));
             d[j / 4] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (j & 3));
           }
-          *place[u] = make_uint2(d[0], d[1]);
+          *place = make_uint2(d[0], d[1]);
         } else if (tok < open.had && shift > 0) {
-          *place[u] = make_uint2(coarser(before[u].x, shift), coarser(before[u].y, shift));
+          const uint2 d = *place;
+          *place = make_uint2(coarser(d.x, shift), coarser(d.y, shift));
         }
       }
       if (tok == 0 && lane == 0) a.pool.ks[at] = static_cast<uint8_t>(open.byte);
@@ -480,7 +490,7 @@ AppendPlan plan(const KvPool &pool, const KvSeqs &seqs, int64_t Hq) {
   const int at_once = 16 >> p.log2_L;
   const int64_t slots = block_slots(seqs.T, seqs.N), sets = (pool.Hk + at_once - 1) / at_once;
   auto share = [](int64_t all, int64_t most) {
-    const int64_t n = all / 2048;
+    const int64_t n = all / 1024;
     return n < 1 ? 1 : n < most ? n : most;
   };
   p.heads = static_cast<int>(share(slots * sets, sets < 8 ? sets : 8) * at_once);
