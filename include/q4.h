@@ -468,7 +468,7 @@ q4_status q8_kv_read(const q8_kv_cache *cache, const int32_t *starts, const int3
                      void *v_out, q4_dtype yt, void *stream);
 
 /* Bytes of device workspace that q8_attention needs, from sizes alone; 0 for
- * sizes that it refuses.  It depends on q4_set_path. */
+ * sizes that it refuses. */
 size_t q8_attention_workspace(int64_t T, int64_t sequences, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len,
                               int64_t window, int64_t sinks);
 

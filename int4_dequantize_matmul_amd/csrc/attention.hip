@@ -262,12 +262,24 @@ void go(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hipStre
 
 }  // namespace
 
+// Rows kernel | tiles, us, of N sequences of L tokens, n of them rows, Hq / Hk heads
+// of D.  bf16 with D above 64: from 128 tiles of 256 rows on (32/8 of 128: N 1 n 512 L
+// 4096, 64 tiles, 119 | 127, n 1024 157 | 133, n 4096 342 | 164; 16/4 of 96, N 1 n 2048 L
+// 4096, 128 tiles, 116 | 113), where a sequence half fills one (16/16 of 128, N 64 n 64 L
+// 1024 125 | 125, N 16 n 128 L 2048 89 | 58).  D up to 64 from 192 on (8/1 of 64, N 1 n 4096
+// L 4096, 128 tiles, 60 | 85; 32/8, N 1 n 2048 L 4096, 256 tiles, 145 | 93).  f32: from 256,
+// where a sequence has two (32/8 of 64, N 16 n 128 L 2048 113 | 141, n 256 223 | 157).
+static bool many_rows(int64_t T, int64_t N, int64_t G, int64_t Hk, int64_t D, bool two) {
+  const int64_t rows = T * G / N, tiles = (rows + 255) / 256 * N * Hk;
+  return two ? tiles >= 256 && rows >= 512 : tiles >= (D > 64 ? 128 : 192) && rows >= 128;
+}
+
 AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len, int64_t window,
-                        int64_t sinks, int path) {
+                        int64_t sinks, bool two, int path) {
   AttnPlan p = {};
   p.splits = 1;
-  // rows of one key head a sequence, on average
-  p.tiled = path == kPathTiled || (path == kPathAuto && T * (Hq / Hk) / N >= 64);
+  p.tiled = attention_tiled_ok(D, two) &&
+            (path == kPathTiled || (path == kPathAuto && many_rows(T, N, Hq / Hk, Hk, D, two)));
   if (p.tiled) return p;
   const int64_t G = Hq / Hk, groups = (T * G + kRows * N - 1) / (kRows * N) * N * Hk;
   int64_t keys = max_len;

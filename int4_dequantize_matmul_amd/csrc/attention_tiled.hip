@@ -1,9 +1,8 @@
 // Attention of prompts: many query rows share a tile of keys (mathematics and
 // operands: attention.hip, attn_device.hpp).
 //
-// A workgroup has 32 rows a wave of one key head, rows of all of its query heads
-// side by side.  Keys and values of a step (64 keys, 32 past 128 columns) become
-// halves once, on their way to LDS, where they lie as the matrix instructions'
+// A workgroup has 256 rows of one key head, 32 a wave, rows of all of its query
+// heads side by side.  Keys and values of a step of 64 keys become halves once, on their way to LDS, where they lie as the matrix instructions'
 // operands, 16 bytes a lane, 1 KB an instruction, so that neither writes nor
 // reads conflict.  An operand is on its way to registers seven instructions before
 // the one that takes it.  One barrier a step, which waits for LDS alone; the second
@@ -16,13 +15,14 @@
 namespace q4 {
 namespace {
 
-// WAVES waves, TILES times 32 keys a step.
-template <int ND, bool TWO, int WAVES, int TILES>
-__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(AttnArgs a, Types types, uint32_t last_slot) {
-  constexpr int kRows = 32 * WAVES, kOps = 2 * ND, kAll = TILES * kOps;   // operands of 1 KB of a product
-  constexpr int kBlocks = 2 * TILES, kSteps = 64 / kBlocks;               // blocks a step; steps whose blocks 64 lanes hold
-  constexpr int kUnits = kBlocks * ((ND + 1) / 2), kLoads = (kUnits + WAVES - 1) / WAVES;   // loads of a step, of a wave
-  __shared__ uint4 key_ops[2][TILES][kOps][64], value_ops[2][TILES][kOps][64];
+constexpr int kWaves = 8, kTiles = 2;   // waves a workgroup; times 32 keys a step
+
+template <int ND, bool TWO>
+__global__ __launch_bounds__(64 * kWaves, kWaves / 4) void attention_tiled_kernel(AttnArgs a, Types types, uint32_t last_slot) {
+  constexpr int kRows = 32 * kWaves, kOps = 2 * ND, kAll = kTiles * kOps;   // operands of 1 KB of a product
+  constexpr int kBlocks = 2 * kTiles, kSteps = 64 / kBlocks;               // blocks a step; steps whose blocks 64 lanes hold
+  constexpr int kUnits = kBlocks * ((ND + 1) / 2), kLoads = (kUnits + kWaves - 1) / kWaves;   // loads of a step, of a wave
+  __shared__ uint4 key_ops[2][kTiles][kOps][64], value_ops[2][kTiles][kOps][64];
   __shared__ int2 blocks[2][kBlocks];                                     // scale bytes and first key of a step's blocks
   // heads next to each other go to different XCDs, each with its keys in an L2 of its own; long rows first
   const uint32_t Hk = static_cast<uint32_t>(a.pool.Hk), slot = last_slot - blockIdx.x / Hk;
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   const int64_t unit = kKvBlock * D;
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
-    const int x = wave + WAVES * u, b = x % kBlocks, g = x / kBlocks, tl = b / 2, half = b % 2;
+    const int x = wave + kWaves * u, b = x % kBlocks, g = x / kBlocks, tl = b / 2, half = b % 2;
     // token 4 i + j of block h is row 8 i + 4 h + j of the first product
     const int token = lane & 15, chunk = 4 * g + (lane >> 4), col = 64 * g + lane;
     from_k[u] = min(chunk, D / 16 - 1) * 256 + token * 16;
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   auto load_values = [&] {   // of the step whose keys were loaded last
 #pragma unroll
     for (int u = 0; u < kLoads; ++u)
-      if (wave + WAVES * u < kUnits) raw_v[u] = load16(a.pool.v + of[u] * unit + from_v[u]);
+      if (wave + kWaves * u < kUnits) raw_v[u] = load16(a.pool.v + of[u] * unit + from_v[u]);
   };
   auto load_keys = [&](int s) {
     const int l = s % kSteps;
@@ -106,15 +106,15 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
     }
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      if (wave + WAVES * u >= kUnits) continue;
-      of[u] = __builtin_amdgcn_readlane(cur.at, kBlocks * l + (wave + WAVES * u) % kBlocks);
+      if (wave + kWaves * u >= kUnits) continue;
+      of[u] = __builtin_amdgcn_readlane(cur.at, kBlocks * l + (wave + kWaves * u) % kBlocks);
       raw_k[u] = load16(a.pool.k + of[u] * unit + from_k[u]);
     }
   };
   auto store = [&](uint4 *ops, const int (&to)[kLoads], const uint4 (&raw)[kLoads]) {
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      if (wave + WAVES * u >= kUnits || to[u] < 0) continue;
+      if (wave + kWaves * u >= kUnits || to[u] < 0) continue;
       ops[to[u]] = codes_to_f16(raw[u].x, raw[u].y);
       ops[to[u] + 64] = codes_to_f16(raw[u].z, raw[u].w);
     }
@@ -146,20 +146,20 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   State<f32x16, ND, 2, TWO> st;
   constexpr int kRing = 8;
   uint4 ring[kRing];
-  f32x16 acc[TILES];
-  typename decltype(st)::Keys w[TILES];
+  f32x16 acc[kTiles];
+  typename decltype(st)::Keys w[kTiles];
 #pragma unroll
-  for (int tl = 0; tl < TILES; ++tl)
+  for (int tl = 0; tl < kTiles; ++tl)
 #pragma unroll
     for (int u = 0; u < 2; ++u) w[tl].p[u] = w[tl].rest[u] = make_uint4(0, 0, 0, 0);
-  int by[TILES], key[TILES];
+  int by[kTiles], key[kTiles];
   // The products of step s - 1 with its values, of step s with its keys.  The first
   // step has weights and values of 0 in front of it, and behind the last one scores
   // that nobody reads: one form of this loop, whose results stay where they are.
   auto multiply = [&](int s) {
     const uint4 *vo = &value_ops[(s - 1) & 1][0][0][lane], *ko = &key_ops[s & 1][0][0][lane];
 #pragma unroll
-    for (int tl = 0; tl < TILES; ++tl) {
+    for (int tl = 0; tl < kTiles; ++tl) {
       const int2 m = blocks[s & 1][2 * tl + h];
       by[tl] = m.x, key[tl] = m.y;
       acc[tl] = f32x16{};
@@ -186,11 +186,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
   auto weigh = [&](int s) {
     if (s >= inner && s < outer) {
 #pragma unroll
-      for (int tl = 0; tl < TILES; ++tl)
+      for (int tl = 0; tl < kTiles; ++tl)
         w[tl].template scores<false>(acc[tl], q.factor, by[tl] & 255, by[tl] >> 8, [](int) { return false; });
     } else {
 #pragma unroll
-      for (int tl = 0; tl < TILES; ++tl)
+      for (int tl = 0; tl < kTiles; ++tl)
         w[tl].template scores<true>(acc[tl], q.factor, by[tl] & 255, by[tl] >> 8, [&](int j) {
           return sight.hides(pos, key[tl] + j);
         });
@@ -204,10 +204,10 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
     store_keys(0);
     if (steps > 1) load_keys(1);
   }
-  for (int x = threadIdx.x; x < kAll * 64; x += 64 * WAVES) (&value_ops[1][0][0][0])[x] = make_uint4(0, 0, 0, 0);
+  for (int x = threadIdx.x; x < kAll * 64; x += 64 * kWaves) (&value_ops[1][0][0][0])[x] = make_uint4(0, 0, 0, 0);
   lds_barrier();
   // Between two barriers, step s: K(s) and V(s - 1) are read, K(s + 1) and V(s) written.
-  const bool second = WAVES == 8 && wave >= 4;
+  const bool second = wave >= kWaves / 2;
   for (int s = 0; s <= steps; ++s) {
     if (s <= end) multiply(s);
     stage(s);
@@ -232,33 +232,28 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void attention_tiled_kernel(
 
 template <int ND, bool TWO>
 void go(const AttnArgs &a, const Types &t, hipStream_t st) {
-  // 64 keys of more than 128 columns would be more than 64 KB in two buffers, and eight waves' registers too few
-  constexpr int WAVES = ND <= 4 ? 8 : 4, TILES = ND <= 4 ? 2 : 1;
-  const int64_t slots = tile_slots(a.seqs.T, a.seqs.N, a.G, 32 * WAVES), most = max_groups(64 * WAVES) / a.pool.Hk;
+  const int64_t slots = tile_slots(a.seqs.T, a.seqs.N, a.G, 32 * kWaves), most = max_groups(64 * kWaves) / a.pool.Hk;
   for (int64_t left = slots; left > 0; left -= most)   // slots of a launch
-    attention_tiled_kernel<ND, TWO, WAVES, TILES>
-        <<<static_cast<unsigned>((left < most ? left : most) * a.pool.Hk), 64 * WAVES, 0, st>>>(
-            a, t, static_cast<uint32_t>(left - 1));
-}
-
-template <bool TWO>
-void pick(const AttnArgs &a, const Types &t, hipStream_t st) {
-  switch ((a.pool.D + 31) / 32) {
-    case 1: return go<1, TWO>(a, t, st);
-    case 2: return go<2, TWO>(a, t, st);
-    case 3: return go<3, TWO>(a, t, st);
-    case 4: return go<4, TWO>(a, t, st);
-    case 5: return go<5, TWO>(a, t, st);
-    case 6: return go<6, TWO>(a, t, st);
-    case 7: return go<7, TWO>(a, t, st);
-    default: return go<8, TWO>(a, t, st);
-  }
+    attention_tiled_kernel<ND, TWO><<<static_cast<unsigned>((left < most ? left : most) * a.pool.Hk), 64 * kWaves, 0, st>>>(
+        a, t, static_cast<uint32_t>(left - 1));
 }
 
 }  // namespace
 
+// Past 128 columns, with two halves past 64, a wave's registers would not do.
+bool attention_tiled_ok(int64_t D, bool two) { return D <= (two ? 64 : 128); }
+
 hipError_t launch_attention_tiled(const AttnArgs &a, const Types &t, hipStream_t st) {
-  t.in_bf16 && t.out_bf16 ? pick<false>(a, t, st) : pick<true>(a, t, st);
+  const int64_t nd = (a.pool.D + 31) / 32;
+  if (t.in_bf16 && t.out_bf16) {
+    if (nd == 1) go<1, false>(a, t, st);
+    else if (nd == 2) go<2, false>(a, t, st);
+    else if (nd == 3) go<3, false>(a, t, st);
+    else go<4, false>(a, t, st);
+  } else {
+    if (nd == 1) go<1, true>(a, t, st);
+    else go<2, true>(a, t, st);
+  }
   return hipGetLastError();
 }
 

@@ -295,7 +295,9 @@ __device__ __forceinline__ void store4(void *y, bool bf16, int64_t i, float a, f
 }
 
 
-// Many rows a sequence (attention_tiled.hip); launch_attention chooses.
+// Many rows a sequence (attention_tiled.hip); attention_plan chooses.  two: queries
+// or results in f32.
+bool attention_tiled_ok(int64_t D, bool two);
 hipError_t launch_attention_tiled(const AttnArgs &a, const Types &t, hipStream_t st);
 
 }  // namespace q4

@@ -223,14 +223,15 @@ struct AttnArgs {
 };
 // The routes that attention_plan knows (values of q4_path); any other means few rows.
 constexpr int kPathAuto = 0, kPathTiled = 3;
-// How a call is shared out; from sizes alone, so that the workspace is known before.
+// How a call is shared out; from sizes alone, so that the workspace is known
+// before.  two: queries or results in f32.
 struct AttnPlan {
   bool tiled;      // LDS-tiled kernel for many rows a sequence, else waves that share out the keys
   int splits;      // workgroups that share out a sequence's keys
   size_t ws;       // bytes of workspace
 };
 AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len, int64_t window,
-                        int64_t sinks, int path);
+                        int64_t sinks, bool two, int path);
 hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, bool bf16, bool out_bf16, void *ws, hipStream_t st);
 
 }  // namespace q4

@@ -971,7 +971,8 @@ extern "C" size_t q8_attention_workspace(int64_t T, int64_t sequences, int64_t H
                                          int64_t max_len, int64_t window, int64_t sinks) {
   if (T <= 0 || sequences <= 0 || max_len < 0 || window < 0 || sinks < 0) return 0;
   if (attention_shape_bad(T, sequences, Hq, Hk, D, max_len)) return 0;
-  return q4::attention_plan(T, sequences, Hq, Hk, D, max_len, window, sinks, g_path.load(std::memory_order_relaxed)).ws;
+  // of the kernel for few rows, whichever route a call takes
+  return q4::attention_plan(T, sequences, Hq, Hk, D, max_len, window, sinks, true, Q4_PATH_GEMV).ws;
 }
 
 extern "C" q4_status q8_attention(const void *q, int64_t q_token, int64_t q_head, q4_dtype xt_arg,
@@ -989,7 +990,8 @@ extern "C" q4_status q8_attention(const void *q, int64_t q_token, int64_t q_head
   uint64_t qb;
   if (!span(T, Hq, c.D, q_token, q_head, size_of(xt), &qb)) return Q4_ESHAPE;
   if (T == 0 || c.sequences == 0) return Q4_OK;
-  const q4::AttnPlan p = q4::attention_plan(T, c.sequences, Hq, c.heads, c.D, max_len, window, sinks,
+  const bool two = xt == Q4_DT_F32 || yt == Q4_DT_F32;
+  const q4::AttnPlan p = q4::attention_plan(T, c.sequences, Hq, c.heads, c.D, max_len, window, sinks, two,
                                             g_path.load(std::memory_order_relaxed));
   if (p.ws > 0 && (!ws || ws_bytes < p.ws)) return Q4_EINVAL;
   const CacheBufs b(c, starts, lengths);
