@@ -41,10 +41,10 @@ def check(x, gain, residual, eps, what, total=None):
     return got
 
 
-# rows of one wave and of four, in registers and read again; whole and partial runs of 8
+# rows of one to 16 waves, in registers and read again; whole and partial runs of 8
 @pytest.mark.parametrize("xt", ["f32", "bf16"])
 @pytest.mark.parametrize("M,K", [(1, 1), (3, 7), (2, 8), (5, 9), (4, 511), (7, 512), (1, 520), (2, 1023), (3, 2048),
-                                 (2, 2049), (1, 4095), (2, 5632), (1, 8191), (2, 8192), (2, 8200), (1, 20001), (130, 64)])
+                                 (2, 2049), (1, 4095), (2, 5632), (1, 8191), (2, 8192), (2, 8200), (1, 13312), (2, 16384), (1, 20001), (130, 64)])
 def test_parity(M, K, xt):
     rng = np.random.default_rng(M + K)
     x, r = (dev(rng.standard_normal((M, K)).astype(np.float32)).to(TORCH[xt]) for _ in range(2))
@@ -57,7 +57,7 @@ def test_parity(M, K, xt):
 @pytest.mark.parametrize("xt", ["f32", "bf16"])
 @pytest.mark.parametrize("K", [64, 520, 1000, 1024, 1500, 2048])
 def test_many_rows(K, xt):
-    """A wave a row: from 2048 rows on."""
+    """More rows than run at a time."""
     gen = torch.Generator(DEV).manual_seed(K)
     x, r = (torch.randn(2050, K, device=DEV, generator=gen).to(TORCH[xt]) for _ in range(2))
     g = (1 + 0.1 * torch.randn(K, device=DEV, generator=gen)).to(TORCH[xt])
