@@ -201,39 +201,45 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
   }
 }
 
-// Joins the splits of a row: a workgroup a row, its groups of D / 4 lanes share
-// the splits out and meet in LDS, in a fixed order.
-__global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types types, int offset, int splits,
-                                                           const float *parts, int64_t first) {
-  __shared__ float as[kMaxSplits], bs[kMaxSplits], ls[kMaxSplits];
+// Joins the splits of rows: D / 4 lanes times up to `splits` a row, which share the
+// splits out and meet in LDS, in a fixed order; as many rows a workgroup as fit.
+__global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types types, int offset, int splits, int groups,
+                                                           int rows, const float *parts, int64_t first) {
+  __shared__ float as[kMaxSplits], bs[kMaxSplits], ls[kMaxSplits];   // rows x splits, at most
   __shared__ f32x4 sums[kThreads];
-  const int64_t all = a.seqs.T * a.Hq, out = first + blockIdx.x, t = out / a.Hq;
-  const int D = static_cast<int>(a.pool.D), quads = D / 4, groups = kThreads / quads;
-  // rows in front of the first sequence or behind the last are left as they were
-  if (t < Sequence::clamp(a.seqs.starts[0], a.seqs.T) || t >= Sequence::clamp(a.seqs.starts[a.seqs.N], a.seqs.T)) return;
-  for (int s = threadIdx.x; s < splits; s += kThreads) {
-    as[s] = parts[s * all + out];
-    bs[s] = parts[(splits + s) * all + out];
-    ls[s] = parts[(2 * splits + s) * all + out];
+  const int64_t all = a.seqs.T * a.Hq, out0 = first + blockIdx.x * static_cast<int64_t>(rows);
+  const int D = static_cast<int>(a.pool.D), quads = D / 4, each = quads * groups;
+  const int64_t from = Sequence::clamp(a.seqs.starts[0], a.seqs.T) * a.Hq;
+  const int64_t to = Sequence::clamp(a.seqs.starts[a.seqs.N], a.seqs.T) * a.Hq;
+  if (static_cast<int>(threadIdx.x) < rows * splits) {
+    const int64_t out = out0 + threadIdx.x / splits, s = threadIdx.x % splits;
+    if (out < all) {
+      as[threadIdx.x] = parts[s * all + out];
+      bs[threadIdx.x] = parts[(splits + s) * all + out];
+      ls[threadIdx.x] = parts[(2 * splits + s) * all + out];
+    }
   }
   __syncthreads();
+  const int r = threadIdx.x / each, x = threadIdx.x - r * each, g = x / quads, col = 4 * (x - g * quads);
+  const int64_t out = out0 + r;
+  // rows in front of the first sequence or behind the last are left as they were
+  const bool live = r < rows && out >= from && out < to;
+  const float *ra = as + r * splits, *rb = bs + r * splits, *rl = ls + r * splits;
   float ma = -__builtin_inff(), mb = ma, l = 0.0f;
-  for (int s = 0; s < splits; ++s) ma = fmaxf(ma, as[s]), mb = fmaxf(mb, bs[s]);
-  for (int s = 0; s < splits; ++s) l = fmaf(ls[s], rescale(as[s], ls[s], ma), l);
-  const int g = threadIdx.x / quads, col = 4 * (threadIdx.x - g * quads);
   f32x4 sum = {};
-  if (g < groups) {
+  if (live) {
+    for (int s = 0; s < splits; ++s) ma = fmaxf(ma, ra[s]), mb = fmaxf(mb, rb[s]);
+    for (int s = 0; s < splits; ++s) l = fmaf(rl[s], rescale(ra[s], rl[s], ma), l);
 #pragma unroll 4
     for (int s = g; s < splits; s += groups) {
       const f32x4 o = *reinterpret_cast<const f32x4 *>(parts + results_at(splits, all) + (s * all + out) * D + col);
-      sum += o * rescale(bs[s], ls[s], mb);
+      sum += o * rescale(rb[s], rl[s], mb);
     }
   }
   sums[threadIdx.x] = sum;
   __syncthreads();
-  if (threadIdx.x >= quads) return;
-  const int used = groups < splits ? groups : splits;
-  for (int i = 1; i < used; ++i) sum += sums[i * quads + threadIdx.x];
+  if (!live || g > 0) return;
+  for (int i = 1; i < groups; ++i) sum += sums[threadIdx.x + i * quads];
   const Quotient q(ma, mb, l, offset);
   store4(a.y, types.out_bf16, out * D + col, q(sum[0]), q(sum[1]), q(sum[2]), q(sum[3]));
 }
@@ -248,10 +254,14 @@ void go_rows(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hi
         a, t, p.splits, p.splits > 1 ? ws : nullptr, static_cast<uint32_t>(first));
   }
   if (p.splits == 1) return;
-  const int64_t rows = a.seqs.T * a.Hq;
-  for (int64_t first = 0; first < rows; first += most)
-    combine_kernel<<<static_cast<unsigned>(rows - first < most ? rows - first : most), kThreads, 0, st>>>(
-        a, t, State<f32x4, 1, 4, TWO>::kOffset, p.splits, ws, first);
+  const int64_t all = a.seqs.T * a.Hq;
+  const int quads = 4 * NV, groups = p.splits < kThreads / quads ? p.splits : kThreads / quads, rows = kThreads / (quads * groups);
+  const int64_t per = most * rows;
+  for (int64_t first = 0; first < all; first += per) {   // rows of a launch
+    const int64_t n = all - first < per ? all - first : per;
+    combine_kernel<<<static_cast<unsigned>((n + rows - 1) / rows), kThreads, 0, st>>>(
+        a, t, State<f32x4, 1, 4, TWO>::kOffset, p.splits, groups, rows, ws, first);
+  }
 }
 
 template <bool TWO, int NV = 16>
@@ -284,8 +294,12 @@ AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D,
   const int64_t G = Hq / Hk, groups = (T * G + kRows * N - 1) / (kRows * N) * N * Hk;
   int64_t keys = max_len;
   if (window > 0 && window + sinks + 32 < keys) keys = window + sinks + 32;
-  // eight workgroups a CU in all, a wave at least 64 keys of what a sequence may have
-  int64_t s = (2048 + groups - 1) / groups;
+  // Two workgroups a CU in all, what runs at once, or up to eight of 4096 keys or more, which even out lengths; a wave
+  // at least 64 keys of what a sequence may have.  One token, 32 + 8 heads of 128, two against eight: 32 sequences of
+  // 1023 keys 19.5 and 26.4 us, of 4096 46.5 and 54.9, of 16384 189 and 192, of 1 to 16384 124 and 111 (four: 114).
+  int64_t s = (512 + groups - 1) / groups;
+  const int64_t even = (2048 + groups - 1) / groups < keys / 4096 ? (2048 + groups - 1) / groups : keys / 4096;
+  s = s > even ? s : even;
   const int64_t most = keys / (64 * kWaves);
   s = s < most ? s : most;
   p.splits = static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
