@@ -4,7 +4,8 @@ Prompts go through W4A4 products (activations quantized to MX FP4 in the call;
 once for the two projections that share them), single tokens through W4A16
 products (bf16 activations); queries and keys are normalised per head and
 rotated in one call, straight from the fused projection's output.  Attention
-itself is plain torch here.
+over whole keys and values is plain torch here; `served` takes the paged 8-bit
+cache instead, for prompts and single tokens alike.
 
     python examples/mx_decoder_layer.py        (needs an MI355X)
 """
@@ -75,6 +76,18 @@ class Layer:
         h = torch.nn.functional.silu(q4.q4_linear_w4a16_mx(x, *self.gate)) * q4.q4_linear_w4a16_mx(x, *self.up)
         return x + q4.q4_linear_w4a16_mx(h, *self.down), caches
 
+    def served(self, x, cache, pages, starts, lengths):
+        """bf16 rows of the requests' new tokens, one request after the other -> rows.
+        lengths int32 [N] count the new tokens, starts int32 [N + 1] are where a request's rows begin."""
+        T, H, K, D = x.shape[0], self.heads, self.kv_heads, self.head
+        linear = q4.q4_linear_w4a16_mx if T == pages.shape[0] else q4.q4_linear_w4a4_mx_dynamic
+        qkv = linear(x, *self.qkv).view(T, H + 2 * K, D)
+        q = q4.q8_kv_append(cache, pages, starts, lengths, qkv[:, H:H + K], qkv[:, H + K:], qkv[:, :H], self.cos_sin,
+                            self.k_gain, self.q_gain, eps=1e-6)
+        x = x + linear(q4.q8_attention(q, cache, pages, starts, lengths).view(T, H * D), *self.out)
+        h = torch.nn.functional.silu(linear(x, *self.gate)) * linear(x, *self.up)
+        return x + linear(h, *self.down)
+
 
 def main():
     layer, lengths = Layer(), [700, 37, 1, 290]
@@ -92,6 +105,27 @@ def main():
         torch.cuda.synchronize()
         print(f"{run} run: {x.shape[0]} prompt rows {1e3 * (t1 - t):.2f} ms, 8 tokens of {len(lengths)} requests "
               f"{1e3 * (time.perf_counter() - t1):.2f} ms")
+    assert torch.isfinite(y).all() and torch.isfinite(z).all()
+
+    width = -(-(max(lengths) + 16) // 64)
+    pages = torch.arange(len(lengths) * width, dtype=torch.int32, device="cuda:0").view(-1, width)
+    cache = q4.q8_kv_cache(pages.numel(), layer.kv_heads, 64, layer.head)
+    starts = torch.tensor([0, 700, 737, 738, 1028], dtype=torch.int32, device="cuda:0")
+    ones = torch.arange(len(lengths) + 1, dtype=torch.int32, device="cuda:0")
+    for run in ("first", "second"):
+        have = torch.tensor(lengths, dtype=torch.int32, device="cuda:0")
+        torch.cuda.synchronize()
+        t = time.perf_counter()
+        y = layer.served(x, cache, pages, starts, have)
+        torch.cuda.synchronize()
+        t1 = time.perf_counter()
+        z = torch.randn(len(lengths), layer.hidden, generator=gen, device="cuda:0").bfloat16()
+        for _ in range(8):
+            have += 1
+            z = layer.served(z, cache, pages, ones, have)
+        torch.cuda.synchronize()
+        print(f"{run} run, 8-bit cache: {x.shape[0]} prompt rows {1e3 * (t1 - t):.2f} ms, 8 tokens of {len(lengths)} "
+              f"requests {1e3 * (time.perf_counter() - t1):.2f} ms")
     assert torch.isfinite(y).all() and torch.isfinite(z).all()
 
 
