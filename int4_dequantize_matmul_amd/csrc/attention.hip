@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
   const int p0 = uniform(tile.s.first + tile.r0 / static_cast<int>(G));
   const int p1 = uniform(tile.s.first + (tile.r0 + rows - 1) / static_cast<int>(G)), pos = tile.s.first + t;
   const Sight sight(a.window, a.sinks);
-  const KeyBlocks keys(p0, p1, sight);
+  const KeyBlocks keys(p0, p1, sight, a.pool);
 
   const int steps = (keys.count + 3) / 4;
   const int w0 = static_cast<int>(static_cast<int64_t>(steps) * (split * kWaves + wave) / (splits * kWaves));

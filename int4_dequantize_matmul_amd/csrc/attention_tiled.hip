@@ -34,7 +34,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void attention_tiled_kerne
   const int D = static_cast<int>(a.pool.D);
   const int last = (tile.rows - tile.r0 > kRows ? tile.r0 + kRows : tile.rows) - 1;
   const Sight sight(a.window, a.sinks);
-  const KeyBlocks keys(tile.s.first + tile.r0 / static_cast<int>(G), tile.s.first + last / static_cast<int>(G), sight);
+  const KeyBlocks keys(tile.s.first + tile.r0 / static_cast<int>(G), tile.s.first + last / static_cast<int>(G), sight,
+                       a.pool);
   const int steps = (keys.count + kBlocks - 1) / kBlocks;
 
   // blocks of a round of kSteps steps, one a lane, two rounds ahead: pages, then scales
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void attention_tiled_kerne
   if (active) {
     if (p1 >= sight.window) inner = (static_cast<int>((static_cast<uint32_t>(p1 - sight.window) + 16) / kKvBlock) - keys.skip + kBlocks - 1) / kBlocks;
     if (p0 >= 0) outer = (static_cast<int>((static_cast<uint32_t>(p0) + 1) / kKvBlock) - keys.skip) / kBlocks;
-    end = p1 < 0 ? 0 : (p1 / kKvBlock + 1 - keys.skip + kBlocks - 1) / kBlocks;
+    end = p1 < 0 ? 0 : min((p1 / kKvBlock + 1 - keys.skip + kBlocks - 1) / kBlocks, steps);
   }
 
   State<f32x16, ND, 2, TWO> st;

@@ -84,12 +84,16 @@ struct Sight {
 
 // The keys that rows at positions p0 .. p1 see together, as blocks of 16 in a
 // row: sinks' blocks, then those from the window's first key to the last row's own.
+// Blocks past the table are NaN: of them the first that each row sees is enough, so
+// that the work is bounded by the table and not by what `lengths` says.
 struct KeyBlocks {
   int sink_blocks, skip, count;   // block v is v, or v + skip from sink_blocks on
-  __device__ __forceinline__ KeyBlocks(int p0, int p1, const Sight &s) {
-    const int end = p1 < 0 ? 0 : p1 / kKvBlock + 1;
+  __device__ __forceinline__ KeyBlocks(int p0, int p1, const Sight &s, const KvPool &pool) {
+    const int table = static_cast<int>(pool.width << pool.page_blocks_log2);
     const int first = p0 >= s.window ? (p0 - s.window + 1) / kKvBlock : 0;
-    sink_blocks = min((s.sinks >> 4) + ((s.sinks & 15) != 0), first);
+    const int last_first = p1 >= s.window ? (p1 - s.window + 1) / kKvBlock : 0;   // the last row's
+    const int end = p1 < 0 ? 0 : min(p1 / kKvBlock, max(table, last_first)) + 1;
+    sink_blocks = min(min((s.sinks >> 4) + ((s.sinks & 15) != 0), first), table + 1);
     skip = first - sink_blocks;
     count = end - skip;
   }

@@ -863,6 +863,8 @@ namespace {
 constexpr int64_t kMaxRows = INT32_MAX;   // starts and lengths are int32
 
 // Pointers and sizes of a cache and of a call's sequences.
+constexpr int64_t kKvMaxTokens = (int64_t(1) << 31) - 2048;   // positions a little past them are int32 still
+
 q4_status cache_bad(const q8_kv_cache *c, const int32_t *starts, const int32_t *lengths, int64_t T) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->pages || !starts || !lengths) return Q4_EINVAL;
   if (c->n_pages < 0 || c->page < 0 || c->heads < 0 || c->D < 0 || c->sequences < 0 || c->table < 0 || T < 0)
@@ -872,7 +874,7 @@ q4_status cache_bad(const q8_kv_cache *c, const int32_t *starts, const int32_t *
   if (c->page < 16 || c->page > 65536 || (c->page & (c->page - 1)) != 0) return Q4_ESHAPE;
   if (c->heads < 1 || c->heads > 65536 || c->n_pages < 1 || c->table < 1) return Q4_ESHAPE;
   if (c->n_pages > kMaxRows || c->n_pages * c->heads > kMaxRows / (c->page / 16)) return Q4_ESHAPE;
-  if (T > kMaxRows || c->sequences > kMaxRows || c->table > kMaxRows) return Q4_ESHAPE;
+  if (T > kMaxRows || c->sequences > kMaxRows || c->table > kKvMaxTokens / c->page) return Q4_ESHAPE;
   return Q4_OK;
 }
 

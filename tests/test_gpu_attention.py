@@ -435,3 +435,28 @@ def test_both_paths_of_the_binding_agree(monkeypatch):
     a = q4.q8_attention(*args)
     monkeypatch.setattr(q4, "_DIRECT", q4._NoDirect())
     assert_bitwise(host(q4.q8_attention(*args)), host(a), "paths")
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (8, 0), (8, 3), (30, 100), (8, 10 ** 9), (2 ** 31 - 1, 0), (2 ** 40, 2 ** 40)])
+def test_lengths_past_the_table(window, sinks, xt, path):
+    """Tokens that the table has no entry for are NaN to whoever sees them, without
+    work that goes by the length; the next sequence does not notice."""
+    q4.q4_set_path(path)
+    rng = np.random.default_rng(3)
+    H, Hq, D, page, new = 2, 6, 64, 16, 150
+    pages, P = new_pages(rng, [64, 60], page)
+    pool = random_pool(rng, P, H, page, D)
+    starts = [0, new, new + 2]
+    q = dev((3 * rng.standard_normal((new + 2, Hq, D))).astype(np.float32)).to(TORCH[xt])
+    for first in (75, 160, 64 + new, 2 ** 20, 2 ** 31 - 1):
+        y = q4.q8_attention(q, on_gpu(pool), dev(pages), i32(starts), i32([first, 60]), window=window, sinks=sinks)
+        if first < 1000:
+            check(y, q, pool, pages, starts, [first, 60], np.float32(D ** -0.5), window, sinks, first)
+        else:
+            assert torch.isnan(y[:new]).all()
+            rest = q[new:].contiguous()
+            own = q4.q8_attention(rest, on_gpu(pool), dev(pages[1:]), i32([0, 2]), i32([60]), window=window, sinks=sinks)
+            check(own, rest, pool, pages[1:], [0, 2], [60], np.float32(D ** -0.5), window, sinks, "alone")
+            check(y[new:], rest, pool, pages[1:], [0, 2], [60], np.float32(D ** -0.5), window, sinks, first)

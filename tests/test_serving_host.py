@@ -131,3 +131,14 @@ def test_the_binding_takes_no_host_tensors():
             bad()
     with pytest.raises(ValueError):
         q4.q8_kv_cache(2, 1, 24, 16, device="cpu")
+
+
+def test_limits_of_the_cache():
+    """Tokens of a table, heads, and workgroups of a launch."""
+    many = cache(heads=64)
+    for status, c, T in ((SH, cache(table=2 ** 26), 5), (SH, cache(table=2 ** 26 - 63), 5), (SH, cache(heads=65537), 5),
+                         (SH, many, 2 ** 31 - 1)):
+        assert call("q8_kv_append", dict(APPEND, cache=c, T=T, Hq=0, q=None, q_out=None)) == status
+        assert call("q8_kv_read", dict(cache=c, starts=ST, lengths=LEN, T=T, k_out=X, v_out=Y, yt=F32, stream=None)) == status
+    for c in (cache(table=2 ** 26), cache(table=2 ** 26 - 63), cache(heads=65537)):
+        assert call("q8_attention", dict(ATTENTION, cache=c)) == SH
