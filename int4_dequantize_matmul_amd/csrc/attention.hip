@@ -35,7 +35,12 @@ __host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { 
 // Few rows a sequence: a workgroup has 16 rows of one key head and a share of
 // their keys; its four waves share those out again, 64 keys a step straight from
 // the cache to registers, and meet in LDS.  A step's keys are loaded as soon as
-// those of the step before are multiplied, its values likewise.  parts: a, b, l
+// those of the step before are multiplied, its values likewise.  Bound by memory
+// for long contexts: one token, 131071 keys of 32 + 8 heads of 128 (268 MB) 53 us,
+// 5.1 TB/s; 64 tokens of up to 8192 keys (462 MB) 97 us, 4.8 TB/s.  By the chain of
+// loads (sequence, page, scales, codes) and the launch for short ones: 16 keys 7 us
+// with the call.  Eight waves a workgroup take one more and, as a CU then has one
+// workgroup, twice the time with many sequences (64 of 64 keys 16.6 us against 8.6).  parts: a, b, l
 // and results of splits x rows for combine_kernel, or null with one split.
 template <int NV, bool TWO>   // 16 NV columns
 __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Types types, int splits,
@@ -295,12 +300,14 @@ AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D,
   int64_t keys = max_len;
   if (window > 0 && window + sinks + 32 < keys) keys = window + sinks + 32;
   // Two workgroups a CU in all, what runs at once, or up to eight of 4096 keys or more, which even out lengths; a wave
-  // at least 64 keys of what a sequence may have.  One token, 32 + 8 heads of 128, two against eight: 32 sequences of
-  // 1023 keys 19.5 and 26.4 us, of 4096 46.5 and 54.9, of 16384 189 and 192, of 1 to 16384 124 and 111 (four: 114).
+  // at least 64 keys of what a sequence may have, and no splits below 1024 keys, where the join costs more than it gives.
+  // 32 + 8 heads of 128, one token a sequence, two workgroups a CU and eight: 32 sequences of 1023 keys 19.5 and 26.4
+  // us, of 4096 46.5 and 54.9, of 16384 189 and 192, of 1 to 16384 124 and 111 (four: 114).  One sequence of 512 keys
+  // 8.4 us, in two splits 10.3; of 1023 11.0, in two 11.7, in four 10.9.
   int64_t s = (512 + groups - 1) / groups;
   const int64_t even = (2048 + groups - 1) / groups < keys / 4096 ? (2048 + groups - 1) / groups : keys / 4096;
   s = s > even ? s : even;
-  const int64_t most = keys / (64 * kWaves);
+  const int64_t most = keys < 1024 ? 1 : keys / (64 * kWaves);
   s = s < most ? s : most;
   p.splits = static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
   p.ws = p.splits > 1 ? (results_at(p.splits, T * Hq) + p.splits * T * Hq * D) * sizeof(float) : 0;

@@ -861,10 +861,9 @@ extern "C" q4_status q8_rmsnorm_rows(const void *x, const void *residual, q4_dty
 namespace {
 
 constexpr int64_t kMaxRows = INT32_MAX;   // starts and lengths are int32
-
-// Pointers and sizes of a cache and of a call's sequences.
 constexpr int64_t kKvMaxTokens = (int64_t(1) << 31) - 2048;   // positions a little past them are int32 still
 
+// Pointers and sizes of a cache and of a call's sequences.
 q4_status cache_bad(const q8_kv_cache *c, const int32_t *starts, const int32_t *lengths, int64_t T) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->pages || !starts || !lengths) return Q4_EINVAL;
   if (c->n_pages < 0 || c->page < 0 || c->heads < 0 || c->D < 0 || c->sequences < 0 || c->table < 0 || T < 0)
