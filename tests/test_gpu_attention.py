@@ -460,3 +460,24 @@ def test_lengths_past_the_table(window, sinks, xt, path):
             own = q4.q8_attention(rest, on_gpu(pool), dev(pages[1:]), i32([0, 2]), i32([60]), window=window, sinks=sinks)
             check(own, rest, pool, pages[1:], [0, 2], [60], np.float32(D ** -0.5), window, sinks, "alone")
             check(y[new:], rest, pool, pages[1:], [0, 2], [60], np.float32(D ** -0.5), window, sinks, first)
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("D", [16, 48, 64, 80, 112, 128, 144, 208, 256])
+def test_joined_splits(D, xt, yt):
+    """Four to 64 splits of every head size, rows that fill no workgroup of the join, in front of them
+    and behind them rows of nobody; a workspace with the given bytes and no more."""
+    rng = np.random.default_rng(D + 1)
+    H, Hq, T, lengths, starts = 1, 3, 9, [1100, 0, 40], [2, 5, 5, 7]
+    pages, P = new_pages(rng, lengths, 32)
+    pool = random_pool(rng, P, H, 32, D)
+    q = dev((3 * rng.standard_normal((T, Hq, D))).astype(np.float32)).to(TORCH[xt])
+    for max_len in (1024, 1100, 5000, 10 ** 6):
+        need = q4.q8_attention_workspace(T, 3, Hq, H, D, max_len)
+        assert need > 0
+        room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+        room = room[-room.data_ptr() % 256:]
+        y = torch.full((T, Hq, D), 77.0, dtype=TORCH[yt], device=DEV)
+        q4.q8_attention(q, on_gpu(pool), dev(pages), i32(starts), i32(lengths), max_len=max_len, dtype=yt, ws=room[:need], y=y)
+        check(y, q, pool, pages, starts, lengths, np.float32(D ** -0.5), what=max_len)
+        assert (f64(y)[[0, 1, 7, 8]] == 77).all() and bool((room[need:] == 0xA5).all())
