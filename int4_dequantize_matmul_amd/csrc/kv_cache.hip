@@ -66,6 +66,14 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// 1 / sqrt(x).  In f64 from the instruction's estimate (2^-23 at worst), with three
+// terms of the series in what is left of x y^2: to 2^-51 in 7 operations, not 40.
+__device__ __forceinline__ float inverse_root(float x) { return 1.0f / sqrtf(x); }
+__device__ __forceinline__ double inverse_root(double x) {
+  const double y = __builtin_amdgcn_rsq(x), h = __builtin_fma(-x * y, y, 1.0);
+  return __builtin_fma(y * h, __builtin_fma(0.375, h, 0.5), y);
+}
+
 // How a row's rotation meets its lanes.
 enum Rotation : int {
   kPlain = 0,        // none
@@ -132,9 +140,9 @@ struct Lane {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss += y[u][j] * y[u][j];
+        for (int j = 0; j < 8; ++j) ss = __builtin_elementwise_fma(y[u][j], y[u][j], ss);
       for (int d = 1; d < L; d <<= 1) ss += __shfl_xor(ss, d);
-      const real rms = 1 / sqrt(ss / D + static_cast<real>(a.eps));
+      const real rms = inverse_root(ss / D + static_cast<real>(a.eps));
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -147,16 +155,16 @@ struct Lane {
         for (int j = 0; j < 8; j += 2) {
           if (c[u] + j >= R) break;
           const real p = y[u][j], q = y[u][j + 1], cj = co[u][j / 2], sj = si[u][j / 2];
-          y[u][j] = p * cj - q * sj;
-          y[u][j + 1] = q * cj + p * sj;
+          y[u][j] = __builtin_elementwise_fma(p, cj, -(q * sj));
+          y[u][j + 1] = __builtin_elementwise_fma(q, cj, p * sj);
         }
     } else if constexpr (MODE == kHalves) {
       if (rotated) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const real p = y[0][j], q = y[1][j], cj = co[0][j], sj = si[0][j];
-          y[0][j] = p * cj - q * sj;
-          y[1][j] = q * cj + p * sj;
+          y[0][j] = __builtin_elementwise_fma(p, cj, -(q * sj));
+          y[1][j] = __builtin_elementwise_fma(q, cj, p * sj);
         }
       }
     } else if constexpr (MODE == kHalvesLds) {
@@ -184,12 +192,19 @@ struct Lane {
   }
 };
 
-// The scale byte of a block whose largest magnitude is t, finite: the smallest
-// e + 127 >= 0 with t <= 127 2^e.  127 is 1.984375 2^6.
-__device__ __forceinline__ int scale_byte(double t) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, t);
-  const int e = static_cast<int>(b >> 52) - 1023 - 6;
-  const bool over = (b & 0xFFFFFFFFFFFFFull) > 0xFC00000000000ull;   // 0.984375 of a mantissa
+// What decides a scale byte of |v|: its high word, rounded up.  Infinity and NaN are last.
+__device__ __forceinline__ uint32_t size_of(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return (static_cast<uint32_t>(b >> 32) & 0x7FFFFFFFu) + (static_cast<uint32_t>(b) != 0);
+}
+constexpr uint32_t kNotFinite = 0x7FF00000u;
+
+// The scale byte of a block whose largest magnitude has size t: the smallest
+// e + 127 >= 0 with it <= 127 2^e; 127 is 1.984375 2^6.
+__device__ __forceinline__ int scale_byte(uint32_t t) {
+  if (t >= kNotFinite) return 255;
+  const int e = static_cast<int>(t >> 20) - 1023 - 6;
+  const bool over = (t & 0xFFFFFu) > 0xFC000u;   // 0.984375 of a mantissa
   const int b8 = max(e + (over ? 1 : 0) + 127, 0);
   return min(b8, 255);
 }
@@ -234,7 +249,7 @@ struct AppendPlan {
 template <bool BF16, bool OB, int MODE>
 __global__ __launch_bounds__(kThreads, MODE == kHalvesLds ? 2 : 3) void kv_append_kernel(AppendArgs a, AppendPlan p, uint32_t first) {
   extern __shared__ double lds[];
-  __shared__ unsigned long long tops[16];
+  __shared__ uint32_t tops[16];
   __shared__ uint32_t value_tops[kThreads / 4];
   const uint32_t id = first + blockIdx.x;
   const int D = static_cast<int>(a.pool.D), L = 1 << p.log2_L, lane = threadIdx.x & (L - 1), row_of = threadIdx.x >> p.log2_L;
@@ -321,7 +336,7 @@ __global__ __launch_bounds__(kThreads, MODE == kHalvesLds ? 2 : 3) void kv_appen
     __syncthreads();
     if (!mine) return;
     top = value_tops[hh];
-    open.set(top >= 0x7F800000u ? 255 : scale_byte(static_cast<double>(__uint_as_float(top))));
+    open.set(scale_byte(size_of(static_cast<double>(__uint_as_float(top)))));
     // x / 2^e in two exact factors, since one could pass the range
     const int n = 127 - open.byte;
     const float f0 = ldexpf(1.0f, n / 2), f1 = open.byte == 255 ? 0.0f : ldexpf(1.0f, n - n / 2);
@@ -379,27 +394,20 @@ __global__ __launch_bounds__(kThreads, MODE == kHalvesLds ? 2 : 3) void kv_appen
       for (int j = 0; j < 8; ++j) y[u][j] = element(x[u], j);
     fetch(h + at_once);
     ln.finish(a, L, y, lds + row_of * D);
-    double top = 0.0;
-    bool finite = true;
+    uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double v = fabs(y[u][j]);
-        finite &= v < __builtin_inf();     // NaN is not either
-        top = fmax(top, v);
-      }
-    if (!finite) top = __builtin_inf();
-    if (!(mine && live && ln.in)) top = 0.0;
-    for (int d = 1; d < min(16 * L, 64); d <<= 1) top = fmax(top, __shfl_xor(top, d));
+      for (int j = 0; j < 8; ++j) top = max(top, size_of(y[u][j]));
+    if (!(mine && live && ln.in)) top = 0;
+    for (int d = 1; d < min(16 * L, 64); d <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
     __syncthreads();
-    if ((threadIdx.x & (min(16 * L, 64) - 1)) == 0) atomicMax(&tops[hh], __builtin_bit_cast(unsigned long long, top));
+    if ((threadIdx.x & (min(16 * L, 64) - 1)) == 0) atomicMax(&tops[hh], top);
     __syncthreads();
-    top = __builtin_bit_cast(double, tops[hh]);
-    open.set(top < __builtin_inf() ? scale_byte(top) : 255);
+    open.set(scale_byte(tops[hh]));
     const int shift = open.shift();
     if (mine && ln.in) {
-      // times 2^(127 - byte), which f64 has
+      // times 2^(127 - byte), exactly; the sum with 3 2^51 is rounded to the nearest whole number, in its low bits
       const double f = ldexp(1.0, 127 - open.byte);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -408,10 +416,10 @@ __global__ __launch_bounds__(kThreads, MODE == kHalvesLds ? 2 : 3) void kv_appen
           uint32_t d[2] = {0, 0};
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int q = open.byte == 255 ? 0 : static_cast<int>(rint(y[u][j] * f));
-            d[j / 4] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * (j & 3));
+            const uint32_t q = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, __builtin_fma(y[u][j], f, 0x1.8p52)));
+            d[j / 4] |= (q & 0xFFu) << (8 * (j & 3));
           }
-          *place = make_uint2(d[0], d[1]);
+          *place = open.byte == 255 ? make_uint2(0, 0) : make_uint2(d[0], d[1]);
         } else if (tok < open.had && shift > 0) {
           const uint2 d = *place;
           *place = make_uint2(coarser(d.x, shift), coarser(d.y, shift));
