@@ -11,11 +11,10 @@
 // scaling by a power of two is exact.  Query rows, rounded to 24 or 8 bits, go
 // in f32.
 //
-// Bound: memory; 12000 tokens of 32 + 8 heads of 128, norm and rotation of halves:
-// bf16 68 us (33 of them the cache's part; queries alone cannot do without 38),
-// neighbours 85, f32 114; read back 15.  One token 5.9 us, a chain of loads: sequence,
-// page, scale and codes.  With four waves a SIMD asked for 101 instead of 84: the
-// rows' registers spill.
+// Bound: memory for queries, the codes' arithmetic beside it for keys and values;
+// 12000 tokens of 32 + 8 heads of 128, norm and rotation of halves: bf16 61 us (26 of
+// them the cache's part; queries alone cannot do without 38), neighbours 76, f32 113;
+// read back 15.  One token 5.9 us, a chain of loads: sequence, page, scale and codes.
 //
 // A block of a head has one owner, so nothing is shared between
 // workgroups, and a block's scale is written by who writes its codes; keys, values
@@ -23,7 +22,7 @@
 // D / 16 lanes (rounded up to a power of two) of 16 columns, two runs of 8 that are
 // rotated with each other where the halves' distance allows it; they keep their
 // angles and gains over the heads that their workgroup has.  Four value columns of
-// a block belong to a lane, which turns them in registers, 16 tokens a column.
+// a block belong to a lane, 16 tokens a column, so that turning them costs nothing.
 #include <type_traits>
 
 #include "kv_device.hpp"
@@ -301,23 +300,19 @@ __global__ __launch_bounds__(kThreads, MODE == kHalvesLds ? 2 : 3) void kv_appen
     const int h = static_cast<int>(group - p.key_groups) * each + hh;
     const bool mine = hh < each && h < Hk;
     if (threadIdx.x < kThreads / 4) value_tops[threadIdx.x] = 0;
-    float x[kKvBlock][4];
-    uint32_t top = 0;
+    using Raw = std::conditional_t<BF16, uint2, uint4>;   // four columns of a token
+    Raw x[kKvBlock];
 #pragma unroll
     for (int k = 0; k < kKvBlock; ++k) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[k][i] = 0.0f;
+      x[k] = Raw{};
       if (k < open.had || k >= open.have || !mine) continue;
       const int64_t i0 = (row0 + k) * a.v_t + h * a.v_h + c;
-      if constexpr (BF16) {
-        const uint2 r = load_any<uint2>(static_cast<const uint16_t *>(a.v) + i0);
-        x[k][0] = __uint_as_float(r.x << 16), x[k][1] = __uint_as_float(r.x & 0xFFFF0000u);
-        x[k][2] = __uint_as_float(r.y << 16), x[k][3] = __uint_as_float(r.y & 0xFFFF0000u);
-      } else {
-        const float4 r = load_any<float4>(static_cast<const float *>(a.v) + i0);
-        x[k][0] = r.x, x[k][1] = r.y, x[k][2] = r.z, x[k][3] = r.w;
-      }
+      x[k] = load_any<Raw>(static_cast<const char *>(a.v) + i0 * (BF16 ? 2 : 4));
     }
+    auto value = [&](int k, int i) {   // bits of an f32
+      if constexpr (BF16) return (i < 2 ? x[k].x : x[k].y) << (i & 1 ? 0 : 16) & 0xFFFF0000u;
+      else return i == 0 ? x[k].x : i == 1 ? x[k].y : i == 2 ? x[k].z : x[k].w;
+    };
     if (block0 < 0) return;
     const int64_t at = block0 + (static_cast<int64_t>(mine ? h : 0) << a.pool.page_blocks_log2);
     uint4 codes[4] = {};
@@ -327,39 +322,33 @@ __global__ __launch_bounds__(kThreads, MODE == kHalvesLds ? 2 : 3) void kv_appen
 #pragma unroll
         for (int i = 0; i < 4; ++i) codes[i] = load16(a.pool.v + at * unit + (c + i) * 16);
     }
+    uint32_t top = 0;   // magnitudes order as their bits; NaN and infinity come last
 #pragma unroll
     for (int k = 0; k < kKvBlock; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[k][i]) & 0x7FFFFFFFu);   // NaN and infinity come last
+      for (int i = 0; i < 4; ++i) top = max(top, value(k, i) & 0x7FFFFFFFu);
     __syncthreads();
     if (mine) atomicMax(&value_tops[hh], top);
     __syncthreads();
     if (!mine) return;
     top = value_tops[hh];
     open.set(scale_byte(size_of(static_cast<double>(__uint_as_float(top)))));
-    // x / 2^e in two exact factors, since one could pass the range
-    const int n = 127 - open.byte;
-    const float f0 = ldexpf(1.0f, n / 2), f1 = open.byte == 255 ? 0.0f : ldexpf(1.0f, n - n / 2);
+    // x / 2^e, which the sum with 3 2^22 rounds to the nearest whole number, in its low bits
+    const float f = ldexpf(1.0f, 127 - open.byte);
     const int shift = open.shift();
 #pragma unroll
     for (int k = 0; k < kKvBlock; k += 4) {
-      uint32_t words[4], columns[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {       // a token's four columns
-        words[m] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int q = open.byte == 255 ? 0 : static_cast<int>(rintf(x[k + m][i] * f0 * f1));
-          words[m] |= (static_cast<uint32_t>(q) & 0xFFu) << (8 * i);
-        }
-      }
-      turn4(words, columns);
       const int had = min(max(open.had - k, 0), 4);   // bytes of these words that the block has
       const uint32_t mask = had == 4 ? ~0u : (1u << (8 * had)) - 1;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        uint32_t q[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) q[m] = __float_as_uint(__builtin_fmaf(__uint_as_float(value(k + m, i)), f, 0x1.8p23f));
+        uint32_t w = perm_b32(perm_b32(q[3], q[2], 0x0C0C0400u), perm_b32(q[1], q[0], 0x0C0C0400u), 0x05040100u);
+        if (open.byte == 255) w = 0;
         uint32_t &o = k == 0 ? codes[i].x : k == 4 ? codes[i].y : k == 8 ? codes[i].z : codes[i].w;
-        o = (columns[i] & ~mask) | ((shift > 0 ? coarser(o, shift) : o) & mask);
+        o = open.had ? (w & ~mask) | ((shift > 0 ? coarser(o, shift) : o) & mask) : w;
       }
     }
 #pragma unroll
