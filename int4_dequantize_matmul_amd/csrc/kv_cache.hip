@@ -115,7 +115,13 @@ struct Lane {
       if (rotated) load8<false>(cs, c[0], co[0]), load8<false>(sn, c[0], si[0]);
     } else {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        if (MODE == kNeighbours && c[u] + 8 <= R) {
+          const float4 f = load_any<float4>(cs + c[u] / 2), h = load_any<float4>(sn + c[u] / 2);
+          co[u][0] = f.x, co[u][1] = f.y, co[u][2] = f.z, co[u][3] = f.w;
+          si[u][0] = h.x, si[u][1] = h.y, si[u][2] = h.z, si[u][3] = h.w;
+          continue;
+        }
 #pragma unroll
         for (int j = 0; j < (MODE == kNeighbours ? 4 : 8); ++j) {
           const int col = c[u] + (MODE == kNeighbours ? 2 * j : j);
@@ -123,6 +129,7 @@ struct Lane {
           const int i = MODE == kNeighbours ? col / 2 : col < R / 2 ? col : col - R / 2;
           co[u][j] = cs[i], si[u][j] = sn[i];
         }
+      }
     }
     if (!known) {
 #pragma unroll
@@ -152,7 +159,7 @@ struct Lane {
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          if (c[u] + j >= R) break;
+          if (c[u] + 8 > R && c[u] + j >= R) break;
           const real p = y[u][j], q = y[u][j + 1], cj = co[u][j / 2], sj = si[u][j / 2];
           y[u][j] = __builtin_elementwise_fma(p, cj, -(q * sj));
           y[u][j + 1] = __builtin_elementwise_fma(q, cj, p * sj);
