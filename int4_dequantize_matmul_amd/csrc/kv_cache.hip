@@ -13,14 +13,16 @@
 //
 // Bound: memory for queries, the codes' arithmetic beside it for keys and values;
 // 12000 tokens of 32 + 8 heads of 128, norm and rotation of halves: bf16 61 us (26 of
-// them the cache's part; queries alone cannot do without 38), neighbours 76, f32 113;
+// them the cache's part; queries alone cannot do without 38), neighbours 65, f32 113;
 // read back 15.  One token 5.9 us, a chain of loads: sequence, page, scale and codes.
 //
 // A block of a head has one owner, so nothing is shared between
 // workgroups, and a block's scale is written by who writes its codes; keys, values
 // and queries are workgroups of their own.  A row of a query or key head belongs to
-// D / 16 lanes (rounded up to a power of two) of 16 columns, two runs of 8 that are
-// rotated with each other where the halves' distance allows it; they keep their
+// D / 16 lanes (rounded up to a power of two) of 16 columns, two runs of 8, one in
+// each half of the columns, that are rotated with each other where the halves'
+// distance allows it (16 in a row, whose 16-byte pieces lie 64 bytes apart: f32
+// neighbours 128 us, not 112); they keep their
 // angles and gains over the heads that their workgroup has.  Four value columns of
 // a block belong to a lane, 16 tokens a column, so that turning them costs nothing.
 #include <type_traits>
@@ -95,8 +97,10 @@ struct Lane {
     const int D = static_cast<int>(a.pool.D), R = static_cast<int>(a.R);
     in = p < D / 16;
     rotated = MODE == kHalves && p < R / 16;
-    c[0] = rotated ? 8 * p : 16 * p;
-    c[1] = rotated ? 8 * p + R / 2 : 16 * p + 8;
+    // runs of neighbouring lanes are neighbours, in the first half of the columns and in the second
+    const int from = MODE == kHalves && !rotated ? R : 0, all = MODE != kHalves ? D : rotated ? R : D - R;
+    c[0] = from + 8 * p - from / 2;
+    c[1] = c[0] + all / 2;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (!a.norm || !gain || !in) {
@@ -159,7 +163,7 @@ struct Lane {
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          if (c[u] + 8 > R && c[u] + j >= R) break;
+          if (c[u] + j >= R) break;
           const real p = y[u][j], q = y[u][j + 1], cj = co[u][j / 2], sj = si[u][j / 2];
           y[u][j] = __builtin_elementwise_fma(p, cj, -(q * sj));
           y[u][j + 1] = __builtin_elementwise_fma(q, cj, p * sj);
