@@ -14,7 +14,7 @@
 // Bound: memory for queries, the codes' arithmetic beside it for keys and values;
 // 12000 tokens of 32 + 8 heads of 128, norm and rotation of halves: bf16 61 us (26 of
 // them the cache's part; queries alone cannot do without 38), neighbours 65, f32 113;
-// read back 15.  One token 5.9 us, a chain of loads: sequence, page, scale and codes.
+// read back 15.  One token 5.4 us, a chain of loads: sequence, page, scale and codes.
 //
 // A block of a head has one owner, so nothing is shared between
 // workgroups, and a block's scale is written by who writes its codes; keys, values
