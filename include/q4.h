@@ -490,6 +490,10 @@ size_t q8_attention_workspace(int64_t T, int64_t sequences, int64_t Hq, int64_t 
  * in itself, a key or a value, is NaN.  What a row does not see does not touch
  * it.  A row's result depends on the split of the keys, so on T, sequences and
  * max_len, to its rounding.
+ * Few rows take the decode kernel (Q4_PATH_GEMV), many rows of D up to 128 (f32
+ * queries or results: 64) LDS tiles of 256 rows (Q4_PATH_TILED), by a measured
+ * rule; q4_set_path forces either where it can run.  The other calls on rows and
+ * caches have one route, and report Q4_PATH_GEMV.
  * EINVAL also for a scale that is not finite, window, sinks or max_len < 0, a
  * negative stride, a small or misaligned workspace, or an output overlapping an
  * input; ESHAPE also for Hq not a multiple of heads, T Hq or max_len beyond

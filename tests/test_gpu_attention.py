@@ -481,3 +481,21 @@ def test_joined_splits(D, xt, yt):
         q4.q8_attention(q, on_gpu(pool), dev(pages), i32(starts), i32(lengths), max_len=max_len, dtype=yt, ws=room[:need], y=y)
         check(y, q, pool, pages, starts, lengths, np.float32(D ** -0.5), what=max_len)
         assert (f64(y)[[0, 1, 7, 8]] == 77).all() and bool((room[need:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("xt,D,n,path,want", [
+    ("bf16", 128, 1, "auto", "gemv"), ("bf16", 128, 2048, "auto", "tiled"), ("bf16", 144, 2048, "auto", "gemv"),
+    ("f32", 64, 4096, "auto", "tiled"), ("f32", 96, 4096, "auto", "gemv"), ("bf16", 128, 2048, "gemv", "gemv"),
+    ("bf16", 128, 3, "tiled", "tiled"), ("f32", 80, 3, "tiled", "gemv"), ("bf16", 128, 3, "generic", "gemv")])
+def test_route(xt, D, n, path, want):
+    """What is reported, and the first and last row against the oracle."""
+    q4.q4_set_path(path)
+    rng = np.random.default_rng(16)
+    H, Hq = 8, 32
+    pages, P = new_pages(rng, [n + 40], 64)
+    pool = random_pool(rng, P, H, 64, D)
+    q = dev((3 * rng.standard_normal((n, Hq, D))).astype(np.float32)).to(TORCH[xt])
+    y = q4.q8_attention(q, on_gpu(pool), dev(pages), i32([0, n]), i32([n + 40]))
+    assert q4.q4_last_path() == want
+    for row in (0, n - 1):
+        check(y[row:row + 1], q[row:row + 1], pool, pages, [0, 1], [40 + row + 1], np.float32(D ** -0.5), what=row)
