@@ -16,15 +16,15 @@
 // them the cache's part; queries alone cannot do without 38), neighbours 65, f32 113;
 // read back 15.  One token 5.4 us, a chain of loads: sequence, page, scale and codes.
 //
-// A block of a head has one owner, so nothing is shared between
-// workgroups, and a block's scale is written by who writes its codes; keys, values
-// and queries are workgroups of their own.  A row of a query or key head belongs to
-// D / 16 lanes (rounded up to a power of two) of 16 columns, two runs of 8, one in
-// each half of the columns, that are rotated with each other where the halves'
-// distance allows it (16 in a row, whose 16-byte pieces lie 64 bytes apart: f32
-// neighbours 128 us, not 112); they keep their
-// angles and gains over the heads that their workgroup has.  Four value columns of
-// a block belong to a lane, 16 tokens a column, so that turning them costs nothing.
+// A block of a head has one owner, so nothing is shared between workgroups, and a
+// block's scale is written by who writes its codes; keys, values and queries are
+// workgroups of their own.  A row of a query or key head belongs to D / 16 lanes
+// (rounded up to a power of two) of 16 columns, two runs of 8, one in each half of
+// the columns, that are rotated with each other where the halves' distance allows it
+// (with 16 columns in a row the 16-byte pieces lie 64 bytes apart: f32 neighbours 128
+// us, not 112); they keep their angles and gains over the heads that their workgroup
+// has.  Four value columns of a block belong to a lane, 16 tokens a column, so that
+// turning them costs nothing.
 #include <type_traits>
 
 #include "kv_device.hpp"
