@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = 4, kRows = 16, kMaxSplits = 64;
 
-// Where the results begin behind a, b and l of `splits` parts of `all` rows, on 16 bytes.
+// Where the results begin behind a, d and l of `splits` parts of `all` rows, on 16 bytes.
 __host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { return (3 * splits * all + 3) / 4 * 4; }
 
 // Few rows a sequence: a workgroup has 16 rows of one key head and a share of
@@ -40,13 +40,13 @@ __host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { 
 // 5.1 TB/s; 64 tokens of up to 8192 keys (462 MB) 97 us, 4.8 TB/s.  By the chain of
 // loads (sequence, page, scales, codes) and the launch for short ones: 16 keys 7 us
 // with the call.  Eight waves a workgroup take one more and, as a CU then has one
-// workgroup, twice the time with many sequences (64 of 64 keys 16.6 us against 8.6).  parts: a, b, l
+// workgroup, twice the time with many sequences (64 of 64 keys 16.6 us against 8.6).  parts: a, d, l
 // and results of splits x rows for combine_kernel, or null with one split.
 template <int NV, bool TWO>   // 16 NV columns
 __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Types types, int splits,
                                                                                  float *parts, uint32_t first) {
   constexpr int NS = (NV + 3) / 4, D = 16 * NV;
-  __shared__ float as[kWaves][kRows], bs[kWaves][kRows], ls[kWaves][kRows];
+  __shared__ float as[kWaves][kRows], ds[kWaves][kRows], ls[kWaves][kRows];
   __shared__ __attribute__((aligned(16))) float meet[kWaves - 1][kRows][D + 4];
   const uint32_t Hk = static_cast<uint32_t>(a.pool.Hk), G = static_cast<uint32_t>(a.G);
   const int split = static_cast<int>(blockIdx.x % splits);
@@ -170,14 +170,17 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
 
   // the four waves' parts relative to the same powers, then their sums in order, by the first wave
   st.l = row_sum<4>(st.l);
-  if (q4 == 0) as[wave][c] = st.a, bs[wave][c] = st.b, ls[wave][c] = st.l;
+  if (q4 == 0) as[wave][c] = st.a, ds[wave][c] = st.d, ls[wave][c] = st.l;
   __syncthreads();
-  float ma = as[0][c], mb = bs[0][c], l = 0.0f;
+  float ma = as[0][c], md = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) ma = fmaxf(ma, as[w][c]), mb = fmaxf(mb, bs[w][c]);
+  for (int w = 1; w < kWaves; ++w) ma = fmaxf(ma, as[w][c]);
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) l += ls[w][c] * rescale(as[w][c], ls[w][c], ma);
-  const float f = rescale(st.b, st.l, mb);
+  for (int w = 0; w < kWaves; ++w) {
+    md = fmaxf(md, lag(as[w][c], ds[w][c], ma));
+    l += ls[w][c] * rescale(as[w][c], ls[w][c], ma);
+  }
+  const float f = rescale(st.a, st.d, st.l, ma, md);
 #pragma unroll
   for (int d = 0; d < NV; ++d) st.y[d] *= f;
   if (wave > 0 && c < rows) {
@@ -186,7 +189,7 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
   }
   __syncthreads();
   if (wave > 0 || c >= rows) return;
-  const Quotient quotient(ma, mb, l, decltype(st)::kOffset);
+  const Quotient quotient(md, l, decltype(st)::kOffset);
   const int64_t all = a.seqs.T * a.Hq, out = row * a.Hq + qh;
 #pragma unroll
   for (int d = 0; d < NV; ++d) {
@@ -201,7 +204,7 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
   }
   if (parts && q4 == 0) {
     parts[split * all + out] = ma;
-    parts[(splits + split) * all + out] = mb;
+    parts[(splits + split) * all + out] = md;
     parts[(2 * splits + split) * all + out] = l;
   }
 }
@@ -210,42 +213,54 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
 // splits out and meet in LDS, in a fixed order; as many rows a workgroup as fit.
 __global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types types, int offset, int splits, int groups,
                                                            int rows, const float *parts, int64_t first) {
-  __shared__ float as[kMaxSplits], bs[kMaxSplits], ls[kMaxSplits];   // rows x splits, at most
+  // rows x splits, at most: a split's factor and its part of l, and its row's d
+  __shared__ float factors[kMaxSplits], terms[kMaxSplits], ds[kMaxSplits];
   __shared__ f32x4 sums[kThreads];
+  __shared__ float ls[kThreads];
   const int64_t all = a.seqs.T * a.Hq, out0 = first + blockIdx.x * static_cast<int64_t>(rows);
   const int D = static_cast<int>(a.pool.D), quads = D / 4, each = quads * groups;
   const int64_t from = Sequence::clamp(a.seqs.starts[0], a.seqs.T) * a.Hq;
   const int64_t to = Sequence::clamp(a.seqs.starts[a.seqs.N], a.seqs.T) * a.Hq;
-  if (static_cast<int>(threadIdx.x) < rows * splits) {
-    const int64_t out = out0 + threadIdx.x / splits, s = threadIdx.x % splits;
-    if (out < all) {
-      as[threadIdx.x] = parts[s * all + out];
-      bs[threadIdx.x] = parts[(splits + s) * all + out];
-      ls[threadIdx.x] = parts[(2 * splits + s) * all + out];
-    }
+  if (threadIdx.x < kMaxSplits) {   // the first wave: a split a lane
+    const int lane = threadIdx.x, row = lane / splits, s = lane - row * splits;
+    const int64_t out = out0 + row;
+    const bool has = row < rows && out < all;
+    const float a1 = has ? parts[s * all + out] : -__builtin_inff(), d1 = has ? parts[(splits + s) * all + out] : 0.0f;
+    const float l1 = has ? parts[(2 * splits + s) * all + out] : 0.0f;
+    // the largest of the row's splits: of 2, 4, 8, ... from each one on, round and round
+    auto row_max = [&](float v) {
+      for (int n = 1; n < splits; n *= 2) {
+        const int at = s + n < splits ? lane + n : lane + n - splits;
+        v = fmaxf(v, __shfl(v, at));
+      }
+      return v;
+    };
+    const float ma = row_max(a1), md = row_max(lag(a1, d1, ma));
+    factors[lane] = rescale(a1, d1, l1, ma, md);
+    terms[lane] = l1 * rescale(a1, l1, ma);
+    ds[lane] = md;
   }
   __syncthreads();
   const int r = threadIdx.x / each, x = threadIdx.x - r * each, g = x / quads, col = 4 * (x - g * quads);
   const int64_t out = out0 + r;
   // rows in front of the first sequence or behind the last are left as they were
   const bool live = r < rows && out >= from && out < to;
-  const float *ra = as + r * splits, *rb = bs + r * splits, *rl = ls + r * splits;
-  float ma = -__builtin_inff(), mb = ma, l = 0.0f;
+  float l = 0.0f;
   f32x4 sum = {};
   if (live) {
-    for (int s = 0; s < splits; ++s) ma = fmaxf(ma, ra[s]), mb = fmaxf(mb, rb[s]);
-    for (int s = 0; s < splits; ++s) l = fmaf(rl[s], rescale(ra[s], rl[s], ma), l);
 #pragma unroll 4
     for (int s = g; s < splits; s += groups) {
       const f32x4 o = *reinterpret_cast<const f32x4 *>(parts + results_at(splits, all) + (s * all + out) * D + col);
-      sum += o * rescale(rb[s], rl[s], mb);
+      sum += o * factors[r * splits + s];
+      l += terms[r * splits + s];
     }
   }
   sums[threadIdx.x] = sum;
+  ls[threadIdx.x] = l;
   __syncthreads();
   if (!live || g > 0) return;
-  for (int i = 1; i < groups; ++i) sum += sums[threadIdx.x + i * quads];
-  const Quotient q(ma, mb, l, offset);
+  for (int i = 1; i < groups; ++i) sum += sums[threadIdx.x + i * quads], l += ls[threadIdx.x + i * quads];
+  const Quotient q(ds[r * splits], l, offset);
   store4(a.y, types.out_bf16, out * D + col, q(sum[0]), q(sum[1]), q(sum[2]), q(sum[3]));
 }
 

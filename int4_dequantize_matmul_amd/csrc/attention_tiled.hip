@@ -223,7 +223,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 4) void attention_tiled_kerne
     if (!second) lds_barrier();
   }
 
-  const Quotient quotient(st.a, st.b, add_xor32(st.l), decltype(st)::kOffset);
+  const Quotient quotient(st.d, add_xor32(st.l), decltype(st)::kOffset);
   if (c >= rows) return;
   const int64_t out = (row * a.Hq + qh) * D;
 #pragma unroll

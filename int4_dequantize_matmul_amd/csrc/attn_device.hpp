@@ -176,21 +176,24 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // Running softmax of one query row a lane, which S lanes share (2 or 4), each with
-// the scores of one block of 16 keys a step.  Scores
-// are in powers of two; `a` and `b` are whole numbers: l is this lane's sum of
-// weights 2^(s - a); y holds the results, sums of 2^(s + e - b + kOffset) times
+// the scores of one block of 16 keys a step.  Scores s
+// are in powers of two; `a` and `d` are whole numbers: l is this lane's sum of
+// weights 2^(s - a); y holds the results, sums of 2^(s - a + e - d + kOffset) times
 // codes, e the exponent of their values' scale.  So the weights that meet the
 // codes are rounded next to the largest product of a weight and its values'
-// scale, whatever the scales are.  No maximum is taken as long as the weights
+// scale, whatever the scales are.  `a` is as large as scores come; e, d and
+// kOffset stay below 2^9 and are never added to a sum that would round them away.
+// No maximum is taken as long as the weights
 // stay halves: their sum, which is needed anyway, tells.
 template <class V, int N, int S, bool TWO>   // N vectors of results
 struct State {
   static constexpr int kOffset = TWO ? 10 : 9;
-  float a = -__builtin_inff(), b = -__builtin_inff(), l = 0.0f;
+  float a = -__builtin_inff(), d = -__builtin_inff(), l = 0.0f;
+  bool far = false;   // some row's `a` has few bits behind the point or none
   V y[N];
   __device__ __forceinline__ State() {
 #pragma unroll
-    for (int d = 0; d < N; ++d) y[d] = V{};
+    for (int i = 0; i < N; ++i) y[i] = V{};
   }
   // 16 keys of one block: scores x times f, then weights as operands.
   struct Keys {
@@ -211,15 +214,22 @@ struct State {
         f = 1.0f;
       }
     }
-    // Under the powers a and b.
-    __device__ __forceinline__ void weigh(float a, float b) {
+    // Under the powers a and d.
+    __device__ __forceinline__ void weigh(float a, float d, bool far) {
       // nothing seen so far: any finite number will do
-      const float fa = a == -__builtin_inff() ? 0.0f : a, fb = b == -__builtin_inff() ? 0.0f : b;
+      const float fa = a == -__builtin_inff() ? 0.0f : a, fd = d == -__builtin_inff() ? 0.0f : d;
       // weights of 2^-60 and less of what counts are 0 as halves; kept that large, their f32 sum stays right
-      shift = fmaxf(e + static_cast<float>(kOffset) - fb, -60.0f - fa);
+      shift = fmaxf(e + static_cast<float>(kOffset) - fd, -60.0f);
       float w[16];
+      if (__builtin_expect(far, 0)) {
+        // the same rounded products as in top(), whose differences from `a` are exact where they matter
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = exp2_fast(fmaf(x[j], f, shift));
+        for (int j = 0; j < 16; ++j) w[j] = exp2_fast((x[j] * f - fa) + shift);
+      } else {
+        const float both = shift - fa;   // exact below 2^22
+#pragma unroll
+        for (int j = 0; j < 16; ++j) w[j] = exp2_fast(fmaf(x[j], f, both));
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t q[4], r[4];
@@ -247,48 +257,57 @@ struct State {
   // The weights of the T blocks that this lane has; x: their scores.
   template <int T>
   __device__ __forceinline__ void weights(Keys (&x)[T]) {
-    bool again = b == -__builtin_inff();
+    bool again = d == -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-      x[i].weigh(a, b);
+      x[i].weigh(a, d, far);
       // too large for halves, or kept larger than they are; sums are that of T blocks at most
-      again |= x[i].sum > 32768.0f || x[i].shift <= -60.0f - a;
+      again |= x[i].sum > 32768.0f || x[i].shift <= -60.0f;
     }
     if (__any(again)) {
-      float ta = -__builtin_inff(), tb = ta;
+      float top[T], ta = -__builtin_inff(), td = ta;
 #pragma unroll
-      for (int i = 0; i < T; ++i) {
-        const float v = x[i].top();
-        ta = fmaxf(ta, v), tb = fmaxf(tb, v + x[i].e);
-      }
-      const float na = fmaxf(a, ceilf(row_max<S>(ta))), nb = fmaxf(b, ceilf(row_max<S>(tb)));
-      const float ga = a == na ? 1.0f : exp2_fast(a - na), gb = b == nb ? 1.0f : exp2_fast(b - nb);   // from -inf: 0
-      a = na, b = nb;
+      for (int i = 0; i < T; ++i) top[i] = x[i].top(), ta = fmaxf(ta, top[i]);
+      const float na = fmaxf(a, ceilf(row_max<S>(ta))), fa = na == -__builtin_inff() ? 0.0f : na;
+#pragma unroll
+      for (int i = 0; i < T; ++i) td = fmaxf(td, (top[i] - fa) + x[i].e);
+      // what was relative to a and d, relative to na
+      const float by = a == na ? 0.0f : a - na, nd = fmaxf(by + d, ceilf(row_max<S>(td)));
+      const float ga = exp2_fast(by), gd = by + d == nd ? 1.0f : exp2_fast(by + d - nd);   // from -inf: 0
+      a = na, d = nd, far = __any(fabsf(fa) > 0x1p22f);
       l *= ga;
 #pragma unroll
-      for (int d = 0; d < N; ++d) y[d] *= gb;
+      for (int i = 0; i < N; ++i) y[i] *= gd;
 #pragma unroll
-      for (int i = 0; i < T; ++i) x[i].weigh(a, b);
+      for (int i = 0; i < T; ++i) x[i].weigh(a, d, far);
     }
-    const float fa = a == -__builtin_inff() ? 0.0f : a;
 #pragma unroll
-    for (int i = 0; i < T; ++i) l = fmaf(x[i].sum, exp2_fast(-(x[i].shift + fa)), l);
+    for (int i = 0; i < T; ++i) l = fmaf(x[i].sum, exp2_fast(-x[i].shift), l);
   }
 };
 
-// What sums or results relative to 2^m count relative to 2^to; l is their sum of
-// weights: a part that saw nothing counts 0, one with NaN alone its NaN.
-__device__ __forceinline__ float rescale(float m, float l, float to) {
-  if (m == -__builtin_inff()) return l == 0.0f ? 0.0f : 1.0f;
-  return exp2_fast(m - to);
+// What a part's sum of weights relative to 2^a counts relative to 2^to, and its
+// results relative to 2^(a + d) relative to 2^(to + td); l is the part's sum: one that saw
+// nothing counts 0, one with NaN alone its NaN.
+__device__ __forceinline__ float rescale(float a, float l, float to) {
+  if (a == -__builtin_inff()) return l == 0.0f ? 0.0f : 1.0f;
+  return exp2_fast(a - to);
+}
+__device__ __forceinline__ float rescale(float a, float d, float l, float to, float td) {
+  if (a == -__builtin_inff()) return l == 0.0f ? 0.0f : 1.0f;
+  return exp2_fast((a - to) + d - td);
+}
+// A part's d relative to 2^to, the largest of the parts' a.
+__device__ __forceinline__ float lag(float a, float d, float to) {
+  return a == -__builtin_inff() ? a : (a - to) + d;
 }
 
 // Results over their sum of weights; a row that sees nothing is 0.
 struct Quotient {
   float n;
   int e;
-  __device__ __forceinline__ Quotient(float a, float b, float l, int offset)
-      : n(l == 0.0f ? 0.0f : 1.0f / l), e(b == -__builtin_inff() ? 0 : static_cast<int>(b - a) - offset) {}
+  __device__ __forceinline__ Quotient(float d, float l, int offset)
+      : n(l == 0.0f ? 0.0f : 1.0f / l), e(d == -__builtin_inff() ? 0 : static_cast<int>(d) - offset) {}
   __device__ __forceinline__ float operator()(float y) const { return ldexpf(y * n, e); }
 };
 
