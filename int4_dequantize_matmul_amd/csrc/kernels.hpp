@@ -171,6 +171,7 @@ struct NormArgs {
   int8_t *xq;
   float *sx;
   int64_t M, K;
+  double inv_K;
   float eps;
 };
 hipError_t launch_rmsnorm_rows(const NormArgs &a, bool bf16, hipStream_t st);

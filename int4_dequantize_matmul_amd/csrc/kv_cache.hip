@@ -67,14 +67,6 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// 1 / sqrt(x).  In f64 from the instruction's estimate (2^-23 at worst), with three
-// terms of the series in what is left of x y^2: to 2^-51 in 7 operations, not 40.
-__device__ __forceinline__ float inverse_root(float x) { return 1.0f / sqrtf(x); }
-__device__ __forceinline__ double inverse_root(double x) {
-  const double y = __builtin_amdgcn_rsq(x), h = __builtin_fma(-x * y, y, 1.0);
-  return __builtin_fma(y * h, __builtin_fma(0.375, h, 0.5), y);
-}
-
 // How a row's rotation meets its lanes.
 enum Rotation : int {
   kPlain = 0,        // none

@@ -854,7 +854,7 @@ extern "C" q4_status q8_rmsnorm_rows(const void *x, const void *residual, q4_dty
   if (M == 0) return Q4_OK;
   if (!device_ok()) return Q4_EDEVICE;
   if (K == 0) return finish(q4::launch_zero(sx, u(M) * 4, S(stream)), Q4_PATH_GENERIC);
-  const q4::NormArgs a = {x, residual, gain, gt == Q4_DT_BF16, sum, xq, sx, M, K, eps};
+  const q4::NormArgs a = {x, residual, gain, gt == Q4_DT_BF16, sum, xq, sx, M, K, 1.0 / K, eps};
   return finish(q4::launch_rmsnorm_rows(a, xt == Q4_DT_BF16, S(stream)), Q4_PATH_GEMV);
 }
 

@@ -165,6 +165,15 @@ __device__ __forceinline__ int dpp_row_sum_i32(int v) {
   return v;
 }
 
+// 1 / sqrt(x).  In f64, 0 < x < infinity: from the instruction's estimate (2^-23 at
+// worst), with three terms of the series in what is left of x y^2: to 2^-51 in 7
+// operations, not 40.
+__device__ __forceinline__ float inverse_root(float x) { return 1.0f / sqrtf(x); }
+__device__ __forceinline__ double inverse_root(double x) {
+  const double y = __builtin_amdgcn_rsq(x), h = __builtin_fma(-x * y, y, 1.0);
+  return __builtin_fma(y * h, __builtin_fma(0.375, h, 0.5), y);
+}
+
 __device__ __forceinline__ uint4 load16(const void *p) {
   return *reinterpret_cast<const uint4 *>(p);
 }

@@ -4,19 +4,28 @@
 //   code = rint(127 y / max|y|) = rint(127 u / max|u|),  scale = max|y| / 127
 // The root cancels out of the codes, so they need nothing that is summed: they
 // are the nearest ones of the exact quotients (ties to even, up to a sum x + r
-// past 53 bits), on every route.  Sums and products go in f32; an element whose
+// past 53 bits), on every route.  h and products go in f32; an element whose
 // f32 quotient, off by at most 6 roundings of 2^-24, lies next to a border is
-// divided again in f64, as is the maximum formed.
+// divided again in f64, as is the maximum formed.  No square meets more than 20
+// roundings of the sum, which goes by runs of 8 columns, lanes and waves (runs of a
+// row that is read again are added in f64), so a scale is within 12 steps of 2^-24.
+// Where eps does not make up for squares that f32 loses (they end at steps of 2^-149),
+// rows that have such are summed once more, times 2^100.
 //
 // Bound: memory; x and r are read, the sum and the codes written once.  A row
 // stays in the registers of one to 16 waves, 8 columns a lane at a time; rows of
 // more than 16384 columns are read three times.  8192 rows of 2048 with residual:
 // bf16 28 us (4.2 TB/s), f32 35 us (6.2 TB/s, partly from the last-level cache).
+#include <type_traits>
+
 #include "kernels.hpp"
 #include "mx_device.hpp"
 
 namespace q4 {
 namespace {
+
+// Below this a sum of squares, with eps for each, may lack what f32 lost: at most 2^30 times 2^-149.
+constexpr float kSmall = 0x1p-90f;
 
 template <bool BF16>
 __device__ __forceinline__ float at(const Run8<BF16> &r, int j) {
@@ -43,9 +52,15 @@ __device__ __forceinline__ void join(float &ss, uint32_t &top, float *sums, uint
   if constexpr (W > 1) {
     if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = ss, tops[threadIdx.x >> 6] = top;
     __syncthreads();
-    ss = 0.0f, top = 0;
+    float s[W];
+    top = 0;
 #pragma unroll
-    for (int i = 0; i < W; ++i) ss += sums[i], top = max(top, tops[i]);
+    for (int i = 0; i < W; ++i) s[i] = sums[i], top = max(top, tops[i]);
+#pragma unroll
+    for (int n = W / 2; n > 0; n /= 2)
+#pragma unroll
+      for (int i = 0; i < n; ++i) s[i] += s[i + n];
+    ss = s[0];
   }
 }
 
@@ -73,8 +88,9 @@ __device__ __forceinline__ double join(double m, double *tops) {
 }
 
 // W waves a row; RUNS times 8 columns a lane in registers, or 0 for rows that
-// are read again.
-template <bool BF16, int W, int RUNS>
+// are read again; SMALL: eps may leave squares that f32 loses to count (a kernel of
+// its own, since the second sum takes 8 registers: 8192 rows of 2048 in bf16 29 us, not 28).
+template <bool BF16, int W, int RUNS, bool SMALL>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_rows_kernel(NormArgs a, int64_t first) {
   __shared__ float sums[W];
   __shared__ uint32_t tops[W];
@@ -125,17 +141,46 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_rows_kernel(Nor
     for (int i = 0; i < RUNS; ++i) load(i, int64_t(i) * step + tid * 8);
   }
 
-  float ss = 0.0f;
+  std::conditional_t<RUNS == 0, double, float> lane_ss = 0;
   uint32_t top = 0;
   each([&](int i, int64_t) {
+    float run = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float h = at(x[i], j) + at(r[i], j);
-      ss = fmaf(h, h, ss);
+      run = fmaf(h, h, run);
       top = max(top, magnitude(h * g[i][j]));
     }
+    lane_ss += run;
   });
+  float ss = static_cast<float>(lane_ss);
   join<W>(ss, top, sums, tops);
+  bool scaled = false;
+  if constexpr (SMALL) {
+    scaled = fmaf(static_cast<float>(K), a.eps, ss) < kSmall;   // the same in every wave
+    if (scaled) {
+      if constexpr (W > 1) __syncthreads();   // all have read the sums
+      lane_ss = 0;
+      each([&](int i, int64_t) {
+        float run = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float h = (at(x[i], j) + at(r[i], j)) * 0x1p100f;
+          run = fmaf(h, h, run);
+        }
+        lane_ss += run;
+      });
+      ss = static_cast<float>(lane_ss);
+      join<W>(ss, top, sums, tops);
+    }
+    // sums and products are formed again, not kept in registers (an instruction it is not)
+    if constexpr (RUNS > 0) {
+#pragma unroll
+      for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+        for (int j = 0; j < (BF16 ? 4 : 8); ++j) asm("" : "+v"(x[i].v[j]));
+    }
+  }
   const bool bad = top >= 0x7F800000u || !(ss < __builtin_inff());
 
   // max|u| in f64, from the elements whose f32 product is within its roundings of the largest
@@ -147,9 +192,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_rows_kernel(Nor
       if (magnitude(product(i, j)) >= near_top) m64 = fmax(m64, fabs(product64(i, j)));
   });
   m64 = join<W>(m64, tops64);
-  if (tid == 0)
-    a.sx[m] = bad ? __builtin_nanf("")
-                  : static_cast<float>(m64) * (1.0f / sqrtf(ss / static_cast<float>(K) + a.eps)) / 127.0f;
+  if (tid == 0) {
+    const double mean = (scaled ? ss * 0x1p-200 : static_cast<double>(ss)) * a.inv_K + static_cast<double>(a.eps);
+    const double root = mean < __builtin_inf() ? inverse_root(mean) : 0.0;
+    a.sx[m] = bad ? __builtin_nanf("") : static_cast<float>(m64 * root * (1.0 / 127.0));
+  }
 
   const float f = __uint_as_float(top);
   const bool small = f < 0x1p-100f;   // subnormal products, or 127 / f past the range
@@ -214,13 +261,13 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_rows_kernel(Nor
   });
 }
 
-template <bool BF16, int W, int RUNS>
+template <bool BF16, int W, int RUNS, bool SMALL>
 void go(const NormArgs &a, hipStream_t st) {
   constexpr int threads = W == 1 ? 256 : 64 * W, rows = W == 1 ? 4 : 1;
   const int64_t most = rows * max_groups(threads);
   for (int64_t first = 0; first < a.M; first += most) {   // rows of a launch
     const int64_t n = a.M - first < most ? a.M - first : most;
-    rmsnorm_rows_kernel<BF16, W, RUNS><<<static_cast<unsigned>((n + rows - 1) / rows), threads, 0, st>>>(a, first);
+    rmsnorm_rows_kernel<BF16, W, RUNS, SMALL><<<static_cast<unsigned>((n + rows - 1) / rows), threads, 0, st>>>(a, first);
   }
 }
 
@@ -229,23 +276,25 @@ void go(const NormArgs &a, hipStream_t st) {
 // waves of one run 28 us, one wave of four 36; 4096 of 5632: four waves of three runs
 // 39, of four 52, eight waves of two 43; 2048 of 13312: 16 waves of two 58, four that
 // read their rows again 60; one row of 13312 6.5 against 14).
-template <bool BF16>
+template <bool BF16, bool SMALL>
 void pick(const NormArgs &a, hipStream_t st) {
   const int64_t runs = (a.K + 7) / 8;
-  if (runs <= 64) go<BF16, 1, 1>(a, st);
-  else if (runs <= 128) go<BF16, 2, 1>(a, st);
-  else if (runs <= 256) go<BF16, 4, 1>(a, st);
-  else if (runs <= 512) go<BF16, 4, 2>(a, st);
-  else if (runs <= 768) go<BF16, 4, 3>(a, st);
-  else if (runs <= 1024) go<BF16, 8, 2>(a, st);
-  else if (runs <= 2048) go<BF16, 16, 2>(a, st);
-  else go<BF16, 16, 0>(a, st);
+  if (runs <= 64) go<BF16, 1, 1, SMALL>(a, st);
+  else if (runs <= 128) go<BF16, 2, 1, SMALL>(a, st);
+  else if (runs <= 256) go<BF16, 4, 1, SMALL>(a, st);
+  else if (runs <= 512) go<BF16, 4, 2, SMALL>(a, st);
+  else if (runs <= 768) go<BF16, 4, 3, SMALL>(a, st);
+  else if (runs <= 1024) go<BF16, 8, 2, SMALL>(a, st);
+  else if (runs <= 2048) go<BF16, 16, 2, SMALL>(a, st);
+  else go<BF16, 16, 0, SMALL>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_rmsnorm_rows(const NormArgs &a, bool bf16, hipStream_t st) {
-  bf16 ? pick<true>(a, st) : pick<false>(a, st);
+  const bool small = static_cast<double>(a.K) * a.eps < 2 * kSmall;
+  if (bf16) small ? pick<true, true>(a, st) : pick<true, false>(a, st);
+  else small ? pick<false, true>(a, st) : pick<false, false>(a, st);
   return hipGetLastError();
 }
 

@@ -1,0 +1,45 @@
+"""Scales of q8_rmsnorm_rows over the whole range of rows: within 1e-6 of the
+float64 oracle's (a square meets at most 19 roundings of the sum and twice its own
+number's, each half a step of 2^-23, and the root halves them: 10.5 of 2^-24, with
+the result's own 12, 7.2e-7), codes bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import int4_dequantize_matmul_amd as q4
+import oracle.serving as S
+from tests.gpu_util import DEV, assert_bitwise, dev, host
+from tests.test_gpu_rmsnorm_rows import TORCH, f64
+
+pytestmark = pytest.mark.gpu
+WIDTHS = [40, 757, 1000, 2048, 4000, 6000, 8000, 16000, 16392]   # one to 16 waves, in registers and read again
+
+
+def check(x, gain, residual, eps, what):
+    codes, scales, _ = q4.q8_rmsnorm_rows(x, gain, residual, eps)
+    ref, sref, _ = S.rmsnorm_rows(f64(x), f64(residual), f64(gain), np.float64(np.float32(eps)))
+    assert_bitwise(host(codes), ref, what)
+    got = host(scales).astype(np.float64)
+    # f32 ends at steps of 2^-149
+    assert np.all(np.abs(got - sref) <= 1e-6 * np.abs(sref) + 2.0 ** -149), (what, got[:4], sref[:4])
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", WIDTHS)
+def test_small_and_large_rows_without_eps(K, xt):
+    """Squares far below the range of f32, and as near its end as the sum may come."""
+    rng = np.random.default_rng(K)
+    for power in (-120, -100, -80, -75, -70, -66, -60, 0, 50, 55):
+        x, r = (dev((rng.standard_normal((3, K)) * 2.0 ** power).astype(np.float32)).to(TORCH[xt]) for _ in range(2))
+        g = dev((1 + 0.2 * rng.standard_normal(K)).astype(np.float32))
+        check(x, g, r, 0.0, f"2^{power}")
+        check(x, None, None, 1e-30, f"2^{power} with a small eps")
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [2 ** 14, 2 ** 17, 2 ** 20, 2 ** 24])
+def test_long_rows(K, xt):
+    """Constant rows, whose roundings all go one way."""
+    x = torch.full((1, K), 1.3, device=DEV).to(TORCH[xt])
+    x[0, 5] = 2.6
+    check(x, None, None, 1e-6, "constant")
