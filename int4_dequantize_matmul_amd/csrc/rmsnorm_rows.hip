@@ -183,9 +183,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_rows_kernel(Nor
   }
   const bool bad = top >= 0x7F800000u || !(ss < __builtin_inff());
 
-  // max|u| in f64, from the elements whose f32 product is within its roundings of the largest
+  // max|u| in f64, from the elements whose f32 product is within its roundings of the largest (of all where that is
+  // next to nothing: products below the range of f32 are not 0)
   double m64 = 0.0;
-  const uint32_t near_top = top > 8 ? top - 8 : 1;
+  const uint32_t near_top = top > 8 ? top - 8 : 0;
   each([&](int i, int64_t) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_rows_kernel(Nor
   if (tid == 0) {
     const double mean = (scaled ? ss * 0x1p-200 : static_cast<double>(ss)) * a.inv_K + static_cast<double>(a.eps);
     const double root = mean < __builtin_inf() ? inverse_root(mean) : 0.0;
-    a.sx[m] = bad ? __builtin_nanf("") : static_cast<float>(m64 * root * (1.0 / 127.0));
+    a.sx[m] = bad ? __builtin_nanf("") : m64 == 0.0 ? 0.0f : static_cast<float>(m64 * root * (1.0 / 127.0));
   }
 
   const float f = __uint_as_float(top);
@@ -240,7 +241,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_rows_kernel(Nor
       near |= fabsf(t - q) > 0.4998f;
       code[j] = static_cast<int>(q);
     }
-    if (bad || top == 0) {
+    if (bad || m64 == 0.0) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) code[j] = 0;
     } else if (near) {

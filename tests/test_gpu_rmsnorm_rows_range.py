@@ -36,6 +36,29 @@ def test_small_and_large_rows_without_eps(K, xt):
         check(x, None, None, 1e-30, f"2^{power} with a small eps")
 
 
+@pytest.mark.parametrize("K", WIDTHS)
+def test_products_below_the_range(K):
+    """Rows times gains that are 0 or subnormal in f32: not rows of zeros."""
+    rng = np.random.default_rng(K)
+    x = dev((rng.standard_normal((2, K)) * 2.0 ** -90).astype(np.float32))
+    for power in (-75, -58, -50):
+        g = dev((rng.standard_normal(K) * 2.0 ** power).astype(np.float32))
+        check(x, g, None, 0.0, f"gain 2^{power}")
+
+
+@pytest.mark.parametrize("K", WIDTHS)
+def test_rows_of_zeros_without_eps(K):
+    x = torch.zeros(2, K, device=DEV)
+    x[1, K // 2] = 3.0
+    g = torch.ones(K, device=DEV)
+    g[K // 2] = 0.0                        # the second row's only number meets a gain of 0
+    for gain in (None, g):
+        codes, scales, _ = q4.q8_rmsnorm_rows(x, gain, None, 0.0)
+        ref, sref, _ = S.rmsnorm_rows(f64(x), None, f64(gain), 0.0)
+        assert_bitwise(host(codes), ref, "codes")
+        assert np.all(np.abs(host(scales) - sref) <= 1e-6 * sref)
+
+
 @pytest.mark.parametrize("xt", ["f32", "bf16"])
 @pytest.mark.parametrize("K", [2 ** 14, 2 ** 17, 2 ** 20, 2 ** 24])
 def test_long_rows(K, xt):
