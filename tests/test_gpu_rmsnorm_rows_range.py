@@ -66,3 +66,27 @@ def test_long_rows(K, xt):
     x = torch.full((1, K), 1.3, device=DEV).to(TORCH[xt])
     x[0, 5] = 2.6
     check(x, None, None, 1e-6, "constant")
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K", [(2, 16392), (2, 20001), (300, 16400)])
+def test_sum_in_place_of_rows_that_are_read_again(M, K, xt):
+    gen = torch.Generator(DEV).manual_seed(2)
+    x, r = (torch.randn(M, K, device=DEV, generator=gen).to(TORCH[xt]) for _ in range(2))
+    want = [host(t) for t in q4.q8_rmsnorm_rows(x, None, r, 1e-6)]
+    for place in ("residual", "x"):
+        a, b = x.clone(), r.clone()
+        got = q4.q8_rmsnorm_rows(a, None, b, 1e-6, total=b if place == "residual" else a)
+        assert got[2].data_ptr() == (b if place == "residual" else a).data_ptr()
+        for g, w in zip(got, want):
+            assert_bitwise(host(g), w, place)
+
+
+@pytest.mark.parametrize("K", WIDTHS)
+def test_codes_next_to_borders_at_every_width(K):
+    """Quotients that are ties and their neighbours, over and over; the largest is 127."""
+    half = (np.arange(-126, 126) + 0.5).astype(np.float32)
+    up, down = (np.nextafter(half, np.float32(s)) for s in (1e9, -1e9))
+    x = np.resize(np.concatenate([[np.float32(127)], half, up, down]), (1, K))
+    for s in (1.0, 2.0 ** -110, 2.0 ** 40, 3.0):
+        check(dev((x * np.float32(s)).astype(np.float32)), None, None, 1e-6, f"times {s}")
