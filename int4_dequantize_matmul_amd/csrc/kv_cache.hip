@@ -9,7 +9,7 @@
 // such roundings add up to stays below one step of the last scale.  Key rows are
 // computed in f64, so that a code and the scale depend on no sum's order;
 // scaling by a power of two is exact.  Query rows, rounded to 24 or 8 bits, go
-// in f32.
+// in f32 (the norm of one whose squares f32 does not hold in f64).
 //
 // Bound: memory for queries, the codes' arithmetic beside it for keys and values;
 // 12000 tokens of 32 + 8 heads of 128, norm and rotation of halves: bf16 61 us (26 of
@@ -144,11 +144,34 @@ struct Lane {
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = __builtin_elementwise_fma(y[u][j], y[u][j], ss);
       for (int d = 1; d < L; d <<= 1) ss += __shfl_xor(ss, d);
-      const real rms = inverse_root(ss / D + static_cast<real>(a.eps));
+      const real mean = ss / D + static_cast<real>(a.eps);
+      bool plain = true;
+      if constexpr (std::is_same_v<real, float>) {
+        // squares past the range of f32, or so small that what it lost of them (256 times 2^-149) may count: in f64
+        plain = mean > 0x1p-90f && mean < __builtin_inff();
+        if (__builtin_expect(__any(!plain), 0)) {
+          double sum = 0;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[u][j] = y[u][j] * rms * static_cast<real>(g[u][j]);
+            for (int j = 0; j < 8; ++j) sum = __builtin_fma(static_cast<double>(y[u][j]), static_cast<double>(y[u][j]), sum);
+          for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d);
+          const double root = inverse_root(sum / D + static_cast<double>(a.eps));
+          if (!plain) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[u][j] = static_cast<float>(y[u][j] * root * g[u][j]);
+          }
+        }
+      }
+      if (plain) {
+        const real root = inverse_root(mean);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[u][j] = y[u][j] * root * static_cast<real>(g[u][j]);
+      }
     }
     if constexpr (MODE == kNeighbours) {
 #pragma unroll
