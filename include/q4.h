@@ -421,7 +421,8 @@ q4_status q8_rmsnorm_rows(const void *x, const void *residual, q4_dtype xt, cons
  * Tokens on a page that is not in the table or not in the pool read as NaN and
  * are dropped when written.  ESHAPE: the sizes above, heads, n_pages or table
  * < 1, table page beyond 2^31 - 2^11, T or sequences beyond 2^31 - 1, or more work than 2^32 - 1 workgroups
- * (writing and reading: two for each of T / 16 + 2 sequences and head). */
+ * (writing and reading: two for each of T / 16 + 2 sequences and head, and one
+ * for 16 rows, begun or whole, of a query head). */
 typedef struct {
   int8_t *k, *v;
   uint8_t *k_scale, *v_scale;

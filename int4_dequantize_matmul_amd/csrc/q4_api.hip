@@ -877,9 +877,10 @@ q4_status cache_bad(const q8_kv_cache *c, const int32_t *starts, const int32_t *
   return Q4_OK;
 }
 
-// Workgroups of the append and read kernels: two a block slot and head, one for 16 query rows.
+// Workgroups of the append and read kernels at most: two a block slot and head, one for 16 rows, begun or whole,
+// of a query head.
 bool too_many_groups(const q8_kv_cache &c, int64_t T, int64_t Hq) {
-  return (u(T) / 16 + 2 * u(c.sequences)) * u(c.heads) * 2 + u(T) * u(Hq) / 16 + 1 > UINT32_MAX;
+  return (u(T) / 16 + 2 * u(c.sequences)) * u(c.heads) * 2 + (u(T) + 15) / 16 * u(Hq) > UINT32_MAX;
 }
 
 uint64_t pool_blocks(const q8_kv_cache &c) { return u(c.n_pages) * u(c.heads) * u(c.page / 16); }
