@@ -313,7 +313,7 @@ AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D,
   if (p.tiled) return p;
   const int64_t G = Hq / Hk, groups = (T * G + kRows * N - 1) / (kRows * N) * N * Hk;
   int64_t keys = max_len;
-  if (window > 0 && window + sinks + 32 < keys) keys = window + sinks + 32;
+  if (window > 0 && window < keys && sinks < keys && window + sinks + 32 < keys) keys = window + sinks + 32;
   // Two workgroups a CU in all, what runs at once, or up to eight of 4096 keys or more, which even out lengths; a wave
   // at least 64 keys of what a sequence may have, and no splits below 1024 keys, where the join costs more than it gives.
   // 32 + 8 heads of 128, one token a sequence, two workgroups a CU and eight: 32 sequences of 1023 keys 19.5 and 26.4
