@@ -156,7 +156,8 @@ struct Lane {
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum = __builtin_fma(static_cast<double>(y[u][j]), static_cast<double>(y[u][j]), sum);
           for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d);
-          const double root = inverse_root(sum / D + static_cast<double>(a.eps));
+          const double mean64 = sum / D + static_cast<double>(a.eps);
+          const double root = mean64 < __builtin_inf() ? inverse_root(mean64) : 1.0 / mean64;
           if (!plain) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)

@@ -41,3 +41,23 @@ def test_queries_of_all_sizes(D, how, xt, yt):
                 mag = np.abs(plain) + (0 if cs is None else np.abs(plain).max())
                 tol = (D / 2 + 16) * 2.0 ** -24 * mag + 1e-44 + (2.0 ** -8 * np.abs(ref) if yt == "bf16" else 0)
                 assert np.all(np.abs(out[t, h] - ref) <= tol), (eps, t, h, size[t], out[t, h][:3], ref[:3])
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_queries_that_are_not_finite(eps, xt):
+    """As the formula has it: x / sqrt(mean) with an infinite mean is 0 where x is finite and NaN where it is not."""
+    T, Hq, D = 5, 2, 64
+    gen = torch.Generator(DEV).manual_seed(1)
+    q = torch.randn(T, Hq, D, device=DEV, generator=gen)
+    q[1, 0, 7], q[2, 1, 3], q[3, 0, 0], q[3, 0, 9] = float("inf"), float("nan"), float("-inf"), float("inf")
+    q = q.to(TORCH[xt])
+    k = torch.randn(T, 1, D, device=DEV, generator=gen).to(TORCH[xt])
+    pages, P = new_pages(np.random.default_rng(1), [T], 16)
+    out = f64(q4.q8_kv_append(q4.q8_kv_cache(P, 1, 16, D), dev(pages), i32([0, T]), i32([T]), k, k, q, eps=eps, dtype="f32"))
+    for t in range(T):
+        for h in range(Hq):
+            with np.errstate(invalid="ignore"):
+                ref = S.head(f64(q[t, h]), None, float(np.float32(eps)), None, True)
+            tol = (D / 2 + 16) * 2.0 ** -24 * np.abs(ref)
+            assert np.all((np.abs(out[t, h] - ref) <= tol) | (np.isnan(out[t, h]) & np.isnan(ref))), (t, h)
