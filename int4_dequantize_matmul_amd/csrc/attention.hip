@@ -6,10 +6,15 @@
 // Products go through the f16 matrix instructions: int8 codes are halves
 // exactly; a query row is scaled by a power of two to a maximum between 2^14
 // and 2^15 and rounded to halves (11 bits, exact for bf16 down to 2^-25 of the
-// row's maximum), and so are the weights exp(s), times the power of two that is
-// their values' scale (11 bits down to 2^-23 of the largest such product, half a
-// step of 2^-33 of it below).  For f32 queries or results both come as two
-// halves, 22 bits, at twice the products.  Maximum, sum and results are f32; what
+// row's maximum; f32 rows are two halves, 22 bits, at twice the products), and so
+// are the weights exp(s), times the power of two that is their values' scale: two
+// halves (22 bits down to 2^-24 of the largest such product, half a step of 2^-34
+// of it below), which cost few rows next to nothing beside the cache's bytes (64
+// tokens of up to 8192 keys 104 us, with one half 103, whose bf16 results differ in
+// every 15th number).  The tiles' bf16 weights are one half, 11 bits (2^-33): a
+// prompt's time is its products, which would be half as many again, and there are
+// no registers for the second halves of 128 columns; against 64 bits that adds 0.8 %
+// to the error that bf16 results have.  Maximum, sum and results are f32; what
 // is subtracted from the scores are whole powers of two that may lag behind the
 // maximum, so that results are seldom rescaled, and exactly.
 //
@@ -42,7 +47,7 @@ __host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { 
 // with the call.  Eight waves a workgroup take one more and, as a CU then has one
 // workgroup, twice the time with many sequences (64 of 64 keys 16.6 us against 8.6).  parts: a, d, l
 // and results of splits x rows for combine_kernel, or null with one split.
-template <int NV, bool TWO>   // 16 NV columns
+template <int NV, bool TWO>   // 16 NV columns; TWO: queries in f32
 __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Types types, int splits,
                                                                                  float *parts, uint32_t first) {
   constexpr int NS = (NV + 3) / 4, D = 16 * NV;
@@ -88,7 +93,7 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
     return f;
   };
 
-  State<f32x4, NV, 4, TWO> st;
+  State<f32x4, NV, 4, true> st;
   if (w0 < w1) {
     Info cur = info_of(0, page_of(0)), next = {};
     int page = -1;
@@ -158,10 +163,8 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
         const uint4 lo = codes_to_f16(v[d].x, v[d].y), hi = codes_to_f16(v[d].z, v[d].w);
         st.y[d] = mfma_f16_16x16x32(lo, w[0].p[0], st.y[d]);
         st.y[d] = mfma_f16_16x16x32(hi, w[0].p[1], st.y[d]);
-        if constexpr (TWO) {
-          st.y[d] = mfma_f16_16x16x32(lo, w[0].rest[0], st.y[d]);
-          st.y[d] = mfma_f16_16x16x32(hi, w[0].rest[1], st.y[d]);
-        }
+        st.y[d] = mfma_f16_16x16x32(lo, w[0].rest[0], st.y[d]);
+        st.y[d] = mfma_f16_16x16x32(hi, w[0].rest[1], st.y[d]);
       }
       __builtin_amdgcn_sched_barrier(0);
       if (s + 1 < w1) load_values((l + 1) & 15);
@@ -280,7 +283,7 @@ void go_rows(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hi
   for (int64_t first = 0; first < all; first += per) {   // rows of a launch
     const int64_t n = all - first < per ? all - first : per;
     combine_kernel<<<static_cast<unsigned>((n + rows - 1) / rows), kThreads, 0, st>>>(
-        a, t, State<f32x4, 1, 4, TWO>::kOffset, p.splits, groups, rows, ws, first);
+        a, t, State<f32x4, 1, 4, true>::kOffset, p.splits, groups, rows, ws, first);
   }
 }
 
@@ -332,7 +335,7 @@ AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D,
 hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, bool bf16, bool out_bf16, void *ws, hipStream_t st) {
   const Types t = {bf16, out_bf16};
   if (p.tiled) return launch_attention_tiled(a, t, st);
-  if (bf16 && out_bf16) go<false>(a, t, p, static_cast<float *>(ws), st);
+  if (bf16) go<false>(a, t, p, static_cast<float *>(ws), st);
   else go<true>(a, t, p, static_cast<float *>(ws), st);
   return hipGetLastError();
 }

@@ -40,6 +40,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 // What rounding v to a half leaves, as a half.
 __device__ __forceinline__ float rest_f16(float v) { return v - static_cast<float>(static_cast<_Float16>(v)); }
+// The same of two numbers and their halves: one operation each that takes the half as it lies, subtracts and rounds
+// (with a factor that the compiler does not know, or it would convert, subtract and round in three).
+__device__ __forceinline__ uint32_t rest_f16(uint32_t halves, float lo, float hi) {
+  float minus = -1.0f;
+  asm("" : "+v"(halves), "+s"(minus));
+  const f16x2 h = __builtin_bit_cast(f16x2, halves);
+  return pack_f16(__builtin_fmaf(static_cast<float>(h[0]), minus, lo), __builtin_fmaf(static_cast<float>(h[1]), minus, hi));
+}
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
@@ -235,8 +243,11 @@ struct State {
         uint32_t q[4], r[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          q[j] = pack_f16(w[8 * u + 2 * j], w[8 * u + 2 * j + 1]);
-          r[j] = pack_f16(rest_f16(w[8 * u + 2 * j]), rest_f16(w[8 * u + 2 * j + 1]));
+          const float lo = w[8 * u + 2 * j], hi = w[8 * u + 2 * j + 1];
+          q[j] = pack_f16(lo, hi);
+          if constexpr (TWO) {
+            r[j] = rest_f16(q[j], lo, hi);
+          }
         }
         p[u] = make_uint4(q[0], q[1], q[2], q[3]);
         if constexpr (TWO) rest[u] = make_uint4(r[0], r[1], r[2], r[3]);
