@@ -808,7 +808,9 @@ def q8_kv_append(cache, pages, starts, lengths, k, v, q=None, cos_sin=None, k_ga
     rotated if cos_sin f32 [P, R] is, by their positions; the queries q [T, Hq, D]
     with q_gain likewise -> the queries [T, Hq, D] in dtype (default: q's), or
     None.  pages int32 [N, table], starts int32 [N + 1], lengths int32 [N] (new
-    tokens included): see q8_kv_cache in include/q4.h."""
+    tokens included): see q8_kv_cache in include/q4.h.  Rows of no sequence (in
+    front of starts[0], behind starts[N]: padding) are not written: as they were
+    in q_out if that is given, else anything."""
     out = _direct().kv_append(cache, pages, starts, lengths, k, v, q, cos_sin, k_gain, q_gain, eps, ROPE_PAIRS[pairs],
                               -1 if dtype is None else DT[dtype], q_out)
     if out is not None:
@@ -867,7 +869,8 @@ def q8_kv_append(cache, pages, starts, lengths, k, v, q=None, cos_sin=None, k_ga
 
 
 def q8_kv_read(cache, pages, starts, lengths, T: int, dtype: str = "bf16"):
-    """What the cache holds of the sequences' last tokens, T rows in all -> (k, v) [T, heads, D] in dtype."""
+    """What the cache holds of the sequences' last tokens, T rows in all -> (k, v) [T, heads, D] in dtype.
+    Rows of no sequence and those of positions below 0 are not written and hold anything."""
     out = _direct().kv_read(cache, pages, starts, lengths, T, DT[dtype])
     if out is not None:
         return out
@@ -890,7 +893,8 @@ def q8_attention(q, cache, pages, starts, lengths, scale: float | None = None, w
     over the cache, which holds them already -> y [T, Hq, D] in dtype (default:
     q's).  scale: D ** -0.5 if not given.  window > 0: a row sees the last
     `window` tokens up to its own and the sequence's first `sinks`.  max_len: a
-    bound of lengths, if one is known below the table's."""
+    bound of lengths, if one is known below the table's.  Rows of no sequence
+    (padding) are not written: as they were in y if that is given, else anything."""
     out = _direct().attention(q, cache, pages, starts, lengths, scale, window, sinks, max_len,
                               -1 if dtype is None else DT[dtype], ws, y)
     if out is not None:
