@@ -9,12 +9,13 @@
 // row's maximum; f32 rows are two halves, 22 bits, at twice the products), and so
 // are the weights exp(s), times the power of two that is their values' scale: two
 // halves (22 bits down to 2^-24 of the largest such product, half a step of 2^-34
-// of it below), which cost few rows next to nothing beside the cache's bytes (64
-// tokens of up to 8192 keys 104 us, with one half 103, whose bf16 results differ in
-// every 15th number).  The tiles' bf16 weights are one half, 11 bits (2^-33): a
-// prompt's time is its products, which would be half as many again, and there are
-// no registers for the second halves of 128 columns; against 64 bits that adds 0.8 %
-// to the error that bf16 results have.  Maximum, sum and results are f32; what
+// of it below) for f32 queries or results, and for bf16 where a sequence has up to
+// 16 rows of a key head, whose time is the cache's bytes (64 tokens of up to 8192
+// keys 104 us, with one half 103, whose bf16 results differ in every 15th number).
+// More bf16 rows have one half, 11 bits (2^-33): their time is the products' (512
+// rows of 4096 keys 84 us, with two halves 95, and no registers for two in tiles of
+// 128 columns), and against 64 bits it adds 0.8 % to the error that bf16 results
+// have.  Maximum, sum and results are f32; what
 // is subtracted from the scores are whole powers of two that may lag behind the
 // maximum, so that results are seldom rescaled, and exactly.
 //
@@ -47,7 +48,7 @@ __host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { 
 // with the call.  Eight waves a workgroup take one more and, as a CU then has one
 // workgroup, twice the time with many sequences (64 of 64 keys 16.6 us against 8.6).  parts: a, d, l
 // and results of splits x rows for combine_kernel, or null with one split.
-template <int NV, bool TWO>   // 16 NV columns; TWO: queries in f32
+template <int NV, bool TWO_Q, bool TWO_W>   // 16 NV columns; queries and weights as two halves
 __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Types types, int splits,
                                                                                  float *parts, uint32_t first) {
   constexpr int NS = (NV + 3) / 4, D = 16 * NV;
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
     return f;
   };
 
-  State<f32x4, NV, 4, true> st;
+  State<f32x4, NV, 4, TWO_W> st;
   if (w0 < w1) {
     Info cur = info_of(0, page_of(0)), next = {};
     int page = -1;
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
     };
     load_keys(0);
     load_values(0);
-    Query<NS, 4, TWO> q;
+    Query<NS, 4, TWO_Q> q;
     q.load(a, types, row * a.q_t + qh * a.q_h, true, q4);
     for (int s = w0; s < w1; ++s) {
       const int l = (s - w0) & 15;
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
           const uint4 lo = codes_to_f16(k[b][j].x, k[b][j].y), hi = codes_to_f16(k[b][j].z, k[b][j].w);
           acc = mfma_f16_16x16x32(lo, q.hi[2 * j], acc);
           acc = mfma_f16_16x16x32(hi, q.hi[2 * j + 1], acc);
-          if constexpr (TWO) {
+          if constexpr (TWO_Q) {
             acc = mfma_f16_16x16x32(lo, q.lo[2 * j], acc);
             acc = mfma_f16_16x16x32(hi, q.lo[2 * j + 1], acc);
           }
@@ -163,8 +164,10 @@ __global__ __launch_bounds__(kThreads, NV <= 8 ? 2 : 1) void attention_rows_kern
         const uint4 lo = codes_to_f16(v[d].x, v[d].y), hi = codes_to_f16(v[d].z, v[d].w);
         st.y[d] = mfma_f16_16x16x32(lo, w[0].p[0], st.y[d]);
         st.y[d] = mfma_f16_16x16x32(hi, w[0].p[1], st.y[d]);
-        st.y[d] = mfma_f16_16x16x32(lo, w[0].rest[0], st.y[d]);
-        st.y[d] = mfma_f16_16x16x32(hi, w[0].rest[1], st.y[d]);
+        if constexpr (TWO_W) {
+          st.y[d] = mfma_f16_16x16x32(lo, w[0].rest[0], st.y[d]);
+          st.y[d] = mfma_f16_16x16x32(hi, w[0].rest[1], st.y[d]);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
       if (s + 1 < w1) load_values((l + 1) & 15);
@@ -267,13 +270,13 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(AttnArgs a, Types typ
   store4(a.y, types.out_bf16, out * D + col, q(sum[0]), q(sum[1]), q(sum[2]), q(sum[3]));
 }
 
-template <int NV, bool TWO>
+template <int NV, bool TWO_Q, bool TWO_W>
 void go_rows(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hipStream_t st) {
   const int64_t slots = tile_slots(a.seqs.T, a.seqs.N, a.G, kRows), each = a.pool.Hk * p.splits;
   const int64_t most = max_groups(kThreads);
   for (int64_t first = 0; first < slots; first += most / each) {   // slots of a launch
     const int64_t n = slots - first < most / each ? slots - first : most / each;
-    attention_rows_kernel<NV, TWO><<<static_cast<unsigned>(n * each), kThreads, 0, st>>>(
+    attention_rows_kernel<NV, TWO_Q, TWO_W><<<static_cast<unsigned>(n * each), kThreads, 0, st>>>(
         a, t, p.splits, p.splits > 1 ? ws : nullptr, static_cast<uint32_t>(first));
   }
   if (p.splits == 1) return;
@@ -283,14 +286,14 @@ void go_rows(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hi
   for (int64_t first = 0; first < all; first += per) {   // rows of a launch
     const int64_t n = all - first < per ? all - first : per;
     combine_kernel<<<static_cast<unsigned>((n + rows - 1) / rows), kThreads, 0, st>>>(
-        a, t, State<f32x4, 1, 4, true>::kOffset, p.splits, groups, rows, ws, first);
+        a, t, State<f32x4, 1, 4, TWO_W>::kOffset, p.splits, groups, rows, ws, first);
   }
 }
 
-template <bool TWO, int NV = 16>
+template <bool TWO_Q, bool TWO_W, int NV = 16>
 void go(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hipStream_t st) {
-  if (a.pool.D == 16 * NV) return go_rows<NV, TWO>(a, t, p, ws, st);
-  if constexpr (NV > 1) go<TWO, NV - 1>(a, t, p, ws, st);
+  if (a.pool.D == 16 * NV) return go_rows<NV, TWO_Q, TWO_W>(a, t, p, ws, st);
+  if constexpr (NV > 1) go<TWO_Q, TWO_W, NV - 1>(a, t, p, ws, st);
 }
 
 }  // namespace
@@ -335,8 +338,12 @@ AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D,
 hipError_t launch_attention(const AttnArgs &a, const AttnPlan &p, bool bf16, bool out_bf16, void *ws, hipStream_t st) {
   const Types t = {bf16, out_bf16};
   if (p.tiled) return launch_attention_tiled(a, t, st);
-  if (bf16) go<false>(a, t, p, static_cast<float *>(ws), st);
-  else go<true>(a, t, p, static_cast<float *>(ws), st);
+  // up to 16 rows of a sequence and key head: bound by the cache's bytes
+  const bool fine = !bf16 || !out_bf16 || a.seqs.T * a.G <= kRows * a.seqs.N;
+  float *parts = static_cast<float *>(ws);
+  if (!bf16) go<true, true>(a, t, p, parts, st);
+  else if (fine) go<false, true>(a, t, p, parts, st);
+  else go<false, false>(a, t, p, parts, st);
   return hipGetLastError();
 }
 
