@@ -42,9 +42,9 @@ __host__ __device__ constexpr int64_t results_at(int64_t splits, int64_t all) { 
 // their keys; its four waves share those out again, 64 keys a step straight from
 // the cache to registers, and meet in LDS.  A step's keys are loaded as soon as
 // those of the step before are multiplied, its values likewise.  Bound by memory
-// for long contexts: one token, 131071 keys of 32 + 8 heads of 128 (268 MB) 53 us,
-// 5.1 TB/s; 64 tokens of up to 8192 keys (462 MB) 97 us, 4.8 TB/s.  By the chain of
-// loads (sequence, page, scales, codes) and the launch for short ones: 16 keys 7 us
+// for long contexts: one token, 131071 keys of 32 + 8 heads of 128 (268 MB) 54 us,
+// 5.0 TB/s; 64 tokens of up to 8192 keys (462 MB) 100 us, 4.6 TB/s.  By the chain of
+// loads (sequence, page, scales, codes) and the launch for short ones: 16 keys 7.5 us
 // with the call.  Eight waves a workgroup take one more and, as a CU then has one
 // workgroup, twice the time with many sequences (64 of 64 keys 16.6 us against 8.6).  parts: a, d, l
 // and results of splits x rows for combine_kernel, or null with one split.
@@ -300,11 +300,14 @@ void go(const AttnArgs &a, const Types &t, const AttnPlan &p, float *ws, hipStre
 
 // Rows kernel | tiles, us, of N sequences of L tokens, n of them rows, Hq / Hk heads
 // of D.  bf16 with D above 64: from 128 tiles of 256 rows on (32/8 of 128: N 1 n 512 L
-// 4096, 64 tiles, 119 | 127, n 1024 157 | 133, n 4096 342 | 164; 16/4 of 96, N 1 n 2048 L
-// 4096, 128 tiles, 116 | 113), where a sequence half fills one (16/16 of 128, N 64 n 64 L
-// 1024 125 | 125, N 16 n 128 L 2048 89 | 58).  D up to 64 from 192 on (8/1 of 64, N 1 n 4096
-// L 4096, 128 tiles, 60 | 85; 32/8, N 1 n 2048 L 4096, 256 tiles, 145 | 93).  f32: from 256,
-// where a sequence has two (32/8 of 64, N 16 n 128 L 2048 113 | 141, n 256 223 | 157).
+// 4096, 64 tiles, 88 | 126, n 1024 157 | 133, n 4096 345 | 162; 16/4 of 96, N 1 n 2048 L
+// 4096, 128 tiles, 117 | 111), where a sequence half fills one (16/16 of 128, N 64 n 64 L
+// 1024 128 | 128, N 16 n 128 L 2048 90 | 59).  D up to 64 from 192 on (8/1 of 64, N 1 n 4096
+// L 4096, 128 tiles, 59 | 85; 32/8, N 1 n 2048 L 4096, 256 tiles, 135 | 91).  f32: from 256,
+// where a sequence has two (32/8 of 64, N 16 n 128 L 2048 112 | 137, n 256 219 | 151).
+// All sequences have one route: where lengths and rows differ much that costs (one token of
+// 131071 keys 51, 512 rows of 4096 83, both in one call 453; 63 tokens of 4096 keys 105, a
+// prompt of 4096 162, both 350).
 static bool many_rows(int64_t T, int64_t N, int64_t G, int64_t Hk, int64_t D, bool two) {
   const int64_t rows = T * G / N, tiles = (rows + 255) / 256 * N * Hk;
   return two ? tiles >= 256 && rows >= 512 : tiles >= (D > 64 ? 128 : 192) && rows >= 128;
@@ -322,7 +325,7 @@ AttnPlan attention_plan(int64_t T, int64_t N, int64_t Hq, int64_t Hk, int64_t D,
   if (window > 0 && window < keys && sinks < keys && window + sinks + 32 < keys) keys = window + sinks + 32;
   // Two workgroups a CU in all, what runs at once, or up to eight of 4096 keys or more, which even out lengths; a wave
   // at least 64 keys of what a sequence may have, and no splits below 1024 keys, where the join costs more than it gives.
-  // 32 + 8 heads of 128, one token a sequence, two workgroups a CU and eight: 32 sequences of 1023 keys 19.5 and 26.4
+  // 32 + 8 heads of 128, one token a sequence (weights of one half), two workgroups a CU and eight: 32 sequences of 1023 keys 19.5 and 26.4
   // us, of 4096 46.5 and 54.9, of 16384 189 and 192, of 1 to 16384 124 and 111 (four: 114).  One sequence of 512 keys
   // 8.4 us, in two splits 10.3; of 1023 11.0, in two 11.7, in four 10.9.
   int64_t s = (512 + groups - 1) / groups;
