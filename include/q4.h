@@ -486,11 +486,12 @@ size_t q8_attention_workspace(int64_t T, int64_t sequences, int64_t Hq, int64_t 
  *     if that is 0); calls that may run at a time need one each.
  * Scores, softmax and sums are f32 (a score past its range gives NaN, or weight
  * 0 below it).  f32 queries have 22 bits, as have the weights before the product
- * with the values; with bf16 queries and results the weights have 11 bits where T
- * Hq / heads is more than 16 times `sequences`.  (Weights times their values' scale that are below 2^-23 of the row's
- * largest such product have fewer.)  A row that sees no key is 0; one that sees a NaN,
- * in itself, a key or a value, is NaN.  What a row does not see does not touch
- * it.  A row's result depends on the split of the keys, so on T, sequences and
+ * with the values; with bf16 queries and results the weights have 11 bits on the
+ * tiles, and where T Hq / heads is more than 16 times `sequences`.  (Weights
+ * times their values' scale that are below 2^-23 of the row's largest such
+ * product have fewer.)  A row that sees no key is 0; one that sees a NaN, in
+ * itself, a key or a value, is NaN.  What a row does not see does not touch it.
+ * A row's result depends on the split of the keys, so on T, sequences and
  * max_len, to its rounding.
  * Few rows take the decode kernel (Q4_PATH_GEMV), many rows of D up to 128 (f32
  * queries or results: 64) LDS tiles of 256 rows (Q4_PATH_TILED), by a measured
